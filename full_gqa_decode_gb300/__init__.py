@@ -31,7 +31,8 @@ HD_STATIC_SCRATCH_BYTES = 64 << 20   # the allocation-free entry point's scratch
 STATUS = {0: "HD_OK", 1: "HD_ERR_INVALID_ARG", 2: "HD_ERR_UNSUPPORTED", 3: "HD_ERR_CAPACITY",
           4: "HD_ERR_CUDA", 5: "HD_ERR_STATE"}
 DEVERR = {1: "HD_DEVERR_CONTEXT_NEGATIVE", 2: "HD_DEVERR_CONTEXT_CAPACITY",
-          4: "HD_DEVERR_CONTEXT_PLAN", 8: "HD_DEVERR_WAIT_TIMEOUT"}
+          4: "HD_DEVERR_CONTEXT_PLAN", 8: "HD_DEVERR_WAIT_TIMEOUT", 16: "HD_DEVERR_TOKEN_OFFSETS",
+          32: "HD_DEVERR_PAGE"}
 
 if not os.path.exists(LIBRARY):
     raise ImportError(f"{LIBRARY} is missing: build it with full_gqa_decode_gb300.build.build() "
@@ -66,6 +67,18 @@ class hd_layer_io(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
 
 
+class hd_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+
+
+class hd_paged_batch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("context", ctypes.c_void_p), ("token_offsets", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("num_tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("max_context", ctypes.c_int32)]
+
+
 _c = ctypes
 _P = _c.c_void_p
 _i32, _i64 = _c.c_int32, _c.c_int64
@@ -94,6 +107,13 @@ _SIGS = {
     "hybrid_decode_set_layer_overlap": [_P, _i32],
     "hybrid_decode_set_step_fusion": [_P, _i32],
     "hybrid_decode_set_cluster_combine": [_P, _i32],
+    "hd_validate_paged": [_c.POINTER(hd_config), _c.POINTER(hd_paged_batch), _c.POINTER(hd_paged_cache)],
+    "rope_append_paged": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _i64, _P, _i64, _P, _i64, _P,
+                          _c.POINTER(hd_paged_cache), _P],
+    "attn_paged": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _c.POINTER(hd_paged_cache), _P, _P, _P, _P, _P],
+    "select_pages": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _c.POINTER(hd_paged_cache), _i32, _i32, _i32, _P, _P],
+    "attn_selected_pages": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _c.POINTER(hd_paged_cache), _P, _i32, _P, _P, _P,
+                            _P, _P],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -416,6 +436,164 @@ def decode_attn_full_static_scratch_plan(batch: int, num_q_heads: int, num_kv_he
     st = _lib.decode_attn_full_static_scratch_plan(batch, num_q_heads, num_kv_heads, max_context, num_sms,
                                                    ctypes.byref(nbytes), ctypes.byref(chunk), ctypes.byref(chunks))
     return nbytes.value, chunk.value, chunks.value, st
+
+
+def hd_validate_paged(cfg: Config, batch: hd_paged_batch, cache: hd_paged_cache) -> int:
+    """Status of the pure host check that every paged call makes on its descriptors."""
+    return _lib.hd_validate_paged(ctypes.byref(cfg.to_c()), ctypes.byref(batch), ctypes.byref(cache))
+
+
+class PagedCache:
+    """A pool of K/V pages (see ``paged_cache``): the C descriptor and the tensors it points into."""
+
+    def __init__(self, c, keep, shape, device):
+        self.c, self.ref, self.keep = c, ctypes.byref(c), keep
+        self.num_kv_heads, self.device = shape[1], device
+
+
+class PagedBatch:
+    """The sequences of a paged call (see ``paged_batch``): the C descriptor and its tensors."""
+
+    def __init__(self, c, keep, device):
+        self.c, self.ref, self.keep = c, ctypes.byref(c), keep
+        self.num_tokens, self.device = c.num_tokens, device
+
+
+def paged_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                v_scale: torch.Tensor | None = None, bounds: torch.Tensor | None = None) -> PagedCache:
+    """Describe a pool of pages shaped [num_pages, num_kv_heads, page_size, head_dim] on CUDA:
+    bf16, or E4M3 codes (uint8 or float8_e4m3fn) with fp32 ``k_scale``/``v_scale`` of shape
+    [num_kv_heads].  Pages may lie apart (stride 0) but each is contiguous.  ``bounds``: bf16
+    [num_pages, num_kv_heads, 2, head_dim] for select_pages.  Keep it while the tensors stay."""
+    if k.shape != v.shape or k.dim() != 4 or k.stride() != v.stride():
+        raise ValueError("k and v pages must share a [num_pages, kv_heads, page_size, head_dim] layout")
+    if not k.is_cuda or v.device != k.device:
+        raise ValueError("pages must be CUDA tensors on one device")
+    P, H, S, D = k.shape
+    fp8 = k.dtype in _FP8_CACHE_TYPES
+    if v.dtype != k.dtype or not (fp8 or k.dtype == torch.bfloat16):
+        raise ValueError("pages must be bf16, or E4M3 codes with scales, K and V alike")
+    if D != 256 or k.stride()[1:] != (S * D, D, 1) or (P > 1 and k.stride(0) < H * S * D):
+        raise ValueError("each page must be contiguous [kv_heads, page_size, 256] and pages may not overlap")
+    for name, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not fp8:
+            if sc is not None:
+                raise ValueError("scales belong to FP8 caches only")
+        elif (sc is None or sc.dtype != torch.float32 or tuple(sc.shape) != (H,) or sc.device != k.device or
+              not sc.is_contiguous()):
+            raise ValueError(f"E4M3 pages need {name} as contiguous float32 of shape ({H},) on the pages' device")
+    if bounds is not None and (bounds.dtype != torch.bfloat16 or tuple(bounds.shape) != (P, H, 2, D) or
+                               bounds.device != k.device or not bounds.is_contiguous()):
+        raise ValueError(f"bounds must be contiguous bf16 of shape ({P}, {H}, 2, {D}) on the pages' device")
+    c = hd_paged_cache(k.data_ptr(), v.data_ptr(), k.stride(0) if P > 1 else H * S * D, P, S, _ptr(k_scale),
+                       _ptr(v_scale), _ptr(bounds))
+    r = PagedCache(c, (k, v, k_scale, v_scale, bounds), k.shape, k.device)
+    r.fp8 = fp8
+    return r
+
+
+def paged_batch(block_table: torch.Tensor, context: torch.Tensor, token_offsets: torch.Tensor | None = None,
+                num_tokens: int | None = None, max_tokens: int = 1, max_context: int = 0) -> PagedBatch:
+    """Describe the sequences of a paged call: int32 CUDA tensors ``block_table`` [batch, max_blocks],
+    ``context`` [batch] (previous tokens) and ``token_offsets`` [batch + 1] (None: one new token per
+    sequence).  ``num_tokens``: rows of q / k / v / out (default: the batch); ``max_tokens`` and
+    ``max_context``: bounds on a sequence's new tokens and context (0: what the context serves)."""
+    batch = context.shape[0]
+    if context.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch, max_blocks] and context [batch]")
+    for name, t in (("block_table", block_table), ("context", context), ("token_offsets", token_offsets)):
+        if t is not None and (t.dtype != torch.int32 or t.device != context.device or not t.is_cuda or
+                              (t.numel() > 0 and t.stride(-1) != 1)):
+            raise ValueError(f"{name} must be an int32 CUDA tensor with unit stride, on one device with the others")
+    if token_offsets is not None and (token_offsets.dim() != 1 or token_offsets.shape[0] != batch + 1):
+        raise ValueError(f"token_offsets must have shape ({batch + 1},)")
+    if batch > 1 and block_table.stride(0) < block_table.shape[1]:
+        raise ValueError("rows of the block table may not overlap")
+    c = hd_paged_batch(block_table.data_ptr(), context.data_ptr(), _ptr(token_offsets),
+                       block_table.stride(0) if batch > 1 else block_table.shape[1], block_table.shape[1], batch,
+                       batch if num_tokens is None else num_tokens, max_tokens, max_context)
+    return PagedBatch(c, (block_table, context, token_offsets), context.device)
+
+
+def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype, device, strided: bool = False) -> None:
+    """A tensor of a paged call: its shape, type and device; contiguous, or (strided) contiguous rows."""
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not (t.is_contiguous() or (strided and t.stride(2) == 1 and t.stride(1) == shape[2])):
+        raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
+
+
+def _check_paged(ctx: Context, batch: PagedBatch, cache: PagedCache) -> None:
+    if cache.num_kv_heads != ctx.cfg.num_kv_heads or cache.fp8 != (ctx.cfg.kv_dtype == HD_KV_FP8_E4M3):
+        raise ValueError("the pages' kv heads and element type must be the context's")
+    if batch.device != cache.device:
+        raise ValueError("the batch and the pages must be on one device")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
+                      stream=None) -> None:
+    """Rotate the new q [num_tokens, Hq, 256] into q_rot (bf16; may be q) and the new k, and store
+    k / v [num_tokens, Hkv, 256] in their pages, with the pages' bounds when the cache has them.
+    q, k and v may be parts of wider rows; q and q_rot may both be None."""
+    _check_paged(ctx, batch, cache)
+    n, D, dev = batch.num_tokens, 256, cache.device
+    kv = (n, ctx.cfg.num_kv_heads, D)
+    _check_rows("k", k, kv, torch.bfloat16, dev, True)
+    _check_rows("v", v, kv, torch.bfloat16, dev, True)
+    qs = 0
+    if q is not None:
+        _check_rows("q", q, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev, True)
+        _check_rows("q_rot", q_rot, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev)
+        qs = _row_stride(q)
+    _check(_lib.rope_append_paged(ctx.handle, layer, batch.ref, _ptr(q), qs, k.data_ptr(), _row_stride(k), v.data_ptr(),
+                                  _row_stride(v), _ptr(q_rot), cache.ref, _stream(stream)), "rope_append_paged")
+
+
+def _check_attn_paged(ctx: Context, batch: PagedBatch, q_rot, cache: PagedCache, sink, gate, out, lse) -> None:
+    _check_paged(ctx, batch, cache)
+    n, Hq, dev = batch.num_tokens, ctx.cfg.num_q_heads, cache.device
+    _check_rows("q_rot", q_rot, (n, Hq, 256), torch.bfloat16, dev)
+    _check_rows("out", out, (n, Hq, 256), torch.bfloat16, dev)
+    _check_rows("lse", lse, (n, Hq), torch.float32, dev)
+    _check_sink(sink, Hq, q_rot)
+    _check_gate(gate, n, Hq, q_rot)
+
+
+def attn_paged(ctx: Context, layer: int, batch: PagedBatch, q_rot, cache: PagedCache, sink, out, lse, gate=None,
+               stream=None) -> None:
+    """Attention of every new token over its sequence's pages (appended before by
+    rope_append_paged), one token per sequence or chunks: q_rot / out [num_tokens, Hq, 256] bf16,
+    lse / gate [num_tokens, Hq] fp32."""
+    _check_attn_paged(ctx, batch, q_rot, cache, sink, gate, out, lse)
+    _check(_lib.attn_paged(ctx.handle, layer, batch.ref, q_rot.data_ptr(), cache.ref, _ptr(sink), _ptr(gate),
+                           out.data_ptr(), lse.data_ptr(), _stream(stream)), "attn_paged")
+
+
+def select_pages(ctx: Context, layer: int, batch: PagedBatch, q_rot, cache: PagedCache, selected, keep_first: int = 1,
+                 keep_last: int = 1, stream=None) -> None:
+    """Choose for every new token and kv head the blocks it attends to, by the pages' bounds:
+    ``selected`` int32 [num_tokens, Hkv, num_selected], ascending, -1 behind the last."""
+    _check_paged(ctx, batch, cache)
+    _check_rows("q_rot", q_rot, (batch.num_tokens, ctx.cfg.num_q_heads, 256), torch.bfloat16, cache.device)
+    _check_rows("selected", selected, (batch.num_tokens, ctx.cfg.num_kv_heads, selected.shape[-1]), torch.int32,
+                cache.device)
+    _check(_lib.select_pages(ctx.handle, layer, batch.ref, q_rot.data_ptr(), cache.ref, selected.shape[-1], keep_first,
+                             keep_last, selected.data_ptr(), _stream(stream)), "select_pages")
+
+
+def attn_selected_pages(ctx: Context, layer: int, batch: PagedBatch, q_rot, cache: PagedCache, selected, sink, out, lse,
+                        gate=None, stream=None) -> None:
+    """attn_paged restricted, for every token and kv head, to the blocks in ``selected``."""
+    _check_attn_paged(ctx, batch, q_rot, cache, sink, gate, out, lse)
+    _check_rows("selected", selected, (batch.num_tokens, ctx.cfg.num_kv_heads, selected.shape[-1]), torch.int32,
+                cache.device)
+    _check(_lib.attn_selected_pages(ctx.handle, layer, batch.ref, q_rot.data_ptr(), cache.ref, selected.data_ptr(),
+                                    selected.shape[-1], _ptr(sink), _ptr(gate), out.data_ptr(), lse.data_ptr(),
+                                    _stream(stream)), "attn_selected_pages")
 
 
 def hybrid_decode_read_probe(buffer: torch.Tensor, stream=None) -> int:

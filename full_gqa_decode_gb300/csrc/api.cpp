@@ -7,8 +7,6 @@
 // types, known cache layout); the sink checks mirror `_validate_sinks` of
 // vllm/models/hy_v4/nvidia/flashmla_sparse.py (fp32 by type here, one value
 // per query head, NULL for no sink).
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -18,7 +16,8 @@
 #include <new>
 #include <vector>
 
-#include "hd_internal.h"
+#include "hd_context.h"
+#include "paged.h"
 
 using namespace hd;
 
@@ -64,81 +63,7 @@ void hd::plan_split(int64_t batch, int64_t num_kv_heads, int64_t max_keys, int64
 
 namespace {
 
-struct MapCacheEntry {
-    const void *k = nullptr, *v = nullptr;
-    int64_t seq_stride = 0;
-    int32_t capacity = 0, batch = 0;
-    CUtensorMap kmap, vmap;     // boxes of one stage's keys
-    bool wide_valid = false;    // kmapw / vmapw encoded for this cache
-    CUtensorMap kmapw, vmapw;   // boxes of kWideBoxRows keys (64-key bf16 stages)
-};
-
-struct DeviceTable {
-    float2 *data = nullptr;  // [max_context + 1][rotary_dim / 2]
-    int32_t rotary_dim = 0;
-};
-
-struct LayerCall;
-
-}  // namespace
-
-struct hd_ctx {
-    hd_config cfg;
-    std::vector<int32_t> layer_types;
-    int device = 0;
-    int num_sms = 0;
-    int group = 1;
-    int sliding_layout = HD_LAYOUT_RING;
-    DeviceTable table_sliding, table_full;
-    float *part_o = nullptr;
-    float2 *part_ml = nullptr;
-    int64_t part_slots = 0;              // single-layer calls: capacity in (sequence, chunk) pairs
-    int64_t part_rows = 0;               // capacity in partial rows ([256] floats + (m, l) each)
-    uint8_t *stage_k = nullptr;          // [num_layers][max_batch][Hkv][D] entries of the cache type
-    uint8_t *stage_v = nullptr;
-    int kv_type = KV_BF16;
-    int32_t *counters = nullptr;         // [num_layers][max_batch][Hkv] chunk tickets, zero between calls
-    int32_t *err = nullptr;
-    int consumer = CONSUMER_MMA;
-    int cluster_max = 0;                 // largest cluster the single-layer kernel runs with (0: none)
-    bool cluster_combine = true;         // single-layer calls: small grids merge chunks in a cluster
-    int32_t drop_stage = -1;             // test hook, see hybrid_decode_inject_lost_copy
-    bool layer_overlap = true;           // decode_step: layers start before the previous one finishes
-    bool fuse_step = true;               // decode_step: one grid for all layers (step tables)
-    StepTable step_table;                // parameters of the step grid being launched
-    std::vector<LayerCall> step_calls;   // the layer calls of the step being launched
-    std::vector<int> step_order;         // their order in the step grids
-    // Last independence check of decode_step's layers (host memcmp of the array).
-    std::vector<hd_layer_io> indep_layers;
-    int32_t indep_batch = -1, indep_tokens = -1;
-    bool indep_ok = false;
-    int64_t launches = 0;
-    std::vector<MapCacheEntry> maps;     // one per layer
-    int32_t profile_mask = 0;           // bit (1 << layer type): bracket that type's launches
-    bool profile_seen[2] = {false, false};  // FIRST_ONLY: a layer of that type was bracketed in this step
-    std::vector<cudaEvent_t> ev_begin, ev_end;  // [3][kProfileEvents]: per layer type, then step grids
-    size_t ev_used[3] = {0, 0, 0};
-};
-
-namespace {
-
 constexpr int kProfileEvents = 4096;
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int sliding_capacity(const hd_ctx *ctx) {
     return ctx->sliding_layout == HD_LAYOUT_ROLL ? ctx->cfg.sliding_window
@@ -206,12 +131,6 @@ hd_status check_cache(const hd_ctx *ctx, const hd_kv_cache &c) {
     return HD_OK;
 }
 
-// The context's workspace and tensor maps live on the device it was created on.
-hd_status check_device(const hd_ctx *ctx) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == ctx->device ? HD_OK : HD_ERR_STATE;
-}
-
 hd_status check_call(const hd_ctx *ctx, int layer, int batch, const int32_t *context) {
     if (!ctx) return HD_ERR_INVALID_ARG;
     if (layer < 0 || layer >= ctx->cfg.num_layers) return HD_ERR_INVALID_ARG;
@@ -219,8 +138,6 @@ hd_status check_call(const hd_ctx *ctx, int layer, int batch, const int32_t *con
     if (batch > ctx->cfg.max_batch) return HD_ERR_CAPACITY;
     return HD_OK;
 }
-
-hd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? HD_OK : HD_ERR_CUDA; }
 
 // Workspace bound in (sequence, chunk) pairs: the largest chunk always fits
 // (max_batch * ceil(max_keys / kChunkMax)); smaller chunks are allowed up to
@@ -258,30 +175,12 @@ void free_ctx(hd_ctx *ctx) {
     cudaFree(ctx->stage_v);
     cudaFree(ctx->counters);
     cudaFree(ctx->err);
+    cudaFree(ctx->paged_ws);
+    cudaFree(ctx->paged_tickets);
     for (auto e : ctx->ev_begin) cudaEventDestroy(e);
     for (auto e : ctx->ev_end) cudaEventDestroy(e);
     delete ctx;
 }
-
-// Launches the fused layer kernel (see attn_decode.cu) for one layer call.
-struct LayerCall {
-    int layer, batch;
-    const int32_t *context;
-    int max_keys;           // bound on the cached keys any sequence scores (split plan)
-    int key_set, new_kind, commit;
-    const void *q_bf16;     // rotate q in the kernel, or
-    const float *q_rot;     // take it rotated
-    const void *new_k, *new_v;
-    hd_kv_cache cache;
-    const float *sink;
-    const float *gate;
-    void *out;
-    float *lse;
-    bool pdl;               // previous grid in the stream is this step's previous layer kernel
-    bool early = false;     // pdl: the layer may read and stream before that grid completes
-    bool one_chunk = false; // step grids: the layer needs a single chunk per sequence
-    int tokens = 1, token0 = 0, total_tokens = 1;   // multi-token decode: this pass's tokens
-};
 
 // Kernel arguments of one layer call with a given split; its partials start at
 // partial row part_row0 of the workspace, its tickets at the layer's counters.
@@ -728,6 +627,12 @@ hd_status hybrid_decode_init(const hd_config *cfg, hd_ctx **out_ctx) {
               cudaMalloc(&ctx->err, sizeof(int32_t)) == cudaSuccess &&
               cudaMemset(ctx->err, 0, sizeof(int32_t)) == cudaSuccess;
     const size_t stage = (size_t)cfg->num_layers * B * Hkv * kHeadDim * kv_elem_bytes(ctx->kv_type);
+    ctx->paged_ws_bytes = std::max(paged_partial_bytes(ctx->num_sms),
+                                   any_full ? paged_rank_bytes(B, Hkv, cfg->max_context) : 0);
+    ok = ok && kDecodeCtasPerSm * ctx->num_sms <= kPagedTickets &&
+         cudaMalloc(&ctx->paged_ws, (size_t)ctx->paged_ws_bytes) == cudaSuccess &&
+         cudaMalloc(&ctx->paged_tickets, kPagedTickets * sizeof(int32_t)) == cudaSuccess &&
+         cudaMemset(ctx->paged_tickets, 0, kPagedTickets * sizeof(int32_t)) == cudaSuccess;
     ok = ok && cudaMalloc(&ctx->stage_k, stage) == cudaSuccess && cudaMalloc(&ctx->stage_v, stage) == cudaSuccess;
     // The tables, zeroed counters and error word are complete before any call, on
     // whatever stream the caller uses (a non-blocking stream is not ordered after

@@ -1,0 +1,707 @@
+// Attention of few query rows per kv head over a paged cache: single-token
+// decode, a few drafted tokens, and decode over selected pages.
+//
+// Each item (sequence, up to eight query rows = heads x tokens, kv head)
+// streams its visible keys once through a shared-memory ring of 32 KiB stages
+// (32 bf16 or 64 E4M3 keys of K and V).  One producer warp looks the pages up
+// and issues one 5-D TMA copy per page run and stage half -- the box takes all
+// 256 dims as 128-byte column groups, so a stage is two copies for pages of a
+// stage's keys or more, four (16-row bf16 pages) to eight otherwise -- and
+// four consumer warps split a stage's keys: scores and outputs on mma.sync
+// with an online softmax per warp in log2 units, merged at the end of an item.
+// The work is cut evenly over two CTAs per SM (paged_sched.cuh); the ring runs
+// on across items.
+//
+// Rotated queries come in bf16 and enter the products as they are.  With an
+// E4M3 cache codes convert exactly to f16, and a row's q is scaled by the power
+// of two that brings its largest value below 2, so that f16 holds it: values
+// below 2^-14 of that lose bits under 2^-25 of the largest, less than the fp32
+// sum of the products does.  P is rounded to the cache's 16-bit type for the
+// second product (2^-9 or 2^-12 of each weight, below the output's own
+// rounding once summed); sums and maxima stay in fp32.
+#include "paged_sched.cuh"
+
+namespace hd {
+namespace {
+
+constexpr int kRing = 3;                        // stages of 32 KiB
+constexpr int kWarps = 4;                       // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kRowFloats = kDecodeRows * kHeadDim;
+// Shared memory: ring | merge buffer of two warps' rows | row maxima and sums | barriers | scan.
+constexpr int kBufOff = kRing * kStageBytes;
+constexpr int kMlOff = kBufOff + 2 * kRowFloats * 4;
+constexpr int kBarOff = kMlOff + 2 * kWarps * kDecodeRows * 4;
+constexpr int kMiscOff = kBarOff + 2 * kRing * 8;
+constexpr int kSmemBytes = kMiscOff + 64;
+static_assert(kDecodeCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+
+__host__ __device__ constexpr int stage_shift(int kv) { return kv == KV_FP8 ? 6 : 5; }
+// Shortest share of a CTA, in stages: below 128 keys the merge costs more than the split saves.
+__host__ __device__ constexpr int min_units(int kv) { return kv == KV_FP8 ? 2 : 4; }
+
+// A tile of new tokens of one sequence.
+struct Tile {
+    int t0, nt;       // tokens
+    int lo, hi;       // visible positions [lo, hi) of any of them (SPARSE: hi only)
+    int u0, units;    // stages
+};
+
+template <int KV, bool SPARSE>
+__device__ __forceinline__ int tile_tokens(const PagedAttnArgs &a) {
+    return SPARSE ? 1 : kDecodeRows / a.group;
+}
+
+template <int KV, bool SPARSE>
+__device__ __forceinline__ Tile make_tile(const PagedAttnArgs &a, const SeqSpan &q, int tile) {
+    constexpr int kShift = stage_shift(KV), kKeys = 1 << kShift;
+    Tile t;
+    const int tt = tile_tokens<KV, SPARSE>(a);
+    t.t0 = tile * tt;
+    t.nt = min(tt, q.n - t.t0);
+    t.hi = q.ctx + t.t0 + t.nt;
+    if (SPARSE) {
+        const int blocks = min(a.num_selected, ((t.hi - 1) >> a.seqs.page_shift) + 1);
+        t.lo = 0;
+        t.u0 = 0;
+        t.units = (int)((((long long)blocks << a.seqs.page_shift) + kKeys - 1) >> kShift);
+    } else {
+        t.lo = a.window ? max(0, q.ctx + t.t0 - a.window + 1) : 0;
+        t.u0 = t.lo >> kShift;
+        t.units = ((t.hi + kKeys - 1) >> kShift) - t.u0;
+    }
+    return t;
+}
+
+// Where a CTA is in the list of items.
+struct Cursor {
+    int b, tile, h, off;   // off: stages of the item already passed
+};
+
+template <int KV, bool SPARSE>
+__device__ __forceinline__ int num_tiles(const PagedAttnArgs &a, int n) {
+    const int tt = tile_tokens<KV, SPARSE>(a);
+    return (n + tt - 1) / tt;
+}
+
+// The item after (c, q): advances to the next kv head, tile or sequence.
+template <int KV, bool SPARSE>
+__device__ __forceinline__ void next_item(const PagedAttnArgs &a, Cursor &c, SeqSpan &q) {
+    c.off = 0;
+    if (++c.h < a.num_kv_heads) return;
+    c.h = 0;
+    if (++c.tile < num_tiles<KV, SPARSE>(a, q.n)) return;
+    c.tile = 0;
+    int bit;
+    do {
+        q = seq_span(a.seqs, ++c.b, &bit);
+    } while (q.n == 0 && c.b + 1 < a.seqs.batch);
+}
+
+// Position of key `x` (a stage-aligned index into the item's keys) and the page holding it; -1: no page.
+// SPARSE: x indexes the selected blocks' slots, and the position is huge past their end.
+template <bool SPARSE>
+__device__ __forceinline__ int key_position(const PagedAttnArgs &a, const int32_t *sel, const Tile &t, int x) {
+    if (!SPARSE) return x;
+    const int j = x >> a.seqs.page_shift, slot = x & ((1 << a.seqs.page_shift) - 1);
+    const int blk = j < a.num_selected ? sel[j] : -1;
+    if (blk < 0 || blk > ((t.hi - 1) >> a.seqs.page_shift)) return 0x40000000;
+    return (blk << a.seqs.page_shift) + slot;
+}
+
+// ------------------------------------------------------------- consumers --
+// One warp's keys of a stage against the tile's rows.  `base`: byte offset of
+// the warp's first key row in a stage half, `col`: bytes between its 128-byte
+// column groups; key0: position of that key; [vlo, vhi): positions whose V may
+// be read; full: every row sees every key of the warp.
+struct DecodeBf16 {
+    static constexpr int kKeys = 8;
+    uint32_t qa[16][2];
+    float o[16][4];        // O^T: dims 16 mt + gid (+ 8) x rows 2 t4 (+ 1)
+    float m_run, l_run;    // row gid; l_run: this lane's keys
+    int lo, hi;            // row gid's visible positions
+
+    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        const int tok = gid / a.group, rows = t.nt * a.group;
+        const __nv_bfloat16 *src =
+            a.q + ((size_t)(q.row0 + t.t0 + tok) * a.num_q_heads + h * a.group + gid % a.group) * kHeadDim + 2 * t4;
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+            qa[ks][0] = gid < rows ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks)) : 0u;
+            qa[ks][1] = gid < rows ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 8)) : 0u;
+        }
+        hi = q.ctx + t.t0 + tok;
+        lo = a.window ? hi - a.window + 1 : 0;
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
+        m_run = -INFINITY;
+        l_run = 0.f;
+    }
+
+    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
+                            int vhi, bool full, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3, lr = lane & 7, lsub = lane >> 3;
+        const uint32_t sw0 = (uint32_t)(lsub ^ lr) << 4, sw1 = (uint32_t)((4 + lsub) ^ lr) << 4;
+        const uint32_t kb = smem_u32(kst) + base + lr * 128, vb = smem_u32(vst) + base + lr * 128;
+        // Two accumulators (even / odd k-steps) halve the dependent MMA chain.
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(kb + (p >> 1) * col + (p & 1 ? sw1 : sw0), b0, b1, b2, b3);
+            const uint32_t a0[4] = {qa[2 * p][0], 0u, qa[2 * p][1], 0u};
+            const uint32_t a1[4] = {qa[2 * p + 1][0], 0u, qa[2 * p + 1][1], 0u};
+            mma_16816(s, a0, b0, b1);
+            mma_16816(s2, a1, b2, b3);
+        }
+        const int k0 = key0 + 2 * t4;
+        const bool ok0 = full || (k0 >= lo && k0 <= hi), ok1 = full || (k0 + 1 >= lo && k0 + 1 <= hi);
+        const float x0 = ok0 ? (s[0] + s2[0]) * kQScale : -INFINITY;
+        const float x1 = ok1 ? (s[1] + s2[1]) * kQScale : -INFINITY;
+        float mx = fmaxf(x0, x1);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m_run, mx);
+        const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m_run - mn);
+        const float p0 = ok0 ? fast_exp2(x0 - mn) : 0.f, p1 = ok1 ? fast_exp2(x1 - mn) : 0.f;
+        l_run = fmaf(l_run, alpha, p0 + p1);
+        m_run = mn;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2 t4
+            const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2 t4 + 1
+#pragma unroll
+            for (int mt = 0; mt < 16; ++mt) {
+                o[mt][0] *= a_lo;
+                o[mt][1] *= a_hi;
+                o[mt][2] *= a_lo;
+                o[mt][3] *= a_hi;
+            }
+        }
+        const uint32_t pb = pack_bf16(p0, p1);
+        // Slots outside [vlo, vhi) may hold anything, and 0 * NaN would reach every row.
+        uint32_t vm = 0xFFFFFFFFu;
+        if (!full)
+            vm = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_trans(vb + (p >> 1) * col + (p & 1 ? sw1 : sw0), a0, a1, a2, a3);
+            mma_1688(o[2 * p], a0 & vm, a1 & vm, pb);
+            mma_1688(o[2 * p + 1], a2 & vm, a3 & vm, pb);
+        }
+    }
+
+    // Row gid's maximum and (whole warp's) sum, by the lane with t4 = 0.
+    __device__ void publish(float *ml, int warp, int lane) const {
+        float l = l_run;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if ((lane & 3) == 0) {
+            ml[warp * kDecodeRows + (lane >> 2)] = m_run;
+            ml[(kWarps + warp) * kDecodeRows + (lane >> 2)] = l;
+        }
+    }
+    template <class F> __device__ void each(int lane, F f) {   // f(row, dim, value&)
+        const int gid = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt) {
+            f(2 * t4, 16 * mt + gid, o[mt][0]);
+            f(2 * t4 + 1, 16 * mt + gid, o[mt][1]);
+            f(2 * t4, 16 * mt + gid + 8, o[mt][2]);
+            f(2 * t4 + 1, 16 * mt + gid + 8, o[mt][3]);
+        }
+    }
+};
+
+// E4M3 pages: S^T = K Q^T with the warp's 16 keys on M, codes converted to f16
+// as the A operand; O^T = V^T P^T as in the bf16 case with 16 keys on K.  Lane
+// (gid, t4) reads 16-byte chunks 2 t4 + (p & 1) + 8 (p >> 1) of key rows gid
+// and gid + 8 at step p (eight lanes of a phase hit eight different chunks);
+// q's columns are held in the same order of dims, which leaves every dot
+// product as it is.
+struct DecodeE4m3 {
+    static constexpr int kKeys = 16;
+    uint32_t qb[16][2];
+    float o[16][4];            // O^T tile mt: dims 128 (mt / 8) + 16 gid + 2 (mt % 8) (+ 1) x rows 2 t4 (+ 1)
+    float m_run[2], l_run[2];  // rows 2 t4 + e
+    float sc[2];               // score scale of rows 2 t4 + e, log2 units
+    int lo[2], hi[2];
+
+    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        const int rows = t.nt * a.group;
+        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
+                                          gid % a.group) * kHeadDim;
+        uint2 w[16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = 16 * (2 * t4 + (p & 1) + 8 * (p >> 1)) + 4 * j;
+                w[4 * p + j] = gid < rows ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
+                const uint2 m = make_uint2(w[4 * p + j].x & 0x7FFF7FFFu, w[4 * p + j].y & 0x7FFF7FFFu);
+                top = max(top, max(max(m.x & 0xFFFFu, m.x >> 16), max(m.y & 0xFFFFu, m.y >> 16)));
+            }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = min(max((int)(top >> 7), 1), 253);               // exponent field of the row's largest value
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^(127 - ex)
+        const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            qb[i][0] = pack_f16(__uint_as_float(w[i].x << 16) * down, __uint_as_float(w[i].x & 0xFFFF0000u) * down);
+            qb[i][1] = pack_f16(__uint_as_float(w[i].y << 16) * down, __uint_as_float(w[i].y & 0xFFFF0000u) * down);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sc[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * kQScale);
+            hi[e] = q.ctx + t.t0 + (2 * t4 + e) / a.group;
+            lo[e] = a.window ? hi[e] - a.window + 1 : 0;
+            m_run[e] = -INFINITY;
+            l_run[e] = 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
+    }
+
+    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
+                            int vhi, bool full, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int chunk = 2 * t4 + (p & 1) + 8 * (p >> 1);
+            const uint4 ka = *reinterpret_cast<const uint4 *>(kst + at(gid, chunk));
+            const uint4 kb = *reinterpret_cast<const uint4 *>(kst + at(gid + 8, chunk));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x[4] = {e4m3x2_to_f16x2((uint16_t)(wa[j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(wb[j] & 0xFFFFu)),
+                                       e4m3x2_to_f16x2((uint16_t)(wa[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wb[j] >> 16))};
+                mma_16816_f16(j & 1 ? s2 : s, x, qb[4 * p + j][0], qb[4 * p + j][1]);
+            }
+        }
+        float p[4], alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int k0 = key0 + gid;
+            const bool v0 = full || (k0 >= lo[e] && k0 <= hi[e]), v1 = full || (k0 + 8 >= lo[e] && k0 + 8 <= hi[e]);
+            const float x0 = v0 ? (s[e] + s2[e]) * sc[e] : -INFINITY;
+            const float x1 = v1 ? (s[2 + e] + s2[2 + e]) * sc[e] : -INFINITY;
+            float mx = fmaxf(x0, x1);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m_run[e], mx);
+            alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+            p[e] = v0 ? fast_exp2(x0 - mn) : 0.f;
+            p[2 + e] = v1 ? fast_exp2(x1 - mn) : 0.f;
+            l_run[e] = fmaf(l_run[e], alpha[e], p[e] + p[2 + e]);
+            m_run[e] = mn;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < 16; ++mt) {
+                o[mt][0] *= alpha[0];
+                o[mt][1] *= alpha[1];
+                o[mt][2] *= alpha[0];
+                o[mt][3] *= alpha[1];
+            }
+        }
+        const uint32_t pb0 = movmatrix_trans(pack_f16(p[0], p[1]));   // keys 2 t4 (+ 1) of row gid
+        const uint32_t pb1 = movmatrix_trans(pack_f16(p[2], p[3]));   // keys 8 + 2 t4 (+ 1)
+        uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
+        if (!full) {   // slots outside [vlo, vhi) may hold NaN codes
+            const int k0 = key0 + 2 * t4;
+            m01 = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
+            m89 = (k0 + 8 >= vlo && k0 + 8 < vhi ? 0x0000FFFFu : 0u) | (k0 + 9 >= vlo && k0 + 9 < vhi ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int chunk = 8 * half + gid;
+            const uint4 v0 = *reinterpret_cast<const uint4 *>(vst + at(2 * t4, chunk));
+            const uint4 v1 = *reinterpret_cast<const uint4 *>(vst + at(2 * t4 + 1, chunk));
+            const uint4 v8 = *reinterpret_cast<const uint4 *>(vst + at(2 * t4 + 8, chunk));
+            const uint4 v9 = *reinterpret_cast<const uint4 *>(vst + at(2 * t4 + 9, chunk));
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t w8[4] = {v8.x, v8.y, v8.z, v8.w}, w9[4] = {v9.x, v9.y, v9.z, v9.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {   // dims 4 w + 2 q (row gid) and 4 w + 2 q + 1 (row gid + 8)
+                    const uint32_t sel = q ? 0x7362u : 0x5140u;
+                    const uint32_t x01 = __byte_perm(w0[w], w1[w], sel), x89 = __byte_perm(w8[w], w9[w], sel);
+                    const uint32_t x[4] = {e4m3x2_to_f16x2((uint16_t)(x01 & 0xFFFFu)) & m01, e4m3x2_to_f16x2((uint16_t)(x01 >> 16)) & m01,
+                                           e4m3x2_to_f16x2((uint16_t)(x89 & 0xFFFFu)) & m89, e4m3x2_to_f16x2((uint16_t)(x89 >> 16)) & m89};
+                    mma_16816_f16(o[8 * half + 2 * w + q], x, pb0, pb1);
+                }
+        }
+    }
+
+    __device__ void publish(float *ml, int warp, int lane) const {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = l_run[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (lane < 4) {
+                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e];
+                ml[(kWarps + warp) * kDecodeRows + 2 * lane + e] = l;
+            }
+        }
+    }
+    template <class F> __device__ void each(int lane, F f) {
+        const int gid = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt) {
+            const int d = 128 * (mt >> 3) + 16 * gid + 2 * (mt & 7);
+            f(2 * t4, d, o[mt][0]);
+            f(2 * t4 + 1, d, o[mt][1]);
+            f(2 * t4, d + 1, o[mt][2]);
+            f(2 * t4 + 1, d + 1, o[mt][3]);
+        }
+    }
+};
+
+template <int KV> struct DecodeConsumer;
+template <> struct DecodeConsumer<KV_BF16> { using T = DecodeBf16; };
+template <> struct DecodeConsumer<KV_FP8> { using T = DecodeE4m3; };
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+// exp2(x - m) of a partial's maximum x, 0 for a partial that saw no key.
+__device__ __forceinline__ float part_weight(float x, float m) { return x == -INFINITY ? 0.f : fast_exp2(x - m); }
+
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w,
+                                            int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Rows of a bad sequence: NaN, as the decode calls give.
+__device__ __forceinline__ void fill_bad_rows(const PagedAttnArgs &a, int first, int stride) {
+    for (int b = first; b < a.seqs.batch; b += stride) {
+        int bit, rows = 0;
+        const SeqSpan q = seq_span(a.seqs, b, &bit, &rows);
+        if (!bit) continue;
+        if (threadIdx.x == 0) atomicOr(a.seqs.err, bit);
+        const size_t n = (size_t)rows * a.num_q_heads, r0 = (size_t)q.row0 * a.num_q_heads;
+        for (size_t i = threadIdx.x; i < n * (kHeadDim / 2); i += blockDim.x)
+            reinterpret_cast<uint32_t *>(a.out)[r0 * (kHeadDim / 2) + i] = 0x7FFF7FFFu;
+        for (size_t i = threadIdx.x; i < n; i += blockDim.x) a.lse[r0 + i] = __int_as_float(0x7FC00000);
+    }
+}
+
+// Writes row r of a finished tile (thread's four dims d..d+3 of its
+// unnormalised output, log2-unit maximum m and sum l).
+__device__ __forceinline__ void finish_row(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int r, int d,
+                                           float4 v, float m, float l, float vscale) {
+    const size_t row = (size_t)(q.row0 + t.t0 + r / a.group) * a.num_q_heads + h * a.group + r % a.group;
+    const int head = h * a.group + r % a.group;
+    // A row that sees no key (selected lists only) gives 0 and lse -inf; NaN scores stay NaN.
+    const float lse = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
+    float f = vscale / l;
+    if (a.sink) f *= 1.f / (1.f + fast_exp2((a.sink[head] - lse) * kLog2e));
+    if (a.gate) f *= 1.f / (1.f + fast_exp2(-a.gate[row] * kLog2e));
+    if (l == 0.f) f = 0.f;
+    uint2 w;
+    w.x = pack_bf16(v.x * f, v.y * f);
+    w.y = pack_bf16(v.z * f, v.w * f);
+    *reinterpret_cast<uint2 *>(a.out + row * kHeadDim + d) = w;
+    if (d == 0) a.lse[row] = lse;
+}
+
+template <int KV, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ PagedAttnArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kShift = stage_shift(KV), kKeys = 1 << kShift;
+    constexpr int kHalf = kStageBytes / 2;
+    float *buf = reinterpret_cast<float *>(smem + kBufOff);
+    float *ml = reinterpret_cast<float *>(smem + kMlOff);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff), *empty = full + kRing;
+    int *misc = reinterpret_cast<int *>(smem + kMiscOff);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const PagedSeqs &sq = a.seqs;
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWarps);
+        }
+        fence_mbar_init();
+    }
+    // The whole call's stages, and this CTA's share of them.
+    const int per = (sq.batch + kThreads - 1) / kThreads;
+    const int b_lo = min(tid * per, sq.batch), b_hi = min(b_lo + per, sq.batch);
+    long long mine = 0;
+    int bad = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        int bit;
+        const SeqSpan q = seq_span(sq, b, &bit);
+        bad |= bit;
+        const int tiles = num_tiles<KV, SPARSE>(a, q.n);
+        for (int i = 0; i < tiles; ++i) mine += (long long)make_tile<KV, SPARSE>(a, q, i).units * a.num_kv_heads;
+    }
+    bad = __syncthreads_or(bad);
+    long long T;
+    const long long before = block_prefix(mine, reinterpret_cast<long long *>(buf), &T);
+    if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
+    const int n = (int)min((long long)gridDim.x, max(T / min_units(KV), 1LL));
+    const int cta = blockIdx.x;
+    if (cta >= n || T == 0) return;
+    const long long x0 = T * cta / n, x1 = T * (cta + 1) / n;
+    if (before <= x0 && x0 < before + mine) {
+        long long rem = x0 - before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            int bit;
+            const SeqSpan q = seq_span(sq, b, &bit);
+            const int tiles = num_tiles<KV, SPARSE>(a, q.n);
+            bool found = false;
+            for (int i = 0; i < tiles; ++i) {
+                const int u = make_tile<KV, SPARSE>(a, q, i).units;
+                if (rem < (long long)u * a.num_kv_heads) {
+                    misc[0] = b;
+                    misc[1] = i;
+                    misc[2] = (int)(rem / u);
+                    misc[3] = (int)(rem % u);
+                    found = true;
+                    break;
+                }
+                rem -= (long long)u * a.num_kv_heads;
+            }
+            if (found) break;
+        }
+    }
+    __syncthreads();
+    Cursor c{misc[0], misc[1], misc[2], misc[3]};
+    int bit;
+    SeqSpan q = seq_span(sq, c.b, &bit);
+    const int ps = 1 << sq.page_shift;
+    const int box_shift = min(sq.page_shift, kShift), box_rows = 1 << box_shift;
+    constexpr int kRowBytes = kHeadDim * kv_elem_bytes(KV);
+
+    if (warp == kWarps) {
+        // ---- producer ----
+        const uint32_t copies = kKeys >> box_shift;   // per stage half
+        long long x = x0;
+        int st = 0;
+        uint32_t ph = 0;
+        bool dead = false;
+        int issued = 0;
+        while (x < x1) {
+            const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
+            const int seg = (int)min((long long)(t.units - c.off), x1 - x);
+            const int32_t *row = sq.table + (size_t)c.b * sq.table_stride;
+            const int32_t *sel = SPARSE ? a.selected + ((size_t)(q.row0 + t.t0) * a.num_kv_heads + c.h) * a.num_selected : nullptr;
+            // The segment's copies, 32 at a time: lane l looks up copy i0 + l's page and slot.
+            const int first_key = (t.u0 + c.off) << kShift, total = seg * (int)copies;
+            for (int i0 = 0; i0 < total; i0 += 32) {
+                int page = sq.num_pages, slot = 0;   // page num_pages lies outside the map: the copy fills zeros
+                if (i0 + lane < total) {
+                    const int x_key = first_key + ((i0 + lane) << box_shift);
+                    const int pos = key_position<SPARSE>(a, sel, t, x_key);
+                    slot = x_key & (ps - 1);
+                    if (pos < t.hi && pos + box_rows > t.lo) {
+                        page = row[pos >> sq.page_shift];
+                        if (page < 0 || page >= sq.num_pages) {
+                            atomicOr(sq.err, HD_DEVERR_PAGE);
+                            page = sq.num_pages;
+                        }
+                    }
+                }
+                const int cnt = min(32, total - i0);
+                for (int i = 0; i < cnt; i += copies) {   // copies divides 32
+                    uint8_t *dst = smem + st * kStageBytes;
+                    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
+                    const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
+                    if (!drop) {
+                        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
+                        __syncwarp();
+                        if (lane >= i && lane < i + (int)copies) {
+                            uint8_t *d = dst + (lane - i) * (box_rows * kRowBytes);
+                            tma_load_5d(d, &kmap, &full[st], 0, slot, 0, c.h, page);
+                            tma_load_5d(d + kHalf, &vmap, &full[st], 0, slot, 0, c.h, page);
+                        }
+                    }
+                    ++issued;
+                    if (++st == kRing) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            x += seg;
+            if (x < x1) next_item<KV, SPARSE>(a, c, q);
+        }
+        if (dead && lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
+        return;
+    }
+
+    // ---- consumers ----
+    typename DecodeConsumer<KV>::T cons;
+    constexpr int kWK = decltype(cons)::kKeys;
+    const int r0 = warp * kWK;   // this warp's key rows of a stage
+    const uint32_t base = (uint32_t)(r0 >> box_shift) * (box_rows * kRowBytes) + (r0 & (box_rows - 1)) * 128;
+    const uint32_t col = box_rows * 128;
+    long long x = x0;
+    int st = 0;
+    uint32_t ph = 0;
+    bool dead = false;
+    while (x < x1) {
+        const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
+        const int seg = (int)min((long long)(t.units - c.off), x1 - x);
+        const long long item0 = x - c.off;
+        const int32_t *sel = SPARSE ? a.selected + ((size_t)(q.row0 + t.t0) * a.num_kv_heads + c.h) * a.num_selected : nullptr;
+        cons.init(a, q, t, c.h, lane);
+        const int all_hi = q.ctx + t.t0;                                        // every row sees up to here ..
+        const int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;      // .. from here
+        for (int u = 0; u < seg; ++u) {
+            const int key0 = key_position<SPARSE>(a, sel, t, ((t.u0 + c.off + u) << kShift) + r0);
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[st], ph))) {
+                dead = true;
+                if (lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
+            }
+            if (!dead && key0 < t.hi && key0 + kWK > t.lo) {
+                const uint8_t *stage = smem + st * kStageBytes;
+                const bool whole = key0 >= all_lo && key0 + kWK - 1 <= all_hi;
+                cons.consume(stage, stage + kHalf, base, col, key0, t.lo, t.hi, whole, lane);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+            if (++st == kRing) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+        // Merge the four warps: warps 2 and 3 hand their rows to 0 and 1.
+        const int rows = t.nt * a.group;
+        cons.publish(ml, warp, lane);
+        consumer_sync();
+        auto row_max = [&](int r) {
+            return fmaxf(fmaxf(ml[r], ml[kDecodeRows + r]), fmaxf(ml[2 * kDecodeRows + r], ml[3 * kDecodeRows + r]));
+        };
+        auto row_sum = [&](int r, float m) {
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                l += ml[(kWarps + w) * kDecodeRows + r] * part_weight(ml[w * kDecodeRows + r], m);
+            return l;
+        };
+        {
+            const int ra = 2 * (lane & 3);
+            const float wa = part_weight(ml[warp * kDecodeRows + ra], row_max(ra));
+            const float wb = part_weight(ml[warp * kDecodeRows + ra + 1], row_max(ra + 1));
+            float *mine_buf = buf + (warp & 1) * kRowFloats;
+            if (warp >= 2) cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kHeadDim + d] = v * (r & 1 ? wb : wa); });
+            consumer_sync();
+            if (warp < 2)
+                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kHeadDim + d] += v * (r & 1 ? wb : wa); });
+        }
+        consumer_sync();
+        const bool begins = c.off == 0, ends = c.off + seg == t.units;
+        const float vscale = KV == KV_FP8 ? a.v_scale[c.h] : 1.f;
+        const bool whole_item = begins && ends;
+        const int slot = begins ? 2 * cta + 1 : 2 * cta;
+        for (int i = tid; i < rows * (kHeadDim / 4); i += kWarps * 32) {
+            const int r = i >> 6, d = (i & 63) * 4;
+            float4 v = *reinterpret_cast<const float4 *>(buf + r * kHeadDim + d);
+            const float4 w = *reinterpret_cast<const float4 *>(buf + kRowFloats + r * kHeadDim + d);
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            const float m = row_max(r), l = row_sum(r, m);
+            if (whole_item) {
+                finish_row(a, q, t, c.h, r, d, v, m, l, vscale);
+            } else {
+                *reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kDecodeRows + r) * kHeadDim + d) = v;
+                if (d == 0) a.part_ml[(size_t)slot * kDecodeRows + r] = make_float2(m, l);
+            }
+        }
+        if (!whole_item) {
+            const int i0 = cta_of_unit(item0, T, n), i1 = cta_of_unit(item0 + t.units - 1, T, n), nseg = i1 - i0 + 1;
+            __threadfence();
+            consumer_sync();
+            if (tid == 0) misc[4] = atomicAdd(&a.tickets[i0], 1) == nseg - 1;
+            consumer_sync();
+            if (misc[4]) {
+                __threadfence();
+                // Weights of the pieces, [rows][nseg] in the merge buffer: nseg <= CTAs.
+                auto piece = [&](int j) { return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kDecodeRows; };
+                for (int r = warp; r < rows; r += kWarps) {
+                    float m = -INFINITY;
+                    for (int j = lane; j < nseg; j += 32) m = fmaxf(m, __ldcg(&a.part_ml[piece(j) + r]).x);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    float l = 0.f;
+                    for (int j = lane; j < nseg; j += 32) {
+                        const float2 p = __ldcg(&a.part_ml[piece(j) + r]);
+                        const float w = part_weight(p.x, m);
+                        buf[r * nseg + j] = w;
+                        l += w * p.y;
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    if (lane == 0) {
+                        ml[r] = m;
+                        ml[kDecodeRows + r] = l;
+                    }
+                }
+                consumer_sync();
+                for (int i = tid; i < rows * (kHeadDim / 4); i += kWarps * 32) {
+                    const int r = i >> 6, d = (i & 63) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int j = 0; j < nseg; ++j) {
+                        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (piece(j) + r) * kHeadDim + d));
+                        const float w = buf[r * nseg + j];
+                        v.x = fmaf(w, p.x, v.x);
+                        v.y = fmaf(w, p.y, v.y);
+                        v.z = fmaf(w, p.z, v.z);
+                        v.w = fmaf(w, p.w, v.w);
+                    }
+                    finish_row(a, q, t, c.h, r, d, v, ml[r], ml[kDecodeRows + r], vscale);
+                }
+                if (tid == 0) a.tickets[i0] = 0;
+            }
+        }
+        consumer_sync();   // the merge buffer and ml are free again
+        x += seg;
+        if (x < x1) next_item<KV, SPARSE>(a, c, q);
+    }
+}
+
+template <int KV, bool SPARSE>
+cudaError_t launch(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (!done_on_device(done, &dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<KV, SPARSE>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        mark_done_on_device(done, dev);
+    }
+    paged_decode_kernel<KV, SPARSE><<<kDecodeCtasPerSm * num_sms, kThreads, kSmemBytes, s>>>(*kmap, *vmap, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms,
+                                cudaStream_t s) {
+    const bool sparse = a.selected != nullptr;
+    if (a.kv_type == KV_FP8)
+        return sparse ? launch<KV_FP8, true>(kmap, vmap, a, num_sms, s) : launch<KV_FP8, false>(kmap, vmap, a, num_sms, s);
+    return sparse ? launch<KV_BF16, true>(kmap, vmap, a, num_sms, s) : launch<KV_BF16, false>(kmap, vmap, a, num_sms, s);
+}
+
+}  // namespace hd

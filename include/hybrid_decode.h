@@ -106,7 +106,10 @@ enum {
     HD_DEVERR_CONTEXT_NEGATIVE = 1,  /* context[b] < 0                                     */
     HD_DEVERR_CONTEXT_CAPACITY = 2,  /* full layer: context[b] >= cache capacity            */
     HD_DEVERR_CONTEXT_PLAN = 4,      /* context[b] > max_context (table / split plan)       */
-    HD_DEVERR_WAIT_TIMEOUT = 8       /* a pipeline wait gave up after its time limit        */
+    HD_DEVERR_WAIT_TIMEOUT = 8,      /* a pipeline wait gave up after its time limit        */
+    HD_DEVERR_TOKEN_OFFSETS = 16,    /* paged: a sequence's token_offsets are no row range, or
+                                      * name more than max_tokens rows                      */
+    HD_DEVERR_PAGE = 32              /* paged: a needed block's page is not in the pool      */
 };
 
 typedef struct hd_ctx hd_ctx;
@@ -409,6 +412,141 @@ hd_status decode_attn_full_static_scratch(int32_t batch, int32_t num_q_heads, in
 hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t max_context, int32_t num_sms, int64_t *scratch_bytes,
                                                int32_t *chunk_keys, int32_t *num_chunks);
+
+/* ---------------------------------------------------------------- paged caches --
+ *
+ * An extension beyond the pages' per-sequence tensors, for programs that give
+ * out K/V memory in pages and that take prompts in chunks: the same model, the
+ * same tables, sinks, gates and cache types over a pool of pages.  Block i of a
+ * sequence holds its positions i * page_size .. (i + 1) * page_size - 1, in
+ * the page its row of the block table names; sliding layers keep every
+ * position in the page of its block as well (neither ring nor roll), so blocks
+ * that have left the window can be given back: an entry that no call needs is
+ * never read and may be anything.
+ *
+ * A call takes new tokens of `batch` sequences: one each (decode), a few, or a
+ * chunk of a prompt, ragged.  rope_append_paged first puts their keys and
+ * values into the pages; attn_paged (or select_pages and attn_selected_pages)
+ * then attends.  Each query is rotated and rounded to bf16 once, by
+ * rope_append_paged (the per-sequence calls keep fp32 queries).
+ *
+ * Entries at visible positions must be finite; slots no query may see (behind
+ * a sequence's end, before its window) can hold anything, NaN included.  A
+ * non-finite entry among the positions of a chunk can reach every row of that
+ * chunk.
+ *
+ * These calls share the context's workspace: order all calls on one context,
+ * captured graphs among them, on one stream.  They can be captured, and none
+ * allocates.  hd_paged_cache and hd_paged_batch are read during the call only.
+ *
+ * Bad values on the device: a sequence with bad token_offsets, more than
+ * max_tokens tokens, a context below 0 or above max_context, or a position past
+ * the block table or the rotary table is flagged (HD_DEVERR_*), not stored, and
+ * gets NaN out / lse; a needed page outside the pool is flagged, skipped by the
+ * append and read as zeros by the attention.  Rows of out / lse / q_rot /
+ * selected that belong to no sequence stay as they are. */
+
+/* A pool of pages.  k / v: page p starts at p * page_stride elements; within it
+ * [num_kv_heads][page_size][head_dim], bf16 or E4M3 codes.  page_size: 16, 32,
+ * 64, 128 or 256.  page_stride >= num_kv_heads * page_size * head_dim and a
+ * multiple of 16 bytes; k and v 16-byte aligned.  k_scale / v_scale: fp32
+ * [num_kv_heads], E4M3 only.  bounds: bf16 [num_pages][num_kv_heads][2][head_dim],
+ * 16-byte aligned, the elementwise minimum and maximum of the keys that each
+ * page holds (E4M3: of their codes' values, without the scale); NULL when
+ * select_pages is not used. */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t page_stride;
+    int32_t num_pages;
+    int32_t page_size;
+    const float *k_scale;
+    const float *v_scale;
+    void *bounds;
+} hd_paged_cache;
+
+/* The sequences of a call.  block_table: device [batch][table_stride], of which
+ * the first max_blocks entries of a row are the sequence's pages.  context:
+ * device [batch], previous tokens.  token_offsets: device [batch + 1],
+ * ascending: rows token_offsets[b] .. token_offsets[b + 1] - 1 of q / k / v /
+ * out are sequence b's new tokens, at positions context[b] onwards (none is
+ * allowed); NULL: one token each, row b.  num_tokens: rows of the tensors.
+ * With num_tokens 0 a call does nothing and the row tensors may be NULL.
+ * max_tokens: a bound on any sequence's new tokens; max_context: a bound on
+ * context[b] (0: the largest the context serves, max_context - max_tokens + 1).
+ * The bounds pick kernels and grid sizes; results do not depend on them. */
+typedef struct {
+    const int32_t *block_table;
+    const int32_t *context;
+    const int32_t *token_offsets;
+    int32_t table_stride;
+    int32_t max_blocks;
+    int32_t batch;
+    int32_t num_tokens;
+    int32_t max_tokens;
+    int32_t max_context;
+} hd_paged_batch;
+
+/* Pure host check of a paged call's descriptors against a configuration (no
+ * device use; pointers are not followed).  Every paged call makes it first.
+ * HD_ERR_UNSUPPORTED for a page_size that is not listed above, HD_ERR_CAPACITY
+ * for a batch above max_batch or a max_context above the configuration's. */
+hd_status hd_validate_paged(const hd_config *cfg, const hd_paged_batch *batch, const hd_paged_cache *cache);
+
+/* Rotates the new queries and keys of a layer (`_rope`, `_angles` of
+ * spark_export.py, at positions context[b] + t) and stores the new entries in
+ * their pages: keys rotated exactly and rounded once (to bf16, or to E4M3 of
+ * the quotient by the scale), values bit for bit (or as E4M3), like
+ * rope_append_kv; and brings the touched pages' bounds up to date (a page whose
+ * slot 0 is written starts anew) unless cache->bounds is NULL.
+ *   q       bf16 [num_tokens][num_q_heads][head_dim], rows q_stride elements apart
+ *   k, v    bf16 [num_tokens][num_kv_heads][head_dim], rows k_stride / v_stride apart
+ *   q_rot   bf16 [num_tokens][num_q_heads][head_dim], contiguous; may be q itself
+ * (parts of one projection's rows are taken in place).  q and q_rot may both be
+ * NULL.  Strides are multiples of 8 elements, pointers 16-byte aligned.  Pages
+ * must not be shared by sequences that write them in one call.
+ * HD_ERR_UNSUPPORTED when the layer's rotary_dim is no multiple of 8. */
+hd_status rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_rot,
+                            const hd_paged_cache *cache, void *stream);
+
+/* Attention of every new token over its sequence's pages: position p sees
+ * positions max(0, p - window + 1) .. p on a sliding layer and 0 .. p on a full
+ * one, the new tokens' own entries (already appended) among them; sink and gate
+ * (either may be NULL) as in decode_attn_full.
+ *   q_rot, out  bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned
+ *   gate, lse   fp32 [num_tokens][num_q_heads] */
+hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
+                     const hd_paged_cache *cache, const float *sink, const float *gate, void *out, float *lse,
+                     void *stream);
+
+/* Chooses, for every new token and kv head of a full layer, num_selected blocks
+ * of its sequence: the first keep_first and the last keep_last blocks up to the
+ * token's own, then those of the largest score
+ *     sum over the kv head's query heads and dims of max(q_d lo_d, q_d hi_d)
+ * with lo / hi the block's bounds -- the sum of the largest scores that any of
+ * its keys could reach.  Ties go to the lower block; scores are summed to twice
+ * fp32's precision, so the choice does not depend on the order of summation.
+ *   selected  int32 [num_tokens][num_kv_heads][num_selected]: block numbers,
+ *             ascending, -1 behind the last when a token has fewer blocks.
+ * Bounds must be finite for every block up to the token's own.
+ * HD_ERR_STATE for a sliding layer; HD_ERR_INVALID_ARG without bounds, with
+ * num_selected < 1 or keep_first + keep_last > num_selected; HD_ERR_CAPACITY
+ * above 16384 blocks a sequence, or when the ranking keys (8 bytes for each row,
+ * kv head and block of max_context) exceed the context's workspace, which holds
+ * those of max_batch rows of max_context. */
+hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
+                       const hd_paged_cache *cache, int32_t num_selected, int32_t keep_first, int32_t keep_last,
+                       int32_t *selected, void *stream);
+
+/* attn_paged of a full layer with every (token, kv head) restricted to the
+ * positions of its selected blocks (`selected` as select_pages writes it, or the
+ * caller's own: distinct blocks, the valid ones first).  Entries that are
+ * negative or beyond the token's block are skipped; a row left with no position
+ * gives out 0 and lse -inf. */
+hd_status attn_selected_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
+                              const hd_paged_cache *cache, const int32_t *selected, int32_t num_selected,
+                              const float *sink, const float *gate, void *out, float *lse, void *stream);
 
 /* Measurement utility (no counterpart in the pages): one pass of a pure read
  * stream over `bytes` of the device buffer (16-byte aligned), through shared
