@@ -10,6 +10,8 @@ constexpr int kMinPageShift = 4;    // pages of 16 ..
 constexpr int kMaxPageShift = 8;    // .. 256 slots, a power of two
 constexpr int kDecodeRows = 8;      // query rows per kv head (heads x tokens) of one decode tile
 constexpr int kDecodeCtasPerSm = 2;
+constexpr int kChunkRows = 256;     // query rows of one chunk tile (a pair of CTAs)
+constexpr int kChunkKeys = 128;     // keys of one chunk tile
 constexpr int kPagedTickets = 1024;  // at least the CTAs of a paged attention grid
 constexpr int kMaxSelectBlocks = 16384;   // blocks of one sequence that select_pages ranks (128 KiB of keys)
 
@@ -74,11 +76,15 @@ struct PagedSelectArgs {
     int32_t *selected;
 };
 
-// Workspace of the paged calls: two partial tiles per CTA of the attention grid,
-// or a ranking key per (sequence, kv head, block) of max_batch single-token rows.
-constexpr int64_t paged_partial_bytes(int num_sms) {
-    return (int64_t)2 * kDecodeCtasPerSm * num_sms * kDecodeRows * (kHeadDim * 4 + 8);
+// Workspace of the paged calls: two partial tiles per CTA (decode) or pair of CTAs
+// (chunks) of the attention grid, or a ranking key per (sequence, kv head, block) of max_batch single-token rows.
+constexpr int64_t paged_partial_rows(int num_sms, bool chunk) {
+    return chunk ? (int64_t)2 * (num_sms / 2) * kChunkRows : (int64_t)2 * kDecodeCtasPerSm * num_sms * kDecodeRows;
 }
+constexpr int64_t paged_partial_bytes(int num_sms) {
+    return paged_partial_rows(num_sms, true) * (kHeadDim * 4 + 8);
+}
+static_assert(kChunkRows >= 2 * kDecodeCtasPerSm * kDecodeRows, "the chunk kernel's partials are the larger");
 constexpr int64_t paged_rank_bytes(int64_t max_batch, int64_t num_kv_heads, int64_t max_context) {
     return max_batch * num_kv_heads * ((max_context >> kMinPageShift) + 1) * 8;
 }
@@ -87,6 +93,10 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s);
 // kmap / vmap: 5-D views of the pages with boxes of min(page, stage) rows (paged_map_rows).
 cudaError_t launch_paged_decode(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms,
                                 cudaStream_t s);
+// qmap: 4-D view {64 dims, heads, rows, 64-dim groups} of q_rot in boxes of group x 128 / group rows; kmap / vmap:
+// boxes of chunk_k_rows / chunk_v_rows slots (paged_api.cpp).
+cudaError_t launch_paged_chunk(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                               const PagedAttnArgs &a, cudaStream_t s);
 cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, cudaStream_t s);
 
 }  // namespace hd

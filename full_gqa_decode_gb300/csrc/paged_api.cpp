@@ -45,14 +45,15 @@ hd_status check_paged(const hd_ctx *ctx, int layer, const hd_paged_batch *b, con
 }
 
 // 5-D view {128 bytes of dims, slots, 128-byte column groups, kv heads, pages} of a pool's k or v, read in
-// boxes of `rows` slots x all columns: one copy lands as column groups of `rows` swizzled 128-byte rows.  Page
-// number num_pages lies outside: a copy of it fills zeros.
-bool encode_pages(CUtensorMap *map, const void *base, const hd_paged_cache &c, int num_kv_heads, int kv_type, int rows) {
+// boxes of `rows` slots x `groups` column groups, which land as column groups of `rows` swizzled 128-byte rows.
+// Page number num_pages lies outside: a copy of it fills zeros.
+bool encode_pages(CUtensorMap *map, const void *base, const hd_paged_cache &c, int num_kv_heads, int kv_type, int rows,
+                  int groups) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t es = (cuuint64_t)kv_elem_bytes(kv_type);
-    const cuuint64_t cols = (cuuint64_t)kv_box_cols(kv_type), groups = (cuuint64_t)kv_boxes_per_row(kv_type);
-    const cuuint64_t dims[5] = {cols, (cuuint64_t)c.page_size, groups, (cuuint64_t)num_kv_heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t cols = (cuuint64_t)kv_box_cols(kv_type), all = (cuuint64_t)kv_boxes_per_row(kv_type);
+    const cuuint64_t dims[5] = {cols, (cuuint64_t)c.page_size, all, (cuuint64_t)num_kv_heads, (cuuint64_t)c.num_pages};
     const cuuint64_t strides[4] = {kHeadDim * es, 128, (cuuint64_t)c.page_size * kHeadDim * es,
                                    (cuuint64_t)c.page_stride * es};
     const cuuint32_t box[5] = {(cuuint32_t)cols, (cuuint32_t)rows, (cuuint32_t)groups, 1, 1};
@@ -60,6 +61,20 @@ bool encode_pages(CUtensorMap *map, const void *base, const hd_paged_cache &c, i
     return fn(map, kv_type == KV_FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 4-D view {64 dims, query heads, rows, 64-dim groups} of the rotated queries in boxes of one kv head's heads x as
+// many tokens as make 128 rows; rows behind the last fill zeros.
+bool encode_queries(CUtensorMap *map, const void *q, int num_q_heads, int num_tokens, int group) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)num_q_heads, (cuuint64_t)num_tokens, kHeadDim / 64};
+    const cuuint64_t strides[3] = {kHeadDim * 2, (cuuint64_t)num_q_heads * kHeadDim * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)(kChunkRows / 2 / group), kHeadDim / 64};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -86,15 +101,32 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     a.window = ctx->layer_types[layer] == HD_SLIDING ? ctx->cfg.sliding_window : 0;
     a.kv_type = ctx->kv_type;
     a.drop_stage = ctx->drop_stage;
-    const int64_t rows = (int64_t)2 * kDecodeCtasPerSm * ctx->num_sms * kDecodeRows;
+    // More than eight rows per kv head in some sequence: the tensor-memory kernel, which also serves the call's
+    // single tokens; lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
+    const bool chunk = !selected && (int64_t)seqs.max_tokens * ctx->group > kDecodeRows;
+    const int64_t rows = paged_partial_rows(ctx->num_sms, chunk);
     a.part_o = reinterpret_cast<float *>(ctx->paged_ws);
     a.part_ml = reinterpret_cast<float2 *>(ctx->paged_ws + rows * kHeadDim * 4);
-    CUtensorMap km, vm;
-    const int box = std::min(c.page_size, kv_stage_keys(ctx->kv_type));
-    if (!encode_pages(&km, c.k, c, ctx->cfg.num_kv_heads, ctx->kv_type, box) ||
-        !encode_pages(&vm, c.v, c, ctx->cfg.num_kv_heads, ctx->kv_type, box))
-        return HD_ERR_CUDA;
-    const hd_status st = cuda_status(launch_paged_decode(&km, &vm, a, ctx->num_sms, static_cast<cudaStream_t>(stream)));
+    const int Hkv = ctx->cfg.num_kv_heads, all = kv_boxes_per_row(ctx->kv_type), ps = c.page_size;
+    const bool fp8 = ctx->kv_type == KV_FP8;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap km, vm, qm;
+    hd_status st;
+    if (chunk) {
+        const int krows = std::min(ps, kChunkKeys / 2), vrows = std::min(ps, kChunkKeys);
+        const int kgroups = fp8 || krows == kChunkKeys / 2 ? all : 1;
+        if (!encode_pages(&km, c.k, c, Hkv, ctx->kv_type, krows, kgroups) ||
+            !encode_pages(&vm, c.v, c, Hkv, ctx->kv_type, vrows, all / 2) ||
+            !encode_queries(&qm, q_rot, ctx->cfg.num_q_heads, seqs.num_tokens, ctx->group))
+            return HD_ERR_CUDA;
+        st = cuda_status(launch_paged_chunk(&qm, &km, &vm, a, s));
+    } else {
+        const int box = std::min(ps, kv_stage_keys(ctx->kv_type));
+        if (!encode_pages(&km, c.k, c, Hkv, ctx->kv_type, box, all) ||
+            !encode_pages(&vm, c.v, c, Hkv, ctx->kv_type, box, all))
+            return HD_ERR_CUDA;
+        st = cuda_status(launch_paged_decode(&km, &vm, a, ctx->num_sms, s));
+    }
     if (st == HD_OK) ++ctx->launches;
     return st;
 }

@@ -1,0 +1,841 @@
+// Attention of chunks of new tokens over a paged cache, on the 5th-generation
+// tensor cores.
+//
+//     S = Q K^T,  P = 2^(S log2(e)/16 - m),  O += P V
+//
+// with 256 query rows (heads x tokens of one kv head) and 128 keys at a time.
+// A tile costs 4 x 256 x 128 x 256 flops and moves 128 KiB of K and V, so for
+// long chunks the tensor cores bound it -- if the copies keep up: one SM alone
+// would need 64 bytes a clock of them, all SMs together more than L2 gives.  So
+// two SMs share a tile (a cluster of two CTAs, cta_group::2 MMAs): each holds
+// 128 of the query rows, the scores of its rows, and half of every operand tile
+// -- 64 of the 128 keys for S, 128 of the 256 dims for O -- and the pair reads
+// K and V once.
+//
+// Tensor memory (512 columns in each CTA): scores in two buffers of 128
+// columns, the output of 256.  P, in 16 bits, takes the place of the scores
+// that it came from and is the A operand of the second product.  The MMA warp
+// runs one tile ahead: S(i) is issued before O += P(i-1) V(i-1), so the softmax
+// of one tile overlaps the products of its neighbours, across items too.
+//
+// Roles of a CTA: eight softmax warps, two threads a row (64 scores each,
+// maxima exchanged through shared memory by pairs of warps); a copy warp; the
+// MMA warp (only the first CTA's issues; its barriers collect the arrivals of
+// both CTAs); and stage warps, which hand a landed stage on to the MMA warp:
+// with bf16 pages one warp, which only zeroes the V rows of positions that no
+// row sees (they may hold NaN); with E4M3 pages four warps, which convert the
+// codes to f16 (exact) in the layout of the MMAs.
+//
+// Rows keep the reference m of their weights until a score passes it by 8 (in
+// log2 units), and only then is the output in tensor memory rescaled: weights
+// stay below 2^8, exact in range for bf16, and f16 weights (E4M3 pages) are
+// lifted by another 2^7 away from f16's subnormals.  Sums and maxima are fp32;
+// the rounding of P to 16 bits (2^-9, f16 2^-12 of each weight) is below the
+// output's own once summed.
+#include "paged_rows.cuh"
+
+namespace hd {
+namespace {
+
+constexpr int kTileRows = kChunkRows, kCtaRows = kTileRows / 2, kTileKeys = kChunkKeys, kKeyShift = 7;
+constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kStageWarp = kSoftWarps + 2;
+__host__ __device__ constexpr int stage_warps(int kv) { return kv == KV_FP8 ? 4 : 1; }
+__host__ __device__ constexpr int chunk_threads(int kv) { return (kStageWarp + stage_warps(kv)) * 32; }
+constexpr int kQBytes = kCtaRows * kHeadDim * 2;      // 64 KiB
+constexpr int kSlotBytes = 32 * 1024;                 // this CTA's half of a K or V tile in 16 bits
+constexpr int kRawBytes = 16 * 1024;                  // ... in E4M3 codes
+__host__ __device__ constexpr int num_slots(int kv) { return kv == KV_FP8 ? 3 : 5; }
+constexpr int kRawSlots = 4;
+constexpr int kRingBytes = 160 * 1024;
+static_assert(5 * kSlotBytes == kRingBytes && 3 * kSlotBytes + kRawSlots * kRawBytes == kRingBytes, "ring");
+constexpr int kXmOff = kQBytes + kRingBytes;          // [2][2][128] floats: maxima of both halves, by tile parity
+constexpr int kQexpOff = kXmOff + 2 * 2 * kCtaRows * 4;   // [4][128] bytes: E4M3 pages, exponents of the rows' q
+constexpr int kChunkBarOff = kQexpOff + 4 * kCtaRows;
+constexpr int kChunkBars = 32;
+constexpr int kChunkMiscOff = kChunkBarOff + kChunkBars * 8;
+constexpr int kChunkSmem = kChunkMiscOff + 64;
+constexpr int kMaxPairs = 96;                         // pieces of an item a warp can weigh in registers
+constexpr int kMinTiles = 2;                          // shortest share of a pair
+constexpr float kRescale = 8.f;
+constexpr uint32_t kTmemCols = 512, kOutCol = 256;
+
+// Barriers (index into the barrier area).
+enum : int {
+    BAR_FULL = 0,      // [5] a slot's (E4M3: a raw slot's) copies have landed in this CTA
+    BAR_READY = 5,     // [5] first CTA: both CTAs' halves of a slot are ready for the MMAs
+    BAR_EMPTY = 10,    // [5] the MMAs that read a slot are complete
+    BAR_RAW_FREE = 15, // [4] a raw slot has been converted
+    BAR_Q_FULL = 19,   // the query rows have landed in this CTA
+    BAR_Q_READY = 20,  // first CTA: both CTAs' query rows are ready
+    BAR_Q_EMPTY = 21,  // the MMAs that read the query rows are complete
+    BAR_S = 22,        // [2] scores are complete
+    BAR_P = 24,        // [2] first CTA: the weights of both CTAs are written
+    BAR_PV = 26,       // [2] a tile's output product is complete (by tile parity: a wait is never two phases behind)
+    BAR_O_FREE = 28,   // first CTA: both CTAs have read an item's output
+};
+
+struct ChunkTile {
+    int t0, nt, lo, hi, u0, units;   // as in the decode kernel: tokens, visible positions of any of them, key tiles
+};
+__device__ __forceinline__ ChunkTile make_chunk_tile(const PagedAttnArgs &a, const SeqSpan &q, int tile) {
+    ChunkTile t;
+    const int tt = kTileRows / a.group;
+    t.t0 = tile * tt;
+    t.nt = min(tt, q.n - t.t0);
+    t.hi = q.ctx + t.t0 + t.nt;
+    t.lo = a.window ? max(0, q.ctx + t.t0 - a.window + 1) : 0;
+    t.u0 = t.lo >> kKeyShift;
+    t.units = ((t.hi + kTileKeys - 1) >> kKeyShift) - t.u0;
+    return t;
+}
+__device__ __forceinline__ int num_chunk_tiles(const PagedAttnArgs &a, int n) {
+    const int tt = kTileRows / a.group;
+    return (n + tt - 1) / tt;
+}
+
+// A walk over the tiles of a pair's share, item by item.
+struct Walk {
+    int b, tile, h, u;   // u: key tile within the item
+    SeqSpan q;
+    ChunkTile t;
+    int seg_end;         // key tile of the item where this pair's share of it ends
+    long long left;      // tiles of the share from this one on
+    bool fresh;          // first tile of a segment
+
+    __device__ void start(const PagedAttnArgs &a, const int *at, long long share) {
+        b = at[0];
+        tile = at[1];
+        h = at[2];
+        u = at[3];
+        int bit;
+        q = seq_span(a.seqs, b, &bit);
+        t = make_chunk_tile(a, q, tile);
+        left = share;
+        seg_end = (int)min((long long)t.units, u + left);
+        fresh = true;
+    }
+    __device__ bool last() const { return u + 1 == seg_end; }
+    __device__ int key0() const { return (t.u0 + u) << kKeyShift; }
+    __device__ void next(const PagedAttnArgs &a) {   // only while left > 1
+        --left;
+        fresh = false;
+        if (++u < seg_end) return;
+        u = 0;
+        fresh = true;
+        if (++h == a.num_kv_heads) {
+            h = 0;
+            if (++tile == num_chunk_tiles(a, q.n)) {
+                tile = 0;
+                int bit;
+                do {
+                    q = seq_span(a.seqs, ++b, &bit);
+                } while (q.n == 0 && b + 1 < a.seqs.batch);
+            }
+            t = make_chunk_tile(a, q, tile);
+        }
+        seg_end = (int)min((long long)t.units, left);
+    }
+};
+
+// Position in a ring of slots: index and the parity of its current round.
+template <int N>
+struct RingPos {
+    int st = 0;
+    uint32_t ph = 0;   // parity of the round that fills the slot
+    bool first = true;
+    __device__ void step() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1;
+            first = false;
+        }
+    }
+};
+
+// ------------------------------------------------ cluster and pair-MMA PTX --
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits with the usual time limit; after one has run out (`dead`) it waits no more.
+__device__ __forceinline__ void wait_thread(uint64_t *bar, uint32_t parity, bool &dead, int32_t *err) {
+    if (dead || mbar_try_wait_cluster(bar, parity)) return;
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+    }
+    dead = true;
+    atomicOr(err, HD_DEVERR_WAIT_TIMEOUT);
+}
+// The same for a whole warp, whose lanes go on together.
+__device__ __forceinline__ void wait_warp(uint64_t *bar, uint32_t parity, bool &dead, int32_t *err) {
+    wait_thread(bar, parity, dead, err);
+    dead = __any_sync(0xffffffffu, dead);
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void pair_alloc(uint32_t *dst_smem) {   // whole warp, in both CTAs
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+// D (+)= A B^T over both CTAs: A from shared memory (first form) or tensor memory.
+__device__ __forceinline__ void pair_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs once all MMAs issued so far are complete.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Instruction descriptor for M = 256 rows of the pair: fp32 accumulator, bf16 or f16 operands, A K-major.
+__host__ __device__ constexpr uint32_t pair_idesc(int n, bool bf16, int b_mn) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTileRows >> 4) << 24);
+}
+
+struct ChunkMaps {
+    CUtensorMap q, k, v;
+};
+
+template <int KV>
+__global__ void __launch_bounds__(chunk_threads(KV), 1)
+    paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr bool kFp8 = KV == KV_FP8;
+    constexpr int S = num_slots(KV), kStage = stage_warps(KV);
+    uint8_t *ring = smem + kQBytes, *raw = ring + 3 * kSlotBytes;
+    float *xm = reinterpret_cast<float *>(smem + kXmOff);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChunkBarOff);
+    int *misc = reinterpret_cast<int *>(smem + kChunkMiscOff);
+    uint32_t *taddr_s = reinterpret_cast<uint32_t *>(misc + 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const PagedSeqs &sq = a.seqs;
+    int32_t *err = sq.err;
+
+    if (tid == 0) {
+        for (int i = 0; i < 5; ++i) {
+            mbar_init(&bar[BAR_FULL + i], 1);
+            mbar_init(&bar[BAR_READY + i], 2 * kStage);
+            mbar_init(&bar[BAR_EMPTY + i], 1);
+        }
+        for (int i = 0; i < kRawSlots; ++i) mbar_init(&bar[BAR_RAW_FREE + i], kStage);
+        mbar_init(&bar[BAR_Q_FULL], 1);
+        mbar_init(&bar[BAR_Q_READY], 2 * kStage);
+        mbar_init(&bar[BAR_Q_EMPTY], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[BAR_S + i], 1);
+            mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
+            mbar_init(&bar[BAR_PV + i], 1);
+        }
+        mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
+        fence_mbar_init();
+    }
+    // All key tiles of the call, and this pair's share.
+    const int per = (sq.batch + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int b_lo = min(tid * per, sq.batch), b_hi = min(b_lo + per, sq.batch);
+    long long mine = 0;
+    int bad = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        int bit;
+        const SeqSpan q = seq_span(sq, b, &bit);
+        bad |= bit;
+        const int tiles = num_chunk_tiles(a, q.n);
+        for (int i = 0; i < tiles; ++i) mine += (long long)make_chunk_tile(a, q, i).units * a.num_kv_heads;
+    }
+    bad = __syncthreads_or(bad);
+    long long T;
+    const long long before = block_prefix(mine, reinterpret_cast<long long *>(xm), &T);
+    if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
+    const int n = (int)min((long long)pairs, max(T / kMinTiles, 1LL));
+    if (pair >= n || T == 0) return;   // both CTAs of the pair
+    const long long x0 = T * pair / n, x1 = T * (pair + 1) / n;
+    if (before <= x0 && x0 < before + mine) {
+        long long rem = x0 - before;
+        bool found = false;
+        for (int b = b_lo; b < b_hi && !found; ++b) {
+            int bit;
+            const SeqSpan q = seq_span(sq, b, &bit);
+            const int tiles = num_chunk_tiles(a, q.n);
+            for (int i = 0; i < tiles && !found; ++i) {
+                const int u = make_chunk_tile(a, q, i).units;
+                if (rem < (long long)u * a.num_kv_heads) {
+                    misc[0] = b;
+                    misc[1] = i;
+                    misc[2] = (int)(rem / u);
+                    misc[3] = (int)(rem % u);
+                    found = true;
+                }
+                rem -= (long long)u * a.num_kv_heads;
+            }
+        }
+    }
+    if (warp == kMmaWarp) pair_alloc(taddr_s);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // the peer's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = *taddr_s;
+    const long long N = x1 - x0;
+    Walk w;
+    w.start(a, misc, N);
+    bool dead = false;
+    const int ps = 1 << sq.page_shift;
+
+    if (warp == kCopyWarp) {
+        // ---- copies: K(0), K(1), V(0), K(2), V(1), ... ----
+        const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
+        const int tok = kCtaRows / a.group;
+        // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
+        auto pages_of = [&](const Walk &x) {
+            const int pos = x.key0() + 16 * (lane & 7), first = pos & ~(ps - 1);
+            int page = sq.num_pages;
+            if (first < x.t.hi && first + ps > x.t.lo) {
+                page = sq.table[(size_t)x.b * sq.table_stride + (pos >> sq.page_shift)];
+                if (page < 0 || page >= sq.num_pages) {
+                    atomicOr(err, HD_DEVERR_PAGE);
+                    page = sq.num_pages;
+                }
+            }
+            return page;
+        };
+        int pg = pages_of(w), pg_v = 0, key_v = 0, h_v = 0;
+        RingPos<kFp8 ? kRawSlots : S> pos;
+        int issued = 0;
+        uint32_t seg = 0;
+        for (long long i = 0; i <= N; ++i) {
+            int pg_next = 0;
+            Walk nx = w;
+            if (i + 1 < N) {
+                nx.next(a);
+                pg_next = pages_of(nx);
+            }
+            if (i < N) {
+                if (w.fresh) {
+                    if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
+                    if (lane == 0 && !dead) {
+                        mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
+                        tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h * a.group, w.q.row0 + w.t.t0 + rank * tok, 0);
+                    }
+                    ++seg;
+                }
+            }
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
+                if (kind == 0 ? i >= N : i == 0) continue;
+                if (!pos.first) wait_warp(&bar[(kFp8 ? BAR_RAW_FREE : BAR_EMPTY) + pos.st], pos.ph ^ 1, dead, err);
+                uint8_t *dst = kFp8 ? raw + pos.st * kRawBytes : ring + pos.st * kSlotBytes;
+                uint64_t *full = &bar[BAR_FULL + pos.st];
+                const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
+                if (!drop && lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kRawBytes : kSlotBytes);
+                __syncwarp();
+                const int key0 = kind == 0 ? w.key0() + 64 * rank : key_v;
+                const int head = kind == 0 ? w.h : h_v, src_pg = kind == 0 ? pg : pg_v;
+                int run, col = 0, group16, total;
+                uint32_t off;
+                if (kind == 0) {
+                    // bf16 pages of fewer than 64 slots: a copy per column group, so that the 64 keys' rows of a
+                    // group lie together as the MMA wants them.
+                    const bool split = !kFp8 && rk_shift < 6;
+                    run = split ? lane >> 2 : lane;
+                    col = split ? lane & 3 : 0;
+                    total = (64 >> rk_shift) * (split ? 4 : 1);
+                    off = split ? col * 8192 + (run << rk_shift) * 128
+                                : (uint32_t)(run << rk_shift) * (kFp8 ? kHeadDim : 2 * kHeadDim);
+                    group16 = 4 * rank + ((run << rk_shift) >> 4);
+                } else {
+                    run = lane;
+                    total = 128 >> rv_shift;
+                    off = (uint32_t)(run << rv_shift) * (kFp8 ? 128 : 256);
+                    col = kFp8 ? rank : 2 * rank;
+                    group16 = (run << rv_shift) >> 4;
+                }
+                const int page = __shfl_sync(0xffffffffu, src_pg, group16 & 7);
+                if (!drop && lane < total) {
+                    const int slot = (key0 + (run << (kind == 0 ? rk_shift : rv_shift))) & (ps - 1);
+                    tma_load_5d(dst + off, kind == 0 ? &maps.k : &maps.v, full, 0, slot, col, head, page);
+                }
+                ++issued;
+                pos.step();
+            }
+            pg_v = pg;
+            key_v = w.key0();
+            h_v = w.h;
+            pg = pg_next;
+            w = nx;
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- products: S(0), S(1), O(0), S(2), O(1), ... ----
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t kIdS = pair_idesc(128, !kFp8, 0), kIdO = pair_idesc(256, !kFp8, 1);
+            const int rv_shift = kFp8 ? 7 : min(sq.page_shift, 7);
+            const uint64_t qd0 = umma_desc(smem_u32(smem), 16, 1024, 2);
+            const uint64_t kd0 = umma_desc(smem_u32(ring), 16, 1024, 2);
+            const uint64_t vd0 = umma_desc(smem_u32(ring), 128u << rv_shift, 1024, 2);
+            RingPos<S> pos;
+            uint32_t seg = 0, oseg = 0;
+            bool fresh_o = true;
+            for (long long i = 0; i <= N; ++i) {
+                const bool fresh_s = w.fresh, last_s = w.last();
+                if (i < N) {
+                    if (fresh_s) {
+                        wait_thread(&bar[BAR_Q_READY], seg & 1, dead, err);
+                        ++seg;
+                    }
+                    const int st = pos.st;
+                    wait_thread(&bar[BAR_READY + st], pos.ph, dead, err);
+                    pos.step();
+                    tc_fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * kSlotBytes >> 4);
+                    const uint32_t d = tmem + (uint32_t)(i & 1) * 128;
+#pragma unroll
+                    for (int kk = 0; kk < 16; ++kk)
+                        pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                    kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                    pair_commit(&bar[BAR_EMPTY + st]);
+                    pair_commit(&bar[BAR_S + (i & 1)]);
+                    if (last_s) pair_commit(&bar[BAR_Q_EMPTY]);
+                }
+                if (i > 0) {
+                    const long long j = i - 1;
+                    if (fresh_o) {
+                        if (oseg) wait_thread(&bar[BAR_O_FREE], (oseg - 1) & 1, dead, err);
+                        ++oseg;
+                    }
+                    const int st = pos.st;
+                    wait_thread(&bar[BAR_READY + st], pos.ph, dead, err);
+                    pos.step();
+                    wait_thread(&bar[BAR_P + (j & 1)], (uint32_t)(j >> 1) & 1, dead, err);
+                    tc_fence_after();
+                    const uint32_t p = tmem + (uint32_t)(j & 1) * 128;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const uint32_t run = (uint32_t)(16 * t) >> rv_shift, in = (uint32_t)(16 * t) & ((1u << rv_shift) - 1);
+                        const uint32_t off = (uint32_t)st * kSlotBytes + (run << rv_shift) * 256 + in * 128;
+                        pair_mma_ts(tmem + kOutCol, p + 8 * t, vd0 + (uint64_t)(off >> 4), kIdO, !(fresh_o && t == 0));
+                    }
+                    pair_commit(&bar[BAR_EMPTY + st]);
+                    pair_commit(&bar[BAR_PV + (j & 1)]);
+                }
+                fresh_o = fresh_s;
+                if (i + 1 < N) w.next(a);
+            }
+        }
+    } else if (warp >= kStageWarp) {
+        // ---- stages: hand K(0), K(1), V(0), ... on to the MMA warp ----
+        const int st_tid = tid - kStageWarp * 32;
+        const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
+        const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
+        RingPos<S> pos;
+        RingPos<kRawSlots> raw_pos;
+        uint32_t seg = 0;
+        int key_v = 0, lo_v = 0, hi_v = 0;
+        for (long long i = 0; i <= N; ++i) {
+            if (i < N && w.fresh) {
+                wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
+                if (kFp8) {
+                    // A thread's row of q in f16, scaled by the power of two that brings its largest value below 2
+                    // (and by the sign of the K scale); the softmax multiplies the scores back.
+                    const int row = st_tid;
+                    uint8_t *qrow = smem + row * 128;
+                    uint32_t top = 0;
+#pragma unroll 8
+                    for (int c = 0; c < 32; ++c) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
+                        const uint32_t cw[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = max(top, max(cw[j] & 0xFFFFu, cw[j] >> 16));
+                    }
+                    const int ex = min(max((int)(top >> 7), 1), 253);
+                    const float down = copysignf(__uint_as_float((uint32_t)(254 - ex) << 23), a.k_scale[w.h]);
+#pragma unroll 8
+                    for (int c = 0; c < 32; ++c) {
+                        uint4 *at = reinterpret_cast<uint4 *>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
+                        uint4 x = *at;
+                        auto half2 = [&](uint32_t v) {
+                            return pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
+                        };
+                        *at = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
+                    }
+                    smem[kQexpOff + (seg & 3) * kCtaRows + row] = (uint8_t)ex;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(q_ready);
+                ++seg;
+            }
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {
+                if (kind == 0 ? i >= N : i == 0) continue;
+                uint8_t *slot = ring + pos.st * kSlotBytes;
+                if (kFp8) {
+                    const uint8_t *src = raw + raw_pos.st * kRawBytes;
+                    wait_warp(&bar[BAR_FULL + raw_pos.st], raw_pos.ph, dead, err);
+                    if (!pos.first) wait_warp(&bar[BAR_EMPTY + pos.st], pos.ph ^ 1, dead, err);
+                    // 1024 chunks of 16 codes: 64 keys x 16 (K), 128 keys x 8 (V); a warp's lanes take 32 rows of
+                    // one chunk column, which the swizzle spreads over all banks.
+#pragma unroll
+                    for (int c0 = 0; c0 < 8; ++c0) {
+                        const int unit = c0 * (kStage * 32) + st_tid;
+                        const int row = kind == 0 ? unit & 63 : unit & 127, c = kind == 0 ? unit >> 6 : unit >> 7;
+                        const uint32_t at = kind == 0 ? (uint32_t)(row >> rk_shift << rk_shift) * kHeadDim +
+                                                            (uint32_t)(c >> 3) * (128u << rk_shift) +
+                                                            (uint32_t)(row & ((1 << rk_shift) - 1)) * 128
+                                                      : (uint32_t)row * 128;
+                        uint4 x = *reinterpret_cast<const uint4 *>(src + at + (((c & 7) ^ (row & 7)) << 4));
+                        if (kind == 1 && (key_v + row < lo_v || key_v + row >= hi_v)) x = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            f[2 * j] = e4m3x2_to_f16x2((uint16_t)(cw[j] & 0xFFFFu));
+                            f[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(cw[j] >> 16));
+                        }
+                        uint8_t *dst = slot + (uint32_t)(c >> 2) * (kind == 0 ? 8192u : 16384u) + (uint32_t)row * 128;
+                        *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3)) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
+                } else {
+                    wait_warp(&bar[BAR_FULL + pos.st], pos.ph, dead, err);
+                    if (kind == 1 && (key_v < lo_v || key_v + kTileKeys > hi_v)) {
+                        // Rows of positions that no query row sees: zero, whatever their slots hold.
+                        for (int r = 0; r < kTileKeys; ++r) {
+                            if (key_v + r >= lo_v && key_v + r < hi_v) continue;
+                            const uint32_t at = (uint32_t)(r >> rv_shift << rv_shift) * 256 +
+                                                (uint32_t)(r & ((1 << rv_shift) - 1)) * 128 +
+                                                (lane >> 3 & 1) * (128u << rv_shift) + (lane & 7) * 16;
+                            if (lane < 16) *reinterpret_cast<uint4 *>(slot + at) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kFp8) mbar_arrive(&bar[BAR_RAW_FREE + raw_pos.st]);
+                    mbar_arrive_remote(ready0 + 8 * pos.st);
+                }
+                raw_pos.step();
+                pos.step();
+            }
+            key_v = w.key0();
+            lo_v = w.t.lo;
+            hi_v = w.t.hi;
+            if (i + 1 < N) w.next(a);
+        }
+    } else {
+        // ---- softmax: thread (row, half of the tile's keys) ----
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // lane 32 (warp % 4) in the upper half-word
+        const uint32_t p_bar = dsmem_addr(&bar[BAR_P], 0), o_free = dsmem_addr(&bar[BAR_O_FREE], 0);
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
+        auto soft_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
+        const float lift = kFp8 ? 7.f : 0.f;
+        float m = -INFINITY, l = 0.f, scale = kQScale;
+        int hi_pos = 0, lo_pos = 0, all_hi = 0, all_lo = 0, rows_here = 0;
+        long long item0 = x0 - w.u;   // first tile of the current item in the call's order
+        int seg_u0 = 0;
+        uint32_t seg = 0;
+        for (long long g = 0; g < N; ++g) {
+            if (w.fresh) {
+                m = -INFINITY;
+                l = 0.f;
+                const int r = rank * kCtaRows + row;
+                hi_pos = w.q.ctx + w.t.t0 + r / a.group;
+                lo_pos = a.window ? hi_pos - a.window + 1 : 0;
+                all_hi = w.q.ctx + w.t.t0;
+                all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;
+                rows_here = w.t.nt * a.group - rank * kCtaRows;   // valid rows of this CTA
+                item0 = x0 + g - w.u;
+                seg_u0 = w.u;
+            }
+            const bool idle = (warp & 3) * 32 >= rows_here;   // none of this warp's rows exists
+            const uint32_t buf = lanes + (uint32_t)(g & 1) * 128;
+            wait_warp(&bar[BAR_S + (g & 1)], (uint32_t)(g >> 1) & 1, dead, err);
+            if (w.fresh) {
+                if (kFp8) {
+                    const uint32_t ex = smem[kQexpOff + (seg & 3) * kCtaRows + row];
+                    scale = fmaxf(__uint_as_float(ex << 23) * fabsf(a.k_scale[w.h] * kQScale), 1e-37f);
+                }
+                ++seg;
+            }
+            if (!idle) {
+                tc_fence_after();
+                float s[64];
+                tmem_ld32(buf + half * 64, *reinterpret_cast<float(*)[32]>(s));
+                tmem_ld32(buf + half * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+                const int key0 = w.key0() + half * 64;
+                if (key0 < all_lo || key0 + 63 > all_hi) {
+                    const int from = lo_pos - key0, to = hi_pos - key0;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) s[i] = i >= from && i <= to ? s[i] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float *x = xm + (g & 1) * 2 * kCtaRows;
+                x[half * kCtaRows + row] = top;
+                pair_sync();
+                top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
+                top *= scale;
+                float alpha = 1.f;
+                if (top > m + kRescale) {   // also a row's first key: m = -inf
+                    alpha = fast_exp2(m - top);   // m = -inf: 0
+                    m = top;
+                    l *= alpha;
+                }
+                if (w.u != seg_u0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    wait_warp(&bar[BAR_PV + ((g - 1) & 1)], (uint32_t)((g - 1) >> 1) & 1, dead, err);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        float o[32];
+                        uint32_t ow[32];
+                        tmem_ld32(lanes + kOutCol + half * 128 + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ow[i] = __float_as_uint(o[i] * alpha);
+                        tmem_st32(lanes + kOutCol + half * 128 + c, ow);
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m - lift;
+                uint32_t pw[32];
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float p0 = fast_exp2(fmaf(s[2 * i], scale, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], scale, -ref));
+                    sum[i & 1] += p0;
+                    sum[2 + (i & 1)] += p1;
+                    pw[i] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st32(buf + half * 32, pw);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(p_bar + 8 * (uint32_t)(g & 1));
+
+            if (w.last()) {
+                // ---- the segment's output ----
+                float *x = xm + ((g + 1) & 1) * 2 * kCtaRows;
+                if (!idle) {
+                    x[half * kCtaRows + row] = l;
+                    pair_sync();
+                    l += x[(half ^ 1) * kCtaRows + row];
+                    pair_sync();
+                }
+                wait_warp(&bar[BAR_PV + (g & 1)], (uint32_t)(g >> 1) & 1, dead, err);
+                tc_fence_after();
+                const bool whole = seg_u0 == 0 && w.seg_end == w.t.units;
+                const bool live = row < rows_here;
+                const int r = rank * kCtaRows + row;
+                const float ml_m = m - lift;
+                const int slot = seg_u0 == 0 ? 2 * pair + 1 : 2 * pair;
+                const size_t prow = (size_t)slot * kTileRows + r;
+                const float vscale = kFp8 ? a.v_scale[w.h] : 1.f;
+                const int head = w.h * a.group + r % a.group;
+                const size_t orow = (size_t)(w.q.row0 + w.t.t0 + r / a.group) * a.num_q_heads + head;
+                float f = 1.f;
+                if (live) {
+                    if (whole) {
+                        float lse;
+                        f = row_factor(a, orow, head, ml_m, l, vscale, &lse);
+                        if (half == 0) a.lse[orow] = lse;
+                    } else if (half == 0) {
+                        a.part_ml[prow] = make_float2(ml_m, l);
+                    }
+                }
+                if (!idle) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        float o[32];
+                        tmem_ld32(lanes + kOutCol + half * 128 + c, o);
+                        if (!live) continue;
+                        if (whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + half * 128 + c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] = make_uint4(pack_bf16(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                                                    pack_bf16(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16(o[8 * i + 6] * f, o[8 * i + 7] * f));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * kHeadDim + half * 128 + c);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(o_free);
+                if (!whole) {
+                    // The last of the item's pieces to arrive (for this CTA's rows) merges them.
+                    const int i0 = cta_of_unit(item0, T, n), nseg = cta_of_unit(item0 + w.t.units - 1, T, n) - i0 + 1;
+                    __threadfence();
+                    soft_sync();
+                    if (tid == 0) misc[4] = atomicAdd(&a.tickets[2 * i0 + rank], 1) == nseg - 1;
+                    soft_sync();
+                    if (misc[4]) {
+                        __threadfence();
+                        for (int rr = warp; rr < min(rows_here, kCtaRows); rr += kSoftWarps) {
+                            auto piece = [&](int j) {
+                                return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kTileRows + rank * kCtaRows + rr;
+                            };
+                            float2 ml[3];
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                const int j = lane + 32 * k;
+                                ml[k] = j < nseg ? __ldcg(&a.part_ml[piece(j)]) : make_float2(-INFINITY, 0.f);
+                                top = fmaxf(top, ml[k].x);
+                            }
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            float sum = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                ml[k].x = part_weight(ml[k].x, top);
+                                sum += ml[k].x * ml[k].y;
+                            }
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+                            for (int j = 0; j < nseg; ++j) {
+                                const float wt = __shfl_sync(0xffffffffu, j < 32 ? ml[0].x : j < 64 ? ml[1].x : ml[2].x, j & 31);
+                                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + piece(j) * kHeadDim) + 2 * lane;
+                                const float4 p0 = __ldcg(src), p1 = __ldcg(src + 1);
+                                v0.x = fmaf(wt, p0.x, v0.x); v0.y = fmaf(wt, p0.y, v0.y);
+                                v0.z = fmaf(wt, p0.z, v0.z); v0.w = fmaf(wt, p0.w, v0.w);
+                                v1.x = fmaf(wt, p1.x, v1.x); v1.y = fmaf(wt, p1.y, v1.y);
+                                v1.z = fmaf(wt, p1.z, v1.z); v1.w = fmaf(wt, p1.w, v1.w);
+                            }
+                            const int rt = rank * kCtaRows + rr, hd_ = w.h * a.group + rt % a.group;
+                            const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + rt / a.group) * a.num_q_heads + hd_;
+                            float lse;
+                            const float ff = row_factor(a, out_row, hd_, top, sum, vscale, &lse);
+                            if (lane == 0) a.lse[out_row] = lse;
+                            reinterpret_cast<uint4 *>(a.out + out_row * kHeadDim)[lane] =
+                                make_uint4(pack_bf16(v0.x * ff, v0.y * ff), pack_bf16(v0.z * ff, v0.w * ff),
+                                           pack_bf16(v1.x * ff, v1.y * ff), pack_bf16(v1.z * ff, v1.w * ff));
+                        }
+                        if (tid == 0) a.tickets[2 * i0 + rank] = 0;
+                    }
+                    soft_sync();
+                }
+            }
+            if (g + 1 < N) w.next(a);
+        }
+    }
+    __syncwarp();
+    // No CTA leaves while its peer's MMAs or arrivals may still reach it.
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == kMmaWarp) pair_dealloc(tmem);
+}
+
+template <int KV>
+cudaError_t chunk_setup(int *pairs) {
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> limit[64];
+    int dev = 0;
+    if (!done_on_device(done, &dev)) {
+        cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {2, 1, 1};
+        cfg.gridDim = dim3(2 * kMaxPairs);
+        cfg.blockDim = dim3(chunk_threads(KV));
+        cfg.dynamicSmemBytes = kChunkSmem;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, paged_chunk_kernel<KV>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) limit[dev].store(n, std::memory_order_relaxed);
+        *pairs = n;
+        mark_done_on_device(done, dev);
+        return cudaSuccess;
+    }
+    *pairs = limit[dev].load(std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+template <int KV>
+cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStream_t s) {
+    int pairs = 0;
+    cudaError_t e = chunk_setup<KV>(&pairs);
+    if (e != cudaSuccess) return e;
+    if (pairs > kMaxPairs) pairs = kMaxPairs;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {2, 1, 1};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(chunk_threads(KV));
+    cfg.dynamicSmemBytes = kChunkSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<KV>, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                               const PagedAttnArgs &a, cudaStream_t s) {
+    ChunkMaps maps{*qmap, *kmap, *vmap};
+    return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8>(maps, a, s) : launch_chunk<KV_BF16>(maps, a, s);
+}
+
+}  // namespace hd

@@ -18,8 +18,10 @@
 // below 2^-14 of that lose bits under 2^-25 of the largest, less than the fp32
 // sum of the products does.  P is rounded to the cache's 16-bit type for the
 // second product (2^-9 or 2^-12 of each weight, below the output's own
-// rounding once summed); sums and maxima stay in fp32.
-#include "paged_sched.cuh"
+// rounding once summed); f16 weights are taken 2^15 times as large, which the
+// division by their sum undoes, so that small ones stay clear of f16's
+// subnormals.  Sums and maxima stay in fp32.
+#include "paged_rows.cuh"
 
 namespace hd {
 namespace {
@@ -143,7 +145,7 @@ struct DecodeBf16 {
 
     __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
                             int vhi, bool full, int lane) {
-        const int gid = lane >> 2, t4 = lane & 3, lr = lane & 7, lsub = lane >> 3;
+        const int t4 = lane & 3, lr = lane & 7, lsub = lane >> 3;
         const uint32_t sw0 = (uint32_t)(lsub ^ lr) << 4, sw1 = (uint32_t)((4 + lsub) ^ lr) << 4;
         const uint32_t kb = smem_u32(kst) + base + lr * 128, vb = smem_u32(vst) + base + lr * 128;
         // Two accumulators (even / odd k-steps) halve the dependent MMA chain.
@@ -224,6 +226,7 @@ struct DecodeBf16 {
 // product as it is.
 struct DecodeE4m3 {
     static constexpr int kKeys = 16;
+    static constexpr float kLift = 15.f;
     uint32_t qb[16][2];
     float o[16][4];            // O^T tile mt: dims 128 (mt / 8) + 16 gid + 2 (mt % 8) (+ 1) x rows 2 t4 (+ 1)
     float m_run[2], l_run[2];  // rows 2 t4 + e
@@ -301,8 +304,8 @@ struct DecodeE4m3 {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float mn = fmaxf(m_run[e], mx);
             alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
-            p[e] = v0 ? fast_exp2(x0 - mn) : 0.f;
-            p[2 + e] = v1 ? fast_exp2(x1 - mn) : 0.f;
+            p[e] = v0 ? fast_exp2(x0 - (mn - kLift)) : 0.f;
+            p[2 + e] = v1 ? fast_exp2(x1 - (mn - kLift)) : 0.f;
             l_run[e] = fmaf(l_run[e], alpha[e], p[e] + p[2 + e]);
             m_run[e] = mn;
         }
@@ -353,7 +356,7 @@ struct DecodeE4m3 {
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (lane < 4) {
-                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e];
+                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
                 ml[(kWarps + warp) * kDecodeRows + 2 * lane + e] = l;
             }
         }
@@ -376,44 +379,14 @@ template <> struct DecodeConsumer<KV_BF16> { using T = DecodeBf16; };
 template <> struct DecodeConsumer<KV_FP8> { using T = DecodeE4m3; };
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
-// exp2(x - m) of a partial's maximum x, 0 for a partial that saw no key.
-__device__ __forceinline__ float part_weight(float x, float m) { return x == -INFINITY ? 0.f : fast_exp2(x - m); }
-
-__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w,
-                                            int v) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// Rows of a bad sequence: NaN, as the decode calls give.
-__device__ __forceinline__ void fill_bad_rows(const PagedAttnArgs &a, int first, int stride) {
-    for (int b = first; b < a.seqs.batch; b += stride) {
-        int bit, rows = 0;
-        const SeqSpan q = seq_span(a.seqs, b, &bit, &rows);
-        if (!bit) continue;
-        if (threadIdx.x == 0) atomicOr(a.seqs.err, bit);
-        const size_t n = (size_t)rows * a.num_q_heads, r0 = (size_t)q.row0 * a.num_q_heads;
-        for (size_t i = threadIdx.x; i < n * (kHeadDim / 2); i += blockDim.x)
-            reinterpret_cast<uint32_t *>(a.out)[r0 * (kHeadDim / 2) + i] = 0x7FFF7FFFu;
-        for (size_t i = threadIdx.x; i < n; i += blockDim.x) a.lse[r0 + i] = __int_as_float(0x7FC00000);
-    }
-}
-
 // Writes row r of a finished tile (thread's four dims d..d+3 of its
 // unnormalised output, log2-unit maximum m and sum l).
 __device__ __forceinline__ void finish_row(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int r, int d,
                                            float4 v, float m, float l, float vscale) {
-    const size_t row = (size_t)(q.row0 + t.t0 + r / a.group) * a.num_q_heads + h * a.group + r % a.group;
     const int head = h * a.group + r % a.group;
-    // A row that sees no key (selected lists only) gives 0 and lse -inf; NaN scores stay NaN.
-    const float lse = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
-    float f = vscale / l;
-    if (a.sink) f *= 1.f / (1.f + fast_exp2((a.sink[head] - lse) * kLog2e));
-    if (a.gate) f *= 1.f / (1.f + fast_exp2(-a.gate[row] * kLog2e));
-    if (l == 0.f) f = 0.f;
+    const size_t row = (size_t)(q.row0 + t.t0 + r / a.group) * a.num_q_heads + head;
+    float lse;
+    const float f = row_factor(a, row, head, m, l, vscale, &lse);
     uint2 w;
     w.x = pack_bf16(v.x * f, v.y * f);
     w.y = pack_bf16(v.z * f, v.w * f);

@@ -474,7 +474,8 @@ typedef struct {
  * With num_tokens 0 a call does nothing and the row tensors may be NULL.
  * max_tokens: a bound on any sequence's new tokens; max_context: a bound on
  * context[b] (0: the largest the context serves, max_context - max_tokens + 1).
- * The bounds pick kernels and grid sizes; results do not depend on them. */
+ * The bounds pick kernels and grid sizes; results agree within the stated
+ * tolerances whatever they are. */
 typedef struct {
     const int32_t *block_table;
     const int32_t *context;
