@@ -65,7 +65,7 @@ struct hd_ctx {
     int kv_type = hd::KV_BF16;
     int32_t *counters = nullptr;         // [num_layers][max_batch][Hkv] chunk tickets, zero between calls
     int32_t *err = nullptr;
-    uint8_t *paged_ws = nullptr;         // paged calls: partial rows of cut items, or ranking keys of blocks
+    uint8_t *paged_ws = nullptr;         // paged calls: partial rows of cut items, or scores of blocks
     int64_t paged_ws_bytes = 0;
     int32_t *paged_tickets = nullptr;    // [kPagedTickets], zero between calls
     int consumer = hd::CONSUMER_MMA;

@@ -13,7 +13,7 @@ constexpr int kDecodeCtasPerSm = 2;
 constexpr int kChunkRows = 256;     // query rows of one chunk tile (a pair of CTAs)
 constexpr int kChunkKeys = 128;     // keys of one chunk tile
 constexpr int kPagedTickets = 1024;  // at least the CTAs of a paged attention grid
-constexpr int kMaxSelectBlocks = 16384;   // blocks of one sequence that select_pages ranks (128 KiB of keys)
+constexpr int kMaxSelectBlocks = 16384;   // blocks of one sequence that select_pages ranks (192 KiB of keys)
 
 // The sequences of a paged call.  A sequence's new tokens are rows
 // [offsets[b], offsets[b + 1]) of q / k / v / out (offsets null: row b); they
@@ -69,7 +69,7 @@ struct PagedSelectArgs {
     const __nv_bfloat16 *q;
     const __nv_bfloat16 *bounds;
     const float *k_scale;      // E4M3 or null (its sign turns a key's bounds round)
-    uint64_t *scores;          // [num_tokens][Hkv][score_stride] ranking keys
+    float2 *scores;            // [num_tokens][Hkv][score_stride]: score, sum of its terms' magnitudes
     int32_t score_stride;
     int32_t num_q_heads, num_kv_heads, group;
     int32_t num_selected, keep_first, keep_last;
@@ -77,7 +77,7 @@ struct PagedSelectArgs {
 };
 
 // Workspace of the paged calls: two partial tiles per CTA (decode) or pair of CTAs
-// (chunks) of the attention grid, or a ranking key per (sequence, kv head, block) of max_batch single-token rows.
+// (chunks) of the attention grid, or a score per (sequence, kv head, block) of max_batch single-token rows.
 constexpr int64_t paged_partial_rows(int num_sms, bool chunk) {
     return chunk ? (int64_t)2 * (num_sms / 2) * kChunkRows : (int64_t)2 * kDecodeCtasPerSm * num_sms * kDecodeRows;
 }
@@ -87,6 +87,26 @@ constexpr int64_t paged_partial_bytes(int num_sms) {
 static_assert(kChunkRows >= 2 * kDecodeCtasPerSm * kDecodeRows, "the chunk kernel's partials are the larger");
 constexpr int64_t paged_rank_bytes(int64_t max_batch, int64_t num_kv_heads, int64_t max_context) {
     return max_batch * num_kv_heads * ((max_context >> kMinPageShift) + 1) * 8;
+}
+
+// Launch as a programmatic dependent of the previous kernel in the stream (each of these kernels waits for it
+// before its first access to global memory), in clusters of `cluster` CTAs.
+template <class... P, class... A>
+cudaError_t launch_overlapping(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                               const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s);

@@ -224,7 +224,7 @@ hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, 
     a.q = static_cast<const __nv_bfloat16 *>(q_rot);
     a.bounds = static_cast<const __nv_bfloat16 *>(cache->bounds);
     a.k_scale = cache->k_scale;
-    a.scores = reinterpret_cast<uint64_t *>(ctx->paged_ws);
+    a.scores = reinterpret_cast<float2 *>(ctx->paged_ws);
     a.score_stride = (int32_t)blocks;
     a.num_q_heads = ctx->cfg.num_q_heads;
     a.num_kv_heads = ctx->cfg.num_kv_heads;

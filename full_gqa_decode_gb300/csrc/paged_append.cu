@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kQueryHeads = 4;   // heads of a row that one warp rotates
 
 // e4m3(fl64(y / s)) for y = a c - b sn (the exact rotation, rounded once to
 // binary64), bit for bit.  In binary32: q = RN(b sn), y32 = fma(a, c, -q) with
@@ -94,26 +95,36 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     __shared__ long long scan[33];
     __shared__ int found[4];
     __shared__ float edge[2][kWarps][kHeadDim];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
 
     if ((int)blockIdx.x >= runs * a.num_kv_heads) {
-        // ---- queries ----
+        // ---- queries: a warp takes up to kQueryHeads heads of a row, which share its angles ----
+        const int parts = (a.num_q_heads + kQueryHeads - 1) / kQueryHeads;
         const long long vec = (long long)(blockIdx.x - runs * a.num_kv_heads) * kWarps + warp;
-        const int r = (int)(vec / a.num_q_heads), h = (int)(vec % a.num_q_heads);
+        const int r = (int)(vec / parts), h0 = (int)(vec % parts) * kQueryHeads;
         if (r >= sq.num_tokens) return;
         int bit;
         const SeqSpan q = span_of_row(sq, r, &bit);
         if (q.n == 0) return;
-        const __nv_bfloat16 *src = a.q + (size_t)r * a.q_stride + h * kHeadDim;
-        __nv_bfloat16 *dst = a.q_rot + ((size_t)r * a.num_q_heads + h) * kHeadDim;
-        float x[4], y[4], c[4], s[4];
-        load4(src + ld.d0, x);
-        load4(src + ld.d1, y);
-        if (ld.i >= 0) {
-            load_angles(a.rope + (size_t)(q.ctx + r - q.row0) * half, ld.i, c, s);
-            rotate_bf16(x, y, c, s);
+        const __nv_bfloat16 *src = a.q + (size_t)r * a.q_stride + h0 * kHeadDim;
+        __nv_bfloat16 *dst = a.q_rot + ((size_t)r * a.num_q_heads + h0) * kHeadDim;
+        const int heads = min(kQueryHeads, a.num_q_heads - h0);
+        float x[kQueryHeads][4], y[kQueryHeads][4], c[4], s[4];
+#pragma unroll
+        for (int i = 0; i < kQueryHeads; ++i) {
+            if (i >= heads) break;
+            load4(src + i * kHeadDim + ld.d0, x[i]);
+            load4(src + i * kHeadDim + ld.d1, y[i]);
         }
-        store4(dst + ld.d0, x);
-        store4(dst + ld.d1, y);
+        if (ld.i >= 0) load_angles(a.rope + (size_t)(q.ctx + r - q.row0) * half, ld.i, c, s);
+#pragma unroll
+        for (int i = 0; i < kQueryHeads; ++i) {
+            if (i >= heads) break;
+            if (ld.i >= 0) rotate_bf16(x[i], y[i], c, s);
+            store4(dst + i * kHeadDim + ld.d0, x[i]);
+            store4(dst + i * kHeadDim + ld.d1, y[i]);
+        }
         return;
     }
 
@@ -261,11 +272,11 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s) {
     const PagedSeqs &q = a.seqs;
     // A sequence of n tokens touches at most (n - 1) / page + 2 pages, one of one token exactly one.
     const long long runs = q.offsets ? ((long long)q.num_tokens >> q.page_shift) + 2LL * q.batch : q.batch;
-    const long long qctas = a.q ? ((long long)q.num_tokens * a.num_q_heads + kWarps - 1) / kWarps : 0;
+    const long long parts = (a.num_q_heads + kQueryHeads - 1) / kQueryHeads;
+    const long long qctas = a.q ? ((long long)q.num_tokens * parts + kWarps - 1) / kWarps : 0;
     const long long grid = runs * a.num_kv_heads + qctas;
     if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-    paged_append_kernel<<<(unsigned)grid, kThreads, 0, s>>>(a, (int)runs);
-    return cudaGetLastError();
+    return launch_overlapping(paged_append_kernel, dim3((unsigned)grid), kThreads, 0, 1, s, a, (int)runs);
 }
 
 }  // namespace hd

@@ -102,11 +102,11 @@ struct Walk {
     long long left;      // tiles of the share from this one on
     bool fresh;          // first tile of a segment
 
-    __device__ void start(const PagedAttnArgs &a, const int *at, long long share) {
-        b = at[0];
-        tile = at[1];
-        h = at[2];
-        u = at[3];
+    __device__ void start(const PagedAttnArgs &a, const Start &at, long long share) {
+        b = at.b;
+        tile = at.tile;
+        h = at.h;
+        u = at.off;
         int bit;
         q = seq_span(a.seqs, b, &bit);
         t = make_chunk_tile(a, q, tile);
@@ -278,45 +278,18 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
         fence_mbar_init();
     }
-    // All key tiles of the call, and this pair's share.
-    const int per = (sq.batch + (int)blockDim.x - 1) / (int)blockDim.x;
-    const int b_lo = min(tid * per, sq.batch), b_hi = min(b_lo + per, sq.batch);
-    long long mine = 0;
-    int bad = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-        int bit;
-        const SeqSpan q = seq_span(sq, b, &bit);
-        bad |= bit;
-        const int tiles = num_chunk_tiles(a, q.n);
-        for (int i = 0; i < tiles; ++i) mine += (long long)make_chunk_tile(a, q, i).units * a.num_kv_heads;
-    }
-    bad = __syncthreads_or(bad);
-    long long T;
-    const long long before = block_prefix(mine, reinterpret_cast<long long *>(xm), &T);
+    __syncthreads();
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    // This pair's share of the call's key tiles.
+    long long x0, x1, T;
+    int n, bad;
+    const Start c0 = find_share(
+        sq, a.num_kv_heads, pair, pairs, kMinTiles, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
+        [&](int tokens) { return num_chunk_tiles(a, tokens); },
+        [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units; });
     if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
-    const int n = (int)min((long long)pairs, max(T / kMinTiles, 1LL));
-    if (pair >= n || T == 0) return;   // both CTAs of the pair
-    const long long x0 = T * pair / n, x1 = T * (pair + 1) / n;
-    if (before <= x0 && x0 < before + mine) {
-        long long rem = x0 - before;
-        bool found = false;
-        for (int b = b_lo; b < b_hi && !found; ++b) {
-            int bit;
-            const SeqSpan q = seq_span(sq, b, &bit);
-            const int tiles = num_chunk_tiles(a, q.n);
-            for (int i = 0; i < tiles && !found; ++i) {
-                const int u = make_chunk_tile(a, q, i).units;
-                if (rem < (long long)u * a.num_kv_heads) {
-                    misc[0] = b;
-                    misc[1] = i;
-                    misc[2] = (int)(rem / u);
-                    misc[3] = (int)(rem % u);
-                    found = true;
-                }
-                rem -= (long long)u * a.num_kv_heads;
-            }
-        }
-    }
+    if (x0 >= x1) return;   // both CTAs of the pair
     if (warp == kMmaWarp) pair_alloc(taddr_s);
     tc_fence_before();
     __syncthreads();
@@ -325,7 +298,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     const uint32_t tmem = *taddr_s;
     const long long N = x1 - x0;
     Walk w;
-    w.start(a, misc, N);
+    w.start(a, c0, N);
     bool dead = false;
     const int ps = 1 << sq.page_shift;
 
@@ -817,17 +790,7 @@ cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStre
     if (e != cudaSuccess) return e;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {2, 1, 1};
-    cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(chunk_threads(KV));
-    cfg.dynamicSmemBytes = kChunkSmem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<KV>, maps, a);
+    return launch_overlapping(paged_chunk_kernel<KV>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
 }
 
 }  // namespace

@@ -35,7 +35,8 @@ constexpr int kBufOff = kRing * kStageBytes;
 constexpr int kMlOff = kBufOff + 2 * kRowFloats * 4;
 constexpr int kBarOff = kMlOff + 2 * kWarps * kDecodeRows * 4;
 constexpr int kMiscOff = kBarOff + 2 * kRing * 8;
-constexpr int kSmemBytes = kMiscOff + 64;
+constexpr int kPosOff = kMiscOff + 32;          // [kRing][4] positions of a stage's page runs (selected blocks)
+constexpr int kSmemBytes = kPosOff + kRing * 4 * 4;
 static_assert(kDecodeCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 
 __host__ __device__ constexpr int stage_shift(int kv) { return kv == KV_FP8 ? 6 : 5; }
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     float *buf = reinterpret_cast<float *>(smem + kBufOff);
     float *ml = reinterpret_cast<float *>(smem + kMlOff);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff), *empty = full + kRing;
-    int *misc = reinterpret_cast<int *>(smem + kMiscOff);
+    int *misc = reinterpret_cast<int *>(smem + kMiscOff), *runs = reinterpret_cast<int *>(smem + kPosOff);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedSeqs &sq = a.seqs;
 
@@ -415,50 +416,20 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         }
         fence_mbar_init();
     }
-    // The whole call's stages, and this CTA's share of them.
-    const int per = (sq.batch + kThreads - 1) / kThreads;
-    const int b_lo = min(tid * per, sq.batch), b_hi = min(b_lo + per, sq.batch);
-    long long mine = 0;
-    int bad = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-        int bit;
-        const SeqSpan q = seq_span(sq, b, &bit);
-        bad |= bit;
-        const int tiles = num_tiles<KV, SPARSE>(a, q.n);
-        for (int i = 0; i < tiles; ++i) mine += (long long)make_tile<KV, SPARSE>(a, q, i).units * a.num_kv_heads;
-    }
-    bad = __syncthreads_or(bad);
-    long long T;
-    const long long before = block_prefix(mine, reinterpret_cast<long long *>(buf), &T);
-    if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
-    const int n = (int)min((long long)gridDim.x, max(T / min_units(KV), 1LL));
-    const int cta = blockIdx.x;
-    if (cta >= n || T == 0) return;
-    const long long x0 = T * cta / n, x1 = T * (cta + 1) / n;
-    if (before <= x0 && x0 < before + mine) {
-        long long rem = x0 - before;
-        for (int b = b_lo; b < b_hi; ++b) {
-            int bit;
-            const SeqSpan q = seq_span(sq, b, &bit);
-            const int tiles = num_tiles<KV, SPARSE>(a, q.n);
-            bool found = false;
-            for (int i = 0; i < tiles; ++i) {
-                const int u = make_tile<KV, SPARSE>(a, q, i).units;
-                if (rem < (long long)u * a.num_kv_heads) {
-                    misc[0] = b;
-                    misc[1] = i;
-                    misc[2] = (int)(rem / u);
-                    misc[3] = (int)(rem % u);
-                    found = true;
-                    break;
-                }
-                rem -= (long long)u * a.num_kv_heads;
-            }
-            if (found) break;
-        }
-    }
     __syncthreads();
-    Cursor c{misc[0], misc[1], misc[2], misc[3]};
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    // This CTA's share of the call's stages.
+    const int cta = blockIdx.x;
+    long long x0, x1, T;
+    int n, bad;
+    const Start c0 = find_share(
+        sq, a.num_kv_heads, cta, gridDim.x, min_units(KV), reinterpret_cast<long long *>(buf), misc, &x0, &x1, &T, &n, &bad,
+        [&](int tokens) { return num_tiles<KV, SPARSE>(a, tokens); },
+        [&](const SeqSpan &q, int i) { return make_tile<KV, SPARSE>(a, q, i).units; });
+    if (bad) fill_bad_rows(a, cta, gridDim.x);
+    if (x0 >= x1) return;
+    Cursor c{c0.b, c0.tile, c0.h, c0.off};
     int bit;
     SeqSpan q = seq_span(sq, c.b, &bit);
     const int ps = 1 << sq.page_shift;
@@ -481,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             // The segment's copies, 32 at a time: lane l looks up copy i0 + l's page and slot.
             const int first_key = (t.u0 + c.off) << kShift, total = seg * (int)copies;
             for (int i0 = 0; i0 < total; i0 += 32) {
-                int page = sq.num_pages, slot = 0;   // page num_pages lies outside the map: the copy fills zeros
+                int page = sq.num_pages, slot = 0, pos = 0;   // page num_pages lies outside the map: the copy fills zeros
                 if (i0 + lane < total) {
                     const int x_key = first_key + ((i0 + lane) << box_shift);
-                    const int pos = key_position<SPARSE>(a, sel, t, x_key);
+                    pos = key_position<SPARSE>(a, sel, t, x_key);
                     slot = x_key & (ps - 1);
                     if (pos < t.hi && pos + box_rows > t.lo) {
                         page = row[pos >> sq.page_shift];
@@ -500,9 +471,12 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
                     const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
                     if (!drop) {
+                        const bool mine = lane >= i && lane < i + (int)copies;
+                        if (SPARSE && mine) runs[st * 4 + lane - i] = pos;
+                        __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
                         __syncwarp();
-                        if (lane >= i && lane < i + (int)copies) {
+                        if (mine) {
                             uint8_t *d = dst + (lane - i) * (box_rows * kRowBytes);
                             tma_load_5d(d, &kmap, &full[st], 0, slot, 0, c.h, page);
                             tma_load_5d(d + kHalf, &vmap, &full[st], 0, slot, 0, c.h, page);
@@ -536,16 +510,16 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
         const int seg = (int)min((long long)(t.units - c.off), x1 - x);
         const long long item0 = x - c.off;
-        const int32_t *sel = SPARSE ? a.selected + ((size_t)(q.row0 + t.t0) * a.num_kv_heads + c.h) * a.num_selected : nullptr;
         cons.init(a, q, t, c.h, lane);
         const int all_hi = q.ctx + t.t0;                                        // every row sees up to here ..
         const int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;      // .. from here
         for (int u = 0; u < seg; ++u) {
-            const int key0 = key_position<SPARSE>(a, sel, t, ((t.u0 + c.off + u) << kShift) + r0);
+            int key0 = ((t.u0 + c.off + u) << kShift) + r0;
             if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[st], ph))) {
                 dead = true;
                 if (lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
             }
+            if (SPARSE) key0 = runs[st * 4 + (r0 >> box_shift)] + (r0 & (box_rows - 1));
             if (!dead && key0 < t.hi && key0 + kWK > t.lo) {
                 const uint8_t *stage = smem + st * kStageBytes;
                 const bool whole = key0 >= all_lo && key0 + kWK - 1 <= all_hi;
@@ -630,17 +604,24 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                     }
                 }
                 consumer_sync();
+                // Eight pieces' loads in flight per row: their latency, not their bytes, is what the merge waits for.
                 for (int i = tid; i < rows * (kHeadDim / 4); i += kWarps * 32) {
                     const int r = i >> 6, d = (i & 63) * 4;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int j = 0; j < nseg; ++j) {
-                        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (piece(j) + r) * kHeadDim + d));
-                        const float w = buf[r * nseg + j];
-                        v.x = fmaf(w, p.x, v.x);
-                        v.y = fmaf(w, p.y, v.y);
-                        v.z = fmaf(w, p.z, v.z);
-                        v.w = fmaf(w, p.w, v.w);
+                    for (int j0 = 0; j0 < nseg; j0 += 8) {
+                        float4 p[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            p[k] = j0 + k < nseg ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + (piece(j0 + k) + r) * kHeadDim + d))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float w = j0 + k < nseg ? buf[r * nseg + j0 + k] : 0.f;
+                            v.x = fmaf(w, p[k].x, v.x);
+                            v.y = fmaf(w, p[k].y, v.y);
+                            v.z = fmaf(w, p[k].z, v.z);
+                            v.w = fmaf(w, p[k].w, v.w);
+                        }
                     }
                     finish_row(a, q, t, c.h, r, d, v, ml[r], ml[kDecodeRows + r], vscale);
                 }
@@ -663,8 +644,8 @@ cudaError_t launch(const CUtensorMap *kmap, const CUtensorMap *vmap, const Paged
         if (e != cudaSuccess) return e;
         mark_done_on_device(done, dev);
     }
-    paged_decode_kernel<KV, SPARSE><<<kDecodeCtasPerSm * num_sms, kThreads, kSmemBytes, s>>>(*kmap, *vmap, a);
-    return cudaGetLastError();
+    return launch_overlapping(paged_decode_kernel<KV, SPARSE>, dim3(kDecodeCtasPerSm * num_sms), kThreads, kSmemBytes, 1, s,
+                              *kmap, *vmap, a);
 }
 
 }  // namespace

@@ -56,17 +56,23 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedSeqs &s, int b, int *bit,
     return q;
 }
 
-// The span of the sequence that row r belongs to; n = 0 when there is none or
-// it cannot be served (*bit; row0 is past r when no sequence has the row).
+// The span of the sequence that row r belongs to (the whole warp asks for the
+// same row); n = 0 when there is none or it cannot be served (*bit; row0 is past
+// r when no sequence has the row).  Offsets ascend: each round the lanes probe
+// 32 of them, so 1024 sequences take two loads in a row.
 __device__ __forceinline__ SeqSpan span_of_row(const PagedSeqs &s, int r, int *bit, int *seq = nullptr) {
     int b = r;
-    if (s.offsets) {   // the last sequence that starts at or before r (offsets ascend)
-        b = 0;
-        for (int hi = s.batch - 1; b < hi;) {
-            const int mid = (b + hi + 1) >> 1;
-            if (s.offsets[mid] <= r) b = mid;
-            else hi = mid - 1;
+    if (s.offsets) {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = s.batch;   // the last sequence that starts at or before r is in [lo, lo + n)
+        while (n > 1) {
+            const int step = (n + 31) >> 5, at = lo + lane * step;
+            const bool starts = lane * step < n && s.offsets[at] <= r;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, starts) | 1u);
+            n = min(step, n - k * step);
+            lo += k * step;
         }
+        b = lo;
     }
     if (seq) *seq = b;
     int rows = 0;
@@ -103,6 +109,96 @@ __device__ __forceinline__ long long block_prefix(long long x, long long *tmp, l
     __syncthreads();
     *total = tmp[warps - 1];
     return v - x + (warp ? tmp[warp - 1] : 0);
+}
+
+// Launched as a programmatic dependent of the previous kernel in the stream: set-up that touches no global memory
+// runs while that one drains, and everything else behind this wait.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// Where a worker's share of the call's units starts: sequence, tile of its new
+// tokens, kv head, and units of that item already passed.
+struct Start {
+    int b, tile, h, off;
+};
+
+// Share `who` of at most `workers` over all units of the call, each at least
+// `least` units: its first unit x0, its end x1 (x0 >= x1: none), the number of
+// shares n and the total T.  All threads of the block call it; `tmp`: 33 64-bit
+// words, `at`: 4 words of shared memory.  *bad: some sequence cannot be served.
+//   tiles(n)      tiles of n new tokens
+//   units(q, i)   units of one kv head of tile i of span q
+template <class Tiles, class Units>
+__device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads, int who, int workers, int least,
+                                            long long *tmp, int *at, long long *x0, long long *x1, long long *T, int *n,
+                                            int *bad, Tiles tiles, Units units) {
+    const int lane = threadIdx.x & 31;
+    // Up to 32 sequences every warp works it out by itself; above, the block together.
+    const bool by_warp = s.batch <= 32;
+    const int who_am = by_warp ? lane : (int)threadIdx.x, of = by_warp ? 32 : (int)blockDim.x;
+    const int per = (s.batch + of - 1) / of;
+    const int b_lo = min(who_am * per, s.batch), b_hi = min(b_lo + per, s.batch);
+    long long mine = 0, before;
+    int flags = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        int bit;
+        const SeqSpan q = seq_span(s, b, &bit);
+        flags |= bit;
+        const int nt = tiles(q.n);
+        for (int i = 0; i < nt; ++i) mine += (long long)units(q, i) * num_kv_heads;
+    }
+    if (by_warp) {
+        long long v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        *T = __shfl_sync(0xffffffffu, v, 31);
+        before = v - mine;
+        *bad = __any_sync(0xffffffffu, flags);
+    } else {
+        *bad = __syncthreads_or(flags);
+        before = block_prefix(mine, tmp, T);
+    }
+    *n = (int)min((long long)workers, max(*T / least, 1LL));
+    *x0 = who < *n ? *T * who / *n : 0;
+    *x1 = who < *n ? *T * (who + 1) / *n : 0;
+    Start c{0, 0, 0, 0};
+    const bool here = before <= *x0 && *x0 < before + mine && *x0 < *x1;
+    if (here) {
+        long long rem = *x0 - before;
+        bool found = false;
+        for (int b = b_lo; b < b_hi && !found; ++b) {
+            int bit;
+            const SeqSpan q = seq_span(s, b, &bit);
+            const int nt = tiles(q.n);
+            for (int i = 0; i < nt && !found; ++i) {
+                const int u = units(q, i);
+                if (rem < (long long)u * num_kv_heads) {
+                    c = {b, i, (int)(rem / u), (int)(rem % u)};
+                    found = true;
+                }
+                rem -= (long long)u * num_kv_heads;
+            }
+        }
+    }
+    if (by_warp) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        if (src >= 0)
+            c = {__shfl_sync(0xffffffffu, c.b, src), __shfl_sync(0xffffffffu, c.tile, src),
+                 __shfl_sync(0xffffffffu, c.h, src), __shfl_sync(0xffffffffu, c.off, src)};
+    } else {
+        if (here) {
+            at[0] = c.b;
+            at[1] = c.tile;
+            at[2] = c.h;
+            at[3] = c.off;
+        }
+        __syncthreads();
+        if (*x0 < *x1) c = {at[0], at[1], at[2], at[3]};
+    }
+    return c;
 }
 
 // Which CTA of n holds unit x of T.

@@ -526,15 +526,16 @@ hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, co
  * token's own, then those of the largest score
  *     sum over the kv head's query heads and dims of max(q_d lo_d, q_d hi_d)
  * with lo / hi the block's bounds -- the sum of the largest scores that any of
- * its keys could reach.  Ties go to the lower block; scores are summed to twice
- * fp32's precision, so the choice does not depend on the order of summation.
+ * its keys could reach.  Ties go to the lower block; scores that fp32
+ * cannot tell apart are summed to twice its precision, so the choice does not
+ * depend on the order of summation.
  *   selected  int32 [num_tokens][num_kv_heads][num_selected]: block numbers,
  *             ascending, -1 behind the last when a token has fewer blocks.
  * Bounds must be finite for every block up to the token's own.
  * HD_ERR_STATE for a sliding layer; HD_ERR_INVALID_ARG without bounds, with
  * num_selected < 1 or keep_first + keep_last > num_selected; HD_ERR_CAPACITY
- * above 16384 blocks a sequence, or when the ranking keys (8 bytes for each row,
- * kv head and block of max_context) exceed the context's workspace, which holds
+ * above 16384 blocks a sequence, or when the scores (8 bytes for each row, kv head
+ * and block of max_context) exceed the context's workspace, which holds
  * those of max_batch rows of max_context. */
 hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
                        const hd_paged_cache *cache, int32_t num_selected, int32_t keep_first, int32_t keep_last,
