@@ -9,7 +9,7 @@ namespace hd {
 constexpr int kMinPageShift = 4;    // pages of 16 ..
 constexpr int kMaxPageShift = 8;    // .. 256 slots, a power of two
 constexpr int kDecodeRows = 8;      // query rows per kv head (heads x tokens) of one decode tile
-constexpr int kDecodeCtasPerSm = 2;
+constexpr int kDecodeCtasPerSm = 1;
 constexpr int kChunkRows = 256;     // query rows of one chunk tile (a pair of CTAs)
 constexpr int kChunkKeys = 128;     // keys of one chunk tile
 constexpr int kPagedTickets = 1024;  // at least the CTAs of a paged attention grid

@@ -2,45 +2,57 @@
 // decode, a few drafted tokens, and decode over selected pages.
 //
 // Each item (sequence, up to eight query rows = heads x tokens, kv head)
-// streams its visible keys once through a shared-memory ring of 32 KiB stages
-// (32 bf16 or 64 E4M3 keys of K and V).  One producer warp looks the pages up
-// and issues one 5-D TMA copy per page run and stage half -- the box takes all
-// 256 dims as 128-byte column groups, so a stage is two copies for pages of a
-// stage's keys or more, four (16-row bf16 pages) to eight otherwise -- and
-// four consumer warps split a stage's keys: scores and outputs on mma.sync
-// with an online softmax per warp in log2 units, merged at the end of an item.
-// The work is cut evenly over two CTAs per SM (paged_sched.cuh); the ring runs
-// on across items.
+// streams its visible keys once: HBM bounds it, so the arithmetic only has to
+// keep out of the way.  One persistent CTA per SM runs a ring of six 32 KiB
+// stages (32 bf16 or 64 E4M3 keys of K and V) on across items.  One producer
+// warp looks the pages up and issues one 5-D TMA copy per page run and stage
+// half -- the box takes all 256 dims as 128-byte column groups, so a stage is
+// two copies for pages of at least a stage's keys, four to eight otherwise.
+// Eight consumer warps take 16 keys each; the warps of a stage (two, or four
+// with E4M3) form a team and the teams take stages in turn, so a warp's chain of
+// dependent MMAs and shuffles overlaps the other teams' and not only its own
+// stage's copies.  The work is cut evenly over the CTAs (paged_sched.cuh).
 //
-// Rotated queries come in bf16 and enter the products as they are.  With an
-// E4M3 cache codes convert exactly to f16, and a row's q is scaled by the power
-// of two that brings its largest value below 2, so that f16 holds it: values
-// below 2^-14 of that lose bits under 2^-25 of the largest, less than the fp32
-// sum of the products does.  P is rounded to the cache's 16-bit type for the
-// second product (2^-9 or 2^-12 of each weight, below the output's own
-// rounding once summed); f16 weights are taken 2^15 times as large, which the
-// division by their sum undoes, so that small ones stay clear of f16's
-// subnormals.  Sums and maxima stay in fp32.
+// Per 16 keys, on mma.sync m16n8k16 with an online softmax in log2 units:
+//     S^T = K Q^T   keys on M, the rows on N: q takes two registers a k-step
+//     O^T += V^T P^T   dims on M; P^T is the scores' fragment transposed
+// Rotated queries enter the products in bf16 as they come.  With an E4M3 cache
+// codes convert exactly to f16, and a row's q is scaled by the power of two that
+// brings its largest value below 2, so that f16 holds it: values below 2^-14 of
+// that lose bits under 2^-25 of the largest, less than the fp32 sum of the
+// products does.  P is rounded to the cache's 16-bit type for the second product
+// (2^-9 or 2^-12 of each weight, below the output's own rounding once summed);
+// f16 weights are taken 2^15 times as large, which the division by their sum
+// undoes, so that small ones stay clear of f16's subnormals.  Sums and maxima
+// stay in fp32.
 #include "paged_rows.cuh"
 
 namespace hd {
 namespace {
 
-constexpr int kRing = 3;                        // stages of 32 KiB
-constexpr int kWarps = 4;                       // consumer warps
+constexpr int kRing = 6;                        // stages of 32 KiB
+// Barriers of landed stages: two rounds of the ring, so that a barrier always serves the same team, which cannot
+// take a round for the one before it (a parity tells only neighbouring rounds apart).
+constexpr int kFulls = 2 * kRing;
+constexpr int kWarps = 8;                       // consumer warps
+constexpr int kWarpKeys = 16;                   // keys a warp takes at a time
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kRowFloats = kDecodeRows * kHeadDim;
-// Shared memory: ring | merge buffer of two warps' rows | row maxima and sums | barriers | scan.
+constexpr int kRowPad = kHeadDim + 4;           // floats between rows of a merge buffer: fragment stores hit all banks
+constexpr int kBufFloats = kDecodeRows * kRowPad;
+constexpr int kBufs = kWarps / 2;
+// Shared memory: ring | merge buffers | row maxima and sums | barriers | scan and flags | page runs of a stage.
 constexpr int kBufOff = kRing * kStageBytes;
-constexpr int kMlOff = kBufOff + 2 * kRowFloats * 4;
+constexpr int kMlOff = kBufOff + kBufs * kBufFloats * 4;
 constexpr int kBarOff = kMlOff + 2 * kWarps * kDecodeRows * 4;
-constexpr int kMiscOff = kBarOff + 2 * kRing * 8;
+constexpr int kMiscOff = kBarOff + (kFulls + kRing) * 8;
 constexpr int kPosOff = kMiscOff + 32;          // [kRing][4] positions of a stage's page runs (selected blocks)
 constexpr int kSmemBytes = kPosOff + kRing * 4 * 4;
-static_assert(kDecodeCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+static_assert(kDecodeCtasPerSm == 1, "the partials' workspace counts one CTA per SM");
 
 __host__ __device__ constexpr int stage_shift(int kv) { return kv == KV_FP8 ? 6 : 5; }
-// Shortest share of a CTA, in stages: below 128 keys the merge costs more than the split saves.
+// Warps of a stage's team, and the shortest share of a CTA in stages.
+__host__ __device__ constexpr int team_warps(int kv) { return (1 << stage_shift(kv)) / kWarpKeys; }
 __host__ __device__ constexpr int min_units(int kv) { return kv == KV_FP8 ? 2 : 4; }
 
 // A tile of new tokens of one sequence.
@@ -113,157 +125,24 @@ __device__ __forceinline__ int key_position(const PagedAttnArgs &a, const int32_
 }
 
 // ------------------------------------------------------------- consumers --
-// One warp's keys of a stage against the tile's rows.  `base`: byte offset of
-// the warp's first key row in a stage half, `col`: bytes between its 128-byte
+// One warp's 16 keys of a stage against the tile's rows.  `base`: byte offset
+// of the warp's first key row in a stage half, `col`: bytes between its 128-byte
 // column groups; key0: position of that key; [vlo, vhi): positions whose V may
 // be read; full: every row sees every key of the warp.
-struct DecodeBf16 {
-    static constexpr int kKeys = 8;
-    uint32_t qa[16][2];
-    float o[16][4];        // O^T: dims 16 mt + gid (+ 8) x rows 2 t4 (+ 1)
-    float m_run, l_run;    // row gid; l_run: this lane's keys
-    int lo, hi;            // row gid's visible positions
 
-    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
-        const int gid = lane >> 2, t4 = lane & 3;
-        const int tok = gid / a.group, rows = t.nt * a.group;
-        const __nv_bfloat16 *src =
-            a.q + ((size_t)(q.row0 + t.t0 + tok) * a.num_q_heads + h * a.group + gid % a.group) * kHeadDim + 2 * t4;
-#pragma unroll
-        for (int ks = 0; ks < 16; ++ks) {
-            qa[ks][0] = gid < rows ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks)) : 0u;
-            qa[ks][1] = gid < rows ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 8)) : 0u;
-        }
-        hi = q.ctx + t.t0 + tok;
-        lo = a.window ? hi - a.window + 1 : 0;
-#pragma unroll
-        for (int mt = 0; mt < 16; ++mt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
-        m_run = -INFINITY;
-        l_run = 0.f;
-    }
+// What both cache types share: the softmax on S^T fragments (register r of
+// lane (gid, t4): key gid + 8 (r / 2), row 2 t4 + r % 2), and the rows' state.
+template <bool F16>
+struct DecodeRowsState {
+    static constexpr float kLift = F16 ? 15.f : 0.f;
+    float o[16][4];            // O^T: dims (two of tile mt) x rows 2 t4 (+ 1)
+    float m_run[2], l_run[2];  // rows 2 t4 + e; l_run: this lane's keys
+    int lo[2], hi[2];          // visible positions of these rows
 
-    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
-                            int vhi, bool full, int lane) {
-        const int t4 = lane & 3, lr = lane & 7, lsub = lane >> 3;
-        const uint32_t sw0 = (uint32_t)(lsub ^ lr) << 4, sw1 = (uint32_t)((4 + lsub) ^ lr) << 4;
-        const uint32_t kb = smem_u32(kst) + base + lr * 128, vb = smem_u32(vst) + base + lr * 128;
-        // Two accumulators (even / odd k-steps) halve the dependent MMA chain.
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(kb + (p >> 1) * col + (p & 1 ? sw1 : sw0), b0, b1, b2, b3);
-            const uint32_t a0[4] = {qa[2 * p][0], 0u, qa[2 * p][1], 0u};
-            const uint32_t a1[4] = {qa[2 * p + 1][0], 0u, qa[2 * p + 1][1], 0u};
-            mma_16816(s, a0, b0, b1);
-            mma_16816(s2, a1, b2, b3);
-        }
-        const int k0 = key0 + 2 * t4;
-        const bool ok0 = full || (k0 >= lo && k0 <= hi), ok1 = full || (k0 + 1 >= lo && k0 + 1 <= hi);
-        const float x0 = ok0 ? (s[0] + s2[0]) * kQScale : -INFINITY;
-        const float x1 = ok1 ? (s[1] + s2[1]) * kQScale : -INFINITY;
-        float mx = fmaxf(x0, x1);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m_run, mx);
-        const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m_run - mn);
-        const float p0 = ok0 ? fast_exp2(x0 - mn) : 0.f, p1 = ok1 ? fast_exp2(x1 - mn) : 0.f;
-        l_run = fmaf(l_run, alpha, p0 + p1);
-        m_run = mn;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-            const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2 t4
-            const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2 t4 + 1
-#pragma unroll
-            for (int mt = 0; mt < 16; ++mt) {
-                o[mt][0] *= a_lo;
-                o[mt][1] *= a_hi;
-                o[mt][2] *= a_lo;
-                o[mt][3] *= a_hi;
-            }
-        }
-        const uint32_t pb = pack_bf16(p0, p1);
-        // Slots outside [vlo, vhi) may hold anything, and 0 * NaN would reach every row.
-        uint32_t vm = 0xFFFFFFFFu;
-        if (!full)
-            vm = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_trans(vb + (p >> 1) * col + (p & 1 ? sw1 : sw0), a0, a1, a2, a3);
-            mma_1688(o[2 * p], a0 & vm, a1 & vm, pb);
-            mma_1688(o[2 * p + 1], a2 & vm, a3 & vm, pb);
-        }
-    }
-
-    // Row gid's maximum and (whole warp's) sum, by the lane with t4 = 0.
-    __device__ void publish(float *ml, int warp, int lane) const {
-        float l = l_run;
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if ((lane & 3) == 0) {
-            ml[warp * kDecodeRows + (lane >> 2)] = m_run;
-            ml[(kWarps + warp) * kDecodeRows + (lane >> 2)] = l;
-        }
-    }
-    template <class F> __device__ void each(int lane, F f) {   // f(row, dim, value&)
-        const int gid = lane >> 2, t4 = lane & 3;
-#pragma unroll
-        for (int mt = 0; mt < 16; ++mt) {
-            f(2 * t4, 16 * mt + gid, o[mt][0]);
-            f(2 * t4 + 1, 16 * mt + gid, o[mt][1]);
-            f(2 * t4, 16 * mt + gid + 8, o[mt][2]);
-            f(2 * t4 + 1, 16 * mt + gid + 8, o[mt][3]);
-        }
-    }
-};
-
-// E4M3 pages: S^T = K Q^T with the warp's 16 keys on M, codes converted to f16
-// as the A operand; O^T = V^T P^T as in the bf16 case with 16 keys on K.  Lane
-// (gid, t4) reads 16-byte chunks 2 t4 + (p & 1) + 8 (p >> 1) of key rows gid
-// and gid + 8 at step p (eight lanes of a phase hit eight different chunks);
-// q's columns are held in the same order of dims, which leaves every dot
-// product as it is.
-struct DecodeE4m3 {
-    static constexpr int kKeys = 16;
-    static constexpr float kLift = 15.f;
-    uint32_t qb[16][2];
-    float o[16][4];            // O^T tile mt: dims 128 (mt / 8) + 16 gid + 2 (mt % 8) (+ 1) x rows 2 t4 (+ 1)
-    float m_run[2], l_run[2];  // rows 2 t4 + e
-    float sc[2];               // score scale of rows 2 t4 + e, log2 units
-    int lo[2], hi[2];
-
-    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
-        const int gid = lane >> 2, t4 = lane & 3;
-        const int rows = t.nt * a.group;
-        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
-                                          gid % a.group) * kHeadDim;
-        uint2 w[16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d = 16 * (2 * t4 + (p & 1) + 8 * (p >> 1)) + 4 * j;
-                w[4 * p + j] = gid < rows ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
-                const uint2 m = make_uint2(w[4 * p + j].x & 0x7FFF7FFFu, w[4 * p + j].y & 0x7FFF7FFFu);
-                top = max(top, max(max(m.x & 0xFFFFu, m.x >> 16), max(m.y & 0xFFFFu, m.y >> 16)));
-            }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = min(max((int)(top >> 7), 1), 253);               // exponent field of the row's largest value
-        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^(127 - ex)
-        const float up = __uint_as_float((uint32_t)ex << 23);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            qb[i][0] = pack_f16(__uint_as_float(w[i].x << 16) * down, __uint_as_float(w[i].x & 0xFFFF0000u) * down);
-            qb[i][1] = pack_f16(__uint_as_float(w[i].y << 16) * down, __uint_as_float(w[i].y & 0xFFFF0000u) * down);
-        }
+    __device__ void init_rows(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int lane) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            sc[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * kQScale);
-            hi[e] = q.ctx + t.t0 + (2 * t4 + e) / a.group;
+            hi[e] = q.ctx + t.t0 + (2 * (lane & 3) + e) / a.group;
             lo[e] = a.window ? hi[e] - a.window + 1 : 0;
             m_run[e] = -INFINITY;
             l_run[e] = 0.f;
@@ -273,32 +152,17 @@ struct DecodeE4m3 {
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
     }
-
-    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
-                            int vhi, bool full, int lane) {
-        const int gid = lane >> 2, t4 = lane & 3;
-        auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int chunk = 2 * t4 + (p & 1) + 8 * (p >> 1);
-            const uint4 ka = *reinterpret_cast<const uint4 *>(kst + at(gid, chunk));
-            const uint4 kb = *reinterpret_cast<const uint4 *>(kst + at(gid + 8, chunk));
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x[4] = {e4m3x2_to_f16x2((uint16_t)(wa[j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(wb[j] & 0xFFFFu)),
-                                       e4m3x2_to_f16x2((uint16_t)(wa[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wb[j] >> 16))};
-                mma_16816_f16(j & 1 ? s2 : s, x, qb[4 * p + j][0], qb[4 * p + j][1]);
-            }
-        }
+    // Scores (times scale[e], log2 units) to weights; returns the two P^T operands: keys 2 t4 (+ 1) and 8 + 2 t4
+    // (+ 1) of row gid.
+    __device__ __forceinline__ void weigh(const float (&s)[4], const float (&scale)[2], int key0, bool full, int lane,
+                                          uint32_t &pb0, uint32_t &pb1) {
+        const int k0 = key0 + (lane >> 2);
         float p[4], alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int k0 = key0 + gid;
             const bool v0 = full || (k0 >= lo[e] && k0 <= hi[e]), v1 = full || (k0 + 8 >= lo[e] && k0 + 8 <= hi[e]);
-            const float x0 = v0 ? (s[e] + s2[e]) * sc[e] : -INFINITY;
-            const float x1 = v1 ? (s[2 + e] + s2[2 + e]) * sc[e] : -INFINITY;
+            const float x0 = v0 ? s[e] * scale[e] : -INFINITY;
+            const float x1 = v1 ? s[2 + e] * scale[e] : -INFINITY;
             float mx = fmaxf(x0, x1);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -319,14 +183,162 @@ struct DecodeE4m3 {
                 o[mt][3] *= alpha[1];
             }
         }
-        const uint32_t pb0 = movmatrix_trans(pack_f16(p[0], p[1]));   // keys 2 t4 (+ 1) of row gid
-        const uint32_t pb1 = movmatrix_trans(pack_f16(p[2], p[3]));   // keys 8 + 2 t4 (+ 1)
-        uint32_t m01 = 0xFFFFFFFFu, m89 = 0xFFFFFFFFu;
-        if (!full) {   // slots outside [vlo, vhi) may hold NaN codes
-            const int k0 = key0 + 2 * t4;
-            m01 = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
-            m89 = (k0 + 8 >= vlo && k0 + 8 < vhi ? 0x0000FFFFu : 0u) | (k0 + 9 >= vlo && k0 + 9 < vhi ? 0xFFFF0000u : 0u);
+        pb0 = movmatrix_trans(F16 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+        pb1 = movmatrix_trans(F16 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
+    }
+    // Masks of the V values of keys 2 t4 (+ 1) and 8 + 2 t4 (+ 1): slots outside [vlo, vhi) may hold anything, and
+    // 0 * NaN would reach every row.
+    __device__ static __forceinline__ void value_masks(int key0, int vlo, int vhi, bool full, int lane, uint32_t &m01,
+                                                       uint32_t &m89) {
+        m01 = m89 = 0xFFFFFFFFu;
+        if (full) return;
+        const int k0 = key0 + 2 * (lane & 3);
+        m01 = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
+        m89 = (k0 + 8 >= vlo && k0 + 8 < vhi ? 0x0000FFFFu : 0u) | (k0 + 9 >= vlo && k0 + 9 < vhi ? 0xFFFF0000u : 0u);
+    }
+    // Rows' maxima and (whole warp's) sums.
+    __device__ void publish(float *ml, int warp, int lane) const {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = l_run[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (lane < 4) {
+                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
+                ml[(kWarps + warp) * kDecodeRows + 2 * lane + e] = l;
+            }
         }
+    }
+};
+
+// bf16 pages.  O^T tile mt: dims 16 mt + gid (+ 8).
+struct DecodeBf16 : DecodeRowsState<false> {
+    uint32_t qb[16][2];
+    float scale[2];
+
+    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        const bool live = gid < t.nt * a.group;
+        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
+                                          gid % a.group) * kHeadDim + 2 * t4;
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+            qb[ks][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks)) : 0u;
+            qb[ks][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 8)) : 0u;
+        }
+        scale[0] = scale[1] = kQScale;
+        init_rows(a, q, t, lane);
+    }
+
+    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
+                            int vhi, bool full, int lane) {
+        const int lr = lane & 7;
+        // K: matrices (keys 0-7, 8-15) x (dims 0-7, 8-15) of k-step ks.
+        const uint32_t kb = smem_u32(kst) + base + (lr + (lane & 8)) * 128;
+        const uint32_t kc = (uint32_t)lane >> 4;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+            uint32_t x[4];
+            ldsm_x4(kb + (ks >> 2) * col + ((((uint32_t)(2 * (ks & 3)) + kc) ^ lr) << 4), x[0], x[1], x[2], x[3]);
+            mma_16816(ks & 1 ? s2 : s, x, qb[ks][0], qb[ks][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += s2[i];
+        uint32_t pb0, pb1, m01, m89;
+        weigh(s, scale, key0, full, lane, pb0, pb1);
+        value_masks(key0, vlo, vhi, full, lane, m01, m89);
+        // V^T: matrices (dims 0-7, 8-15 of tile mt) x (keys 0-7, 8-15), transposed on the way.
+        const uint32_t vb = smem_u32(vst) + base + (lr + ((lane & 16) >> 1)) * 128;
+        const uint32_t vc = (uint32_t)(lane >> 3) & 1;
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt) {
+            uint32_t x[4];
+            ldsm_x4_trans(vb + (mt >> 2) * col + ((((uint32_t)(2 * (mt & 3)) + vc) ^ lr) << 4), x[0], x[1], x[2], x[3]);
+            x[0] &= m01;
+            x[1] &= m01;
+            x[2] &= m89;
+            x[3] &= m89;
+            mma_16816(o[mt], x, pb0, pb1);
+        }
+    }
+    template <class F> __device__ void each(int lane, F f) {   // f(row, dim, value&)
+        const int gid = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int mt = 0; mt < 16; ++mt) {
+            f(2 * t4, 16 * mt + gid, o[mt][0]);
+            f(2 * t4 + 1, 16 * mt + gid, o[mt][1]);
+            f(2 * t4, 16 * mt + gid + 8, o[mt][2]);
+            f(2 * t4 + 1, 16 * mt + gid + 8, o[mt][3]);
+        }
+    }
+};
+
+// E4M3 pages.  Lane (gid, t4) reads 16-byte chunks 2 t4 + (p & 1) + 8 (p >> 1)
+// of key rows gid and gid + 8 at step p (eight lanes of a phase hit eight
+// different chunks); q's columns are held in the same order of dims, which
+// leaves every dot product as it is.  O^T tile mt: dims 128 (mt / 8) + 16 gid +
+// 2 (mt % 8) (+ 1).
+struct DecodeE4m3 : DecodeRowsState<true> {
+    uint32_t qb[16][2];
+    float scale[2];
+
+    __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        const bool live = gid < t.nt * a.group;
+        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
+                                          gid % a.group) * kHeadDim;
+        uint32_t top = 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = 16 * (2 * t4 + (p & 1) + 8 * (p >> 1)) + 4 * j;
+                const uint2 w = live ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
+                qb[4 * p + j][0] = w.x;
+                qb[4 * p + j][1] = w.y;
+                const uint2 m = make_uint2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+                top = max(top, max(max(m.x & 0xFFFFu, m.x >> 16), max(m.y & 0xFFFFu, m.y >> 16)));
+            }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = min(max((int)(top >> 7), 1), 253);               // exponent field of the row's largest value
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^(127 - ex)
+        const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                qb[i][j] = pack_f16(__uint_as_float(qb[i][j] << 16) * down, __uint_as_float(qb[i][j] & 0xFFFF0000u) * down);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) scale[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * kQScale);
+        init_rows(a, q, t, lane);
+    }
+
+    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
+                            int vhi, bool full, int lane) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int chunk = 2 * t4 + (p & 1) + 8 * (p >> 1);
+            const uint4 ka = *reinterpret_cast<const uint4 *>(kst + at(gid, chunk));
+            const uint4 kb = *reinterpret_cast<const uint4 *>(kst + at(gid + 8, chunk));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x[4] = {e4m3x2_to_f16x2((uint16_t)(wa[j] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(wb[j] & 0xFFFFu)),
+                                       e4m3x2_to_f16x2((uint16_t)(wa[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wb[j] >> 16))};
+                mma_16816_f16(j & 1 ? s2 : s, x, qb[4 * p + j][0], qb[4 * p + j][1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += s2[i];
+        uint32_t pb0, pb1, m01, m89;
+        weigh(s, scale, key0, full, lane, pb0, pb1);
+        value_masks(key0, vlo, vhi, full, lane, m01, m89);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int chunk = 8 * half + gid;
@@ -346,20 +358,6 @@ struct DecodeE4m3 {
                                            e4m3x2_to_f16x2((uint16_t)(x89 & 0xFFFFu)) & m89, e4m3x2_to_f16x2((uint16_t)(x89 >> 16)) & m89};
                     mma_16816_f16(o[8 * half + 2 * w + q], x, pb0, pb1);
                 }
-        }
-    }
-
-    __device__ void publish(float *ml, int warp, int lane) const {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float l = l_run[e];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if (lane < 4) {
-                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
-                ml[(kWarps + warp) * kDecodeRows + 2 * lane + e] = l;
-            }
         }
     }
     template <class F> __device__ void each(int lane, F f) {
@@ -404,16 +402,14 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     constexpr int kHalf = kStageBytes / 2;
     float *buf = reinterpret_cast<float *>(smem + kBufOff);
     float *ml = reinterpret_cast<float *>(smem + kMlOff);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff), *empty = full + kRing;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff), *empty = full + kFulls;
     int *misc = reinterpret_cast<int *>(smem + kMiscOff), *runs = reinterpret_cast<int *>(smem + kPosOff);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedSeqs &sq = a.seqs;
 
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kWarps);
-        }
+        for (int i = 0; i < kFulls; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&empty[i], team_warps(KV));
         fence_mbar_init();
     }
     __syncthreads();
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         // ---- producer ----
         const uint32_t copies = kKeys >> box_shift;   // per stage half
         long long x = x0;
-        int st = 0;
+        int st = 0, odd = 0;   // ring slot, and kRing in the ring's odd rounds
         uint32_t ph = 0;
         bool dead = false;
         int issued = 0;
@@ -474,17 +470,18 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                         const bool mine = lane >= i && lane < i + (int)copies;
                         if (SPARSE && mine) runs[st * 4 + lane - i] = pos;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
+                        if (lane == 0) mbar_arrive_expect_tx(&full[st + odd], kStageBytes);
                         __syncwarp();
                         if (mine) {
                             uint8_t *d = dst + (lane - i) * (box_rows * kRowBytes);
-                            tma_load_5d(d, &kmap, &full[st], 0, slot, 0, c.h, page);
-                            tma_load_5d(d + kHalf, &vmap, &full[st], 0, slot, 0, c.h, page);
+                            tma_load_5d(d, &kmap, &full[st + odd], 0, slot, 0, c.h, page);
+                            tma_load_5d(d + kHalf, &vmap, &full[st + odd], 0, slot, 0, c.h, page);
                         }
                     }
                     ++issued;
                     if (++st == kRing) {
                         st = 0;
+                        odd = kRing - odd;
                         ph ^= 1;
                     }
                 }
@@ -497,47 +494,55 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     }
 
     // ---- consumers ----
+    constexpr int kTeam = team_warps(KV), kTeams = kWarps / kTeam;
+    static_assert(kFulls % kTeams == 0, "a barrier serves one team");
     typename DecodeConsumer<KV>::T cons;
-    constexpr int kWK = decltype(cons)::kKeys;
-    const int r0 = warp * kWK;   // this warp's key rows of a stage
+    const int team = warp / kTeam;
+    const int r0 = (warp % kTeam) * kWarpKeys;   // this warp's key rows of a stage
     const uint32_t base = (uint32_t)(r0 >> box_shift) * (box_rows * kRowBytes) + (r0 & (box_rows - 1)) * 128;
     const uint32_t col = box_rows * 128;
     long long x = x0;
-    int st = 0;
-    uint32_t ph = 0;
+    int fb = team;             // this team's next stage: its barrier, ..
+    uint32_t ph = 0;           // .. the parity of that barrier's round, ..
+    int u = team;              // .. and its number from the segment's first stage
     bool dead = false;
     while (x < x1) {
         const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
         const int seg = (int)min((long long)(t.units - c.off), x1 - x);
-        const long long item0 = x - c.off;
         cons.init(a, q, t, c.h, lane);
         const int all_hi = q.ctx + t.t0;                                        // every row sees up to here ..
         const int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;      // .. from here
-        for (int u = 0; u < seg; ++u) {
-            int key0 = ((t.u0 + c.off + u) << kShift) + r0;
-            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[st], ph))) {
+        for (; u < seg; u += kTeams) {
+            const int st = fb < kRing ? fb : fb - kRing;
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[fb], ph))) {
                 dead = true;
                 if (lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
             }
+            int key0 = ((t.u0 + c.off + u) << kShift) + r0;
             if (SPARSE) key0 = runs[st * 4 + (r0 >> box_shift)] + (r0 & (box_rows - 1));
-            if (!dead && key0 < t.hi && key0 + kWK > t.lo) {
+            if (!dead && key0 < t.hi && key0 + kWarpKeys > t.lo) {
                 const uint8_t *stage = smem + st * kStageBytes;
-                const bool whole = key0 >= all_lo && key0 + kWK - 1 <= all_hi;
+                const bool whole = key0 >= all_lo && key0 + kWarpKeys - 1 <= all_hi;
                 cons.consume(stage, stage + kHalf, base, col, key0, t.lo, t.hi, whole, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
-            if (++st == kRing) {
-                st = 0;
+            fb += kTeams;
+            if (fb >= kFulls) {
+                fb -= kFulls;
                 ph ^= 1;
             }
         }
-        // Merge the four warps: warps 2 and 3 hand their rows to 0 and 1.
+        u -= seg;
+        // Merge the eight warps: the upper four hand their rows to the lower four.
         const int rows = t.nt * a.group;
         cons.publish(ml, warp, lane);
         consumer_sync();
         auto row_max = [&](int r) {
-            return fmaxf(fmaxf(ml[r], ml[kDecodeRows + r]), fmaxf(ml[2 * kDecodeRows + r], ml[3 * kDecodeRows + r]));
+            float m = ml[r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[w * kDecodeRows + r]);
+            return m;
         };
         auto row_sum = [&](int r, float m) {
             float l = 0.f;
@@ -550,22 +555,27 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             const int ra = 2 * (lane & 3);
             const float wa = part_weight(ml[warp * kDecodeRows + ra], row_max(ra));
             const float wb = part_weight(ml[warp * kDecodeRows + ra + 1], row_max(ra + 1));
-            float *mine_buf = buf + (warp & 1) * kRowFloats;
-            if (warp >= 2) cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kHeadDim + d] = v * (r & 1 ? wb : wa); });
+            float *mine_buf = buf + (warp & (kBufs - 1)) * kBufFloats;
+            if (warp >= kBufs)
+                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kRowPad + d] = v * (r & 1 ? wb : wa); });
             consumer_sync();
-            if (warp < 2)
-                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kHeadDim + d] += v * (r & 1 ? wb : wa); });
+            if (warp < kBufs)
+                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kRowPad + d] += v * (r & 1 ? wb : wa); });
         }
         consumer_sync();
+        const long long item0 = x - c.off;
         const bool begins = c.off == 0, ends = c.off + seg == t.units;
         const float vscale = KV == KV_FP8 ? a.v_scale[c.h] : 1.f;
         const bool whole_item = begins && ends;
         const int slot = begins ? 2 * cta + 1 : 2 * cta;
         for (int i = tid; i < rows * (kHeadDim / 4); i += kWarps * 32) {
             const int r = i >> 6, d = (i & 63) * 4;
-            float4 v = *reinterpret_cast<const float4 *>(buf + r * kHeadDim + d);
-            const float4 w = *reinterpret_cast<const float4 *>(buf + kRowFloats + r * kHeadDim + d);
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            float4 v = *reinterpret_cast<const float4 *>(buf + r * kRowPad + d);
+#pragma unroll
+            for (int i = 1; i < kBufs; ++i) {
+                const float4 w = *reinterpret_cast<const float4 *>(buf + i * kBufFloats + r * kRowPad + d);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
             const float m = row_max(r), l = row_sum(r, m);
             if (whole_item) {
                 finish_row(a, q, t, c.h, r, d, v, m, l, vscale);
@@ -585,13 +595,14 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                 // Weights of the pieces, [rows][nseg] in the merge buffer: nseg <= CTAs.
                 auto piece = [&](int j) { return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kDecodeRows; };
                 for (int r = warp; r < rows; r += kWarps) {
-                    float m = -INFINITY;
-                    for (int j = lane; j < nseg; j += 32) m = fmaxf(m, __ldcg(&a.part_ml[piece(j) + r]).x);
+                    float2 first = lane < nseg ? __ldcg(&a.part_ml[piece(lane) + r]) : make_float2(-INFINITY, 0.f);
+                    float m = first.x;
+                    for (int j = lane + 32; j < nseg; j += 32) m = fmaxf(m, __ldcg(&a.part_ml[piece(j) + r]).x);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     float l = 0.f;
                     for (int j = lane; j < nseg; j += 32) {
-                        const float2 p = __ldcg(&a.part_ml[piece(j) + r]);
+                        const float2 p = j < 32 ? first : __ldcg(&a.part_ml[piece(j) + r]);
                         const float w = part_weight(p.x, m);
                         buf[r * nseg + j] = w;
                         l += w * p.y;

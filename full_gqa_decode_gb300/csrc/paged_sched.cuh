@@ -161,9 +161,13 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
         *bad = __syncthreads_or(flags);
         before = block_prefix(mine, tmp, T);
     }
-    *n = (int)min((long long)workers, max(*T / least, 1LL));
-    *x0 = who < *n ? *T * who / *n : 0;
-    *x1 = who < *n ? *T * (who + 1) / *n : 0;
+    *n = *T >= (long long)workers * least ? workers : max((int)*T / least, 1);
+    // T who / n from one division (of 32 bits where T allows): n^2 is small.
+    const int k = *n;
+    const long long each = *T < 0x80000000LL ? (int)*T / k : *T / k;
+    const int rest = (int)(*T - each * k);
+    *x0 = who < k ? who * each + who * rest / k : 0;
+    *x1 = who < k ? (who + 1) * each + (who + 1) * rest / k : 0;
     Start c{0, 0, 0, 0};
     const bool here = before <= *x0 && *x0 < before + mine && *x0 < *x1;
     if (here) {
