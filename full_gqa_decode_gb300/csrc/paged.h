@@ -58,7 +58,7 @@ struct PagedAttnArgs {
     float *part_o;             // partial rows of cut items, two slots per CTA
     float2 *part_ml;           // (max in log2 units, sum)
     int32_t *tickets;          // [CTAs], zero between calls
-    int32_t num_q_heads, num_kv_heads, group;
+    int32_t num_q_heads, num_kv_heads, group, group_shift;   // group: 1, 2, 4 or 8 = 1 << group_shift
     int32_t window;            // sliding layers; 0: all positions
     int32_t kv_type;
     int32_t drop_stage;        // test hook: the producers stop issuing at this stage (-1: off)

@@ -98,6 +98,7 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     a.num_q_heads = ctx->cfg.num_q_heads;
     a.num_kv_heads = ctx->cfg.num_kv_heads;
     a.group = ctx->group;
+    while (1 << a.group_shift < a.group) ++a.group_shift;
     a.window = ctx->layer_types[layer] == HD_SLIDING ? ctx->cfg.sliding_window : 0;
     a.kv_type = ctx->kv_type;
     a.drop_stage = ctx->drop_stage;

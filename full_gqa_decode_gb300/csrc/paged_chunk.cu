@@ -79,7 +79,7 @@ struct ChunkTile {
 };
 __device__ __forceinline__ ChunkTile make_chunk_tile(const PagedAttnArgs &a, const SeqSpan &q, int tile) {
     ChunkTile t;
-    const int tt = kTileRows / a.group;
+    const int tt = kTileRows >> a.group_shift;
     t.t0 = tile * tt;
     t.nt = min(tt, q.n - t.t0);
     t.hi = q.ctx + t.t0 + t.nt;
@@ -89,8 +89,7 @@ __device__ __forceinline__ ChunkTile make_chunk_tile(const PagedAttnArgs &a, con
     return t;
 }
 __device__ __forceinline__ int num_chunk_tiles(const PagedAttnArgs &a, int n) {
-    const int tt = kTileRows / a.group;
-    return (n + tt - 1) / tt;
+    return ((n << a.group_shift) + kTileRows - 1) / kTileRows;
 }
 
 // A walk over the tiles of a pair's share, item by item.
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 m = -INFINITY;
                 l = 0.f;
                 const int r = rank * kCtaRows + row;
-                hi_pos = w.q.ctx + w.t.t0 + r / a.group;
+                hi_pos = w.q.ctx + w.t.t0 + (r >> a.group_shift);
                 lo_pos = a.window ? hi_pos - a.window + 1 : 0;
                 all_hi = w.q.ctx + w.t.t0;
                 all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;

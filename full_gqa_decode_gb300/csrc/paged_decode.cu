@@ -34,8 +34,8 @@ constexpr int kRing = 6;                        // stages of 32 KiB
 // Barriers of landed stages: two rounds of the ring, so that a barrier always serves the same team, which cannot
 // take a round for the one before it (a parity tells only neighbouring rounds apart).
 constexpr int kFulls = 2 * kRing;
-constexpr int kWarps = 8;                       // consumer warps
 constexpr int kWarpKeys = 16;                   // keys a warp takes at a time
+constexpr int kWarps = 8;                       // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRowPad = kHeadDim + 4;           // floats between rows of a merge buffer: fragment stores hit all banks
 constexpr int kBufFloats = kDecodeRows * kRowPad;
@@ -43,9 +43,9 @@ constexpr int kBufs = kWarps / 2;
 // Shared memory: ring | merge buffers | row maxima and sums | barriers | scan and flags | page runs of a stage.
 constexpr int kBufOff = kRing * kStageBytes;
 constexpr int kMlOff = kBufOff + kBufs * kBufFloats * 4;
-constexpr int kBarOff = kMlOff + 2 * kWarps * kDecodeRows * 4;
+constexpr int kBarOff = kMlOff + 2 * (kWarps + 1) * kDecodeRows * 4;
 constexpr int kMiscOff = kBarOff + (kFulls + kRing) * 8;
-constexpr int kPosOff = kMiscOff + 32;          // [kRing][4] positions of a stage's page runs (selected blocks)
+constexpr int kPosOff = kMiscOff + 48;          // [kRing][4] positions of a stage's page runs (selected blocks)
 constexpr int kSmemBytes = kPosOff + kRing * 4 * 4;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 static_assert(kDecodeCtasPerSm == 1, "the partials' workspace counts one CTA per SM");
@@ -64,7 +64,7 @@ struct Tile {
 
 template <int KV, bool SPARSE>
 __device__ __forceinline__ int tile_tokens(const PagedAttnArgs &a) {
-    return SPARSE ? 1 : kDecodeRows / a.group;
+    return SPARSE ? 1 : kDecodeRows >> a.group_shift;
 }
 
 template <int KV, bool SPARSE>
@@ -95,8 +95,7 @@ struct Cursor {
 
 template <int KV, bool SPARSE>
 __device__ __forceinline__ int num_tiles(const PagedAttnArgs &a, int n) {
-    const int tt = tile_tokens<KV, SPARSE>(a);
-    return (n + tt - 1) / tt;
+    return SPARSE ? n : ((n << a.group_shift) + kDecodeRows - 1) / kDecodeRows;
 }
 
 // The item after (c, q): advances to the next kv head, tile or sequence.
@@ -124,11 +123,18 @@ __device__ __forceinline__ int key_position(const PagedAttnArgs &a, const int32_
     return (blk << a.seqs.page_shift) + slot;
 }
 
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+// Row of q / out / lse of row r of a tile.
+__device__ __forceinline__ size_t query_row(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int r) {
+    return (size_t)(q.row0 + t.t0 + (r >> a.group_shift)) * a.num_q_heads + (h << a.group_shift) + (r & (a.group - 1));
+}
+
 // ------------------------------------------------------------- consumers --
 // One warp's 16 keys of a stage against the tile's rows.  `base`: byte offset
 // of the warp's first key row in a stage half, `col`: bytes between its 128-byte
 // column groups; key0: position of that key; [vlo, vhi): positions whose V may
-// be read; full: every row sees every key of the warp.
+// be read; first: position of the tile's first row; full: every row sees every
+// key of the warp.
 
 // What both cache types share: the softmax on S^T fragments (register r of
 // lane (gid, t4): key gid + 8 (r / 2), row 2 t4 + r % 2), and the rows' state.
@@ -137,13 +143,10 @@ struct DecodeRowsState {
     static constexpr float kLift = F16 ? 15.f : 0.f;
     float o[16][4];            // O^T: dims (two of tile mt) x rows 2 t4 (+ 1)
     float m_run[2], l_run[2];  // rows 2 t4 + e; l_run: this lane's keys
-    int lo[2], hi[2];          // visible positions of these rows
 
-    __device__ void init_rows(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int lane) {
+    __device__ void init_rows() {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            hi[e] = q.ctx + t.t0 + (2 * (lane & 3) + e) / a.group;
-            lo[e] = a.window ? hi[e] - a.window + 1 : 0;
             m_run[e] = -INFINITY;
             l_run[e] = 0.f;
         }
@@ -154,13 +157,18 @@ struct DecodeRowsState {
     }
     // Scores (times scale[e], log2 units) to weights; returns the two P^T operands: keys 2 t4 (+ 1) and 8 + 2 t4
     // (+ 1) of row gid.
-    __device__ __forceinline__ void weigh(const float (&s)[4], const float (&scale)[2], int key0, bool full, int lane,
-                                          uint32_t &pb0, uint32_t &pb1) {
-        const int k0 = key0 + (lane >> 2);
+    __device__ __forceinline__ void weigh(const PagedAttnArgs &a, const float (&s)[4], const float (&scale)[2], int key0,
+                                          int first, bool full, int lane, uint32_t &pb0, uint32_t &pb1) {
         float p[4], alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const bool v0 = full || (k0 >= lo[e] && k0 <= hi[e]), v1 = full || (k0 + 8 >= lo[e] && k0 + 8 <= hi[e]);
+            bool v0 = true, v1 = true;
+            if (!full) {   // first: position of the tile's first row
+                const int k0 = key0 + (lane >> 2), hi = first + ((2 * (lane & 3) + e) >> a.group_shift);
+                const int lo = a.window ? hi - a.window + 1 : 0;
+                v0 = k0 >= lo && k0 <= hi;
+                v1 = k0 + 8 >= lo && k0 + 8 <= hi;
+            }
             const float x0 = v0 ? s[e] * scale[e] : -INFINITY;
             const float x1 = v1 ? s[2 + e] * scale[e] : -INFINITY;
             float mx = fmaxf(x0, x1);
@@ -188,16 +196,13 @@ struct DecodeRowsState {
     }
     // Masks of the V values of keys 2 t4 (+ 1) and 8 + 2 t4 (+ 1): slots outside [vlo, vhi) may hold anything, and
     // 0 * NaN would reach every row.
-    __device__ static __forceinline__ void value_masks(int key0, int vlo, int vhi, bool full, int lane, uint32_t &m01,
-                                                       uint32_t &m89) {
-        m01 = m89 = 0xFFFFFFFFu;
-        if (full) return;
+    __device__ static __forceinline__ void value_masks(int key0, int vlo, int vhi, int lane, uint32_t &m01, uint32_t &m89) {
         const int k0 = key0 + 2 * (lane & 3);
         m01 = (k0 >= vlo && k0 < vhi ? 0x0000FFFFu : 0u) | (k0 + 1 >= vlo && k0 + 1 < vhi ? 0xFFFF0000u : 0u);
         m89 = (k0 + 8 >= vlo && k0 + 8 < vhi ? 0x0000FFFFu : 0u) | (k0 + 9 >= vlo && k0 + 9 < vhi ? 0xFFFF0000u : 0u);
     }
-    // Rows' maxima and (whole warp's) sums.
-    __device__ void publish(float *ml, int warp, int lane) const {
+    // Rows' maxima and (whole warp's) sums, [warps][rows] each.
+    __device__ void publish(float *mx, float *sums, int warp, int lane) const {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float l = l_run[e];
@@ -205,8 +210,8 @@ struct DecodeRowsState {
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (lane < 4) {
-                ml[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
-                ml[(kWarps + warp) * kDecodeRows + 2 * lane + e] = l;
+                mx[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
+                sums[warp * kDecodeRows + 2 * lane + e] = l;
             }
         }
     }
@@ -219,20 +224,19 @@ struct DecodeBf16 : DecodeRowsState<false> {
 
     __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
         const int gid = lane >> 2, t4 = lane & 3;
-        const bool live = gid < t.nt * a.group;
-        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
-                                          gid % a.group) * kHeadDim + 2 * t4;
+        const bool live = gid < t.nt << a.group_shift;
+        const __nv_bfloat16 *src = a.q + query_row(a, q, t, h, gid) * kHeadDim + 2 * t4;
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks) {
             qb[ks][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks)) : 0u;
             qb[ks][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 8)) : 0u;
         }
         scale[0] = scale[1] = kQScale;
-        init_rows(a, q, t, lane);
+        init_rows();
     }
 
-    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
-                            int vhi, bool full, int lane) {
+    __device__ void consume(const PagedAttnArgs &a, const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col,
+                            int key0, int vlo, int vhi, int first, bool full, int lane) {
         const int lr = lane & 7;
         // K: matrices (keys 0-7, 8-15) x (dims 0-7, 8-15) of k-step ks.
         const uint32_t kb = smem_u32(kst) + base + (lr + (lane & 8)) * 128;
@@ -247,8 +251,17 @@ struct DecodeBf16 : DecodeRowsState<false> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
         uint32_t pb0, pb1, m01, m89;
-        weigh(s, scale, key0, full, lane, pb0, pb1);
-        value_masks(key0, vlo, vhi, full, lane, m01, m89);
+        weigh(a, s, scale, key0, first, full, lane, pb0, pb1);
+        if (full) {   // the masks fold away
+            products(vst, base, col, lane, pb0, pb1, 0xFFFFFFFFu, 0xFFFFFFFFu);
+        } else {
+            value_masks(key0, vlo, vhi, lane, m01, m89);
+            products(vst, base, col, lane, pb0, pb1, m01, m89);
+        }
+    }
+    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane, uint32_t pb0,
+                                             uint32_t pb1, uint32_t m01, uint32_t m89) {
+        const int lr = lane & 7;
         // V^T: matrices (dims 0-7, 8-15 of tile mt) x (keys 0-7, 8-15), transposed on the way.
         const uint32_t vb = smem_u32(vst) + base + (lr + ((lane & 16) >> 1)) * 128;
         const uint32_t vc = (uint32_t)(lane >> 3) & 1;
@@ -286,9 +299,8 @@ struct DecodeE4m3 : DecodeRowsState<true> {
 
     __device__ void init(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
         const int gid = lane >> 2, t4 = lane & 3;
-        const bool live = gid < t.nt * a.group;
-        const __nv_bfloat16 *src = a.q + ((size_t)(q.row0 + t.t0 + gid / a.group) * a.num_q_heads + h * a.group +
-                                          gid % a.group) * kHeadDim;
+        const bool live = gid < t.nt << a.group_shift;
+        const __nv_bfloat16 *src = a.q + query_row(a, q, t, h, gid) * kHeadDim;
         uint32_t top = 0;
 #pragma unroll
         for (int p = 0; p < 4; ++p)
@@ -313,11 +325,11 @@ struct DecodeE4m3 : DecodeRowsState<true> {
                 qb[i][j] = pack_f16(__uint_as_float(qb[i][j] << 16) * down, __uint_as_float(qb[i][j] & 0xFFFF0000u) * down);
 #pragma unroll
         for (int e = 0; e < 2; ++e) scale[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * kQScale);
-        init_rows(a, q, t, lane);
+        init_rows();
     }
 
-    __device__ void consume(const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col, int key0, int vlo,
-                            int vhi, bool full, int lane) {
+    __device__ void consume(const PagedAttnArgs &a, const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col,
+                            int key0, int vlo, int vhi, int first, bool full, int lane) {
         const int gid = lane >> 2, t4 = lane & 3;
         auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
         float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
@@ -337,8 +349,18 @@ struct DecodeE4m3 : DecodeRowsState<true> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
         uint32_t pb0, pb1, m01, m89;
-        weigh(s, scale, key0, full, lane, pb0, pb1);
-        value_masks(key0, vlo, vhi, full, lane, m01, m89);
+        weigh(a, s, scale, key0, first, full, lane, pb0, pb1);
+        if (full) {   // the masks fold away
+            products(vst, base, col, lane, pb0, pb1, 0xFFFFFFFFu, 0xFFFFFFFFu);
+        } else {
+            value_masks(key0, vlo, vhi, lane, m01, m89);
+            products(vst, base, col, lane, pb0, pb1, m01, m89);
+        }
+    }
+    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane, uint32_t pb0,
+                                             uint32_t pb1, uint32_t m01, uint32_t m89) {
+        const int gid = lane >> 2, t4 = lane & 3;
+        auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int chunk = 8 * half + gid;
@@ -377,13 +399,12 @@ template <int KV> struct DecodeConsumer;
 template <> struct DecodeConsumer<KV_BF16> { using T = DecodeBf16; };
 template <> struct DecodeConsumer<KV_FP8> { using T = DecodeE4m3; };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 // Writes row r of a finished tile (thread's four dims d..d+3 of its
 // unnormalised output, log2-unit maximum m and sum l).
 __device__ __forceinline__ void finish_row(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int r, int d,
                                            float4 v, float m, float l, float vscale) {
-    const int head = h * a.group + r % a.group;
-    const size_t row = (size_t)(q.row0 + t.t0 + r / a.group) * a.num_q_heads + head;
+    const int head = (h << a.group_shift) + (r & (a.group - 1));
+    const size_t row = query_row(a, q, t, h, r);
     float lse;
     const float f = row_factor(a, row, head, m, l, vscale, &lse);
     uint2 w;
@@ -401,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     constexpr int kShift = stage_shift(KV), kKeys = 1 << kShift;
     constexpr int kHalf = kStageBytes / 2;
     float *buf = reinterpret_cast<float *>(smem + kBufOff);
-    float *ml = reinterpret_cast<float *>(smem + kMlOff);
+    // [warps][8] maxima, [warps][8] sums, and the tile's [8] maxima and [8] sums.
+    float *mx = reinterpret_cast<float *>(smem + kMlOff), *sums = mx + kWarps * kDecodeRows, *mfin = sums + kWarps * kDecodeRows;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff), *empty = full + kFulls;
     int *misc = reinterpret_cast<int *>(smem + kMiscOff), *runs = reinterpret_cast<int *>(smem + kPosOff);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -425,6 +447,15 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         [&](const SeqSpan &q, int i) { return make_tile<KV, SPARSE>(a, q, i).units; });
     if (bad) fill_bad_rows(a, cta, gridDim.x);
     if (x0 >= x1) return;
+    // Behind the barrier a share is counted in stages done; what only cut items need waits in shared memory.
+    const int share = (int)(x1 - x0);
+    long long *call = reinterpret_cast<long long *>(misc + 6);   // T, x0
+    if (tid == 0) {
+        call[0] = T;
+        call[1] = x0;
+        misc[5] = n;
+    }
+    __syncthreads();
     Cursor c{c0.b, c0.tile, c0.h, c0.off};
     int bit;
     SeqSpan q = seq_span(sq, c.b, &bit);
@@ -435,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     if (warp == kWarps) {
         // ---- producer ----
         const uint32_t copies = kKeys >> box_shift;   // per stage half
-        long long x = x0;
+        int x = 0;
         int st = 0, odd = 0;   // ring slot, and kRing in the ring's odd rounds
         uint32_t ph = 0;
         bool dead = false;
         int issued = 0;
-        while (x < x1) {
+        while (x < share) {
             const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
-            const int seg = (int)min((long long)(t.units - c.off), x1 - x);
+            const int seg = min(t.units - c.off, share - x);
             const int32_t *row = sq.table + (size_t)c.b * sq.table_stride;
             const int32_t *sel = SPARSE ? a.selected + ((size_t)(q.row0 + t.t0) * a.num_kv_heads + c.h) * a.num_selected : nullptr;
             // The segment's copies, 32 at a time: lane l looks up copy i0 + l's page and slot.
@@ -487,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                 }
             }
             x += seg;
-            if (x < x1) next_item<KV, SPARSE>(a, c, q);
+            if (x < share) next_item<KV, SPARSE>(a, c, q);
         }
         if (dead && lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
         return;
@@ -501,15 +532,23 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     const int r0 = (warp % kTeam) * kWarpKeys;   // this warp's key rows of a stage
     const uint32_t base = (uint32_t)(r0 >> box_shift) * (box_rows * kRowBytes) + (r0 & (box_rows - 1)) * 128;
     const uint32_t col = box_rows * 128;
-    long long x = x0;
+    int x = 0;
     int fb = team;             // this team's next stage: its barrier, ..
     uint32_t ph = 0;           // .. the parity of that barrier's round, ..
     int u = team;              // .. and its number from the segment's first stage
     bool dead = false;
-    while (x < x1) {
+    while (x < share) {
         const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
-        const int seg = (int)min((long long)(t.units - c.off), x1 - x);
+        const int seg = min(t.units - c.off, share - x);
         cons.init(a, q, t, c.h, lane);
+        if (warp == 0 && x + seg < share) {   // the next item's query rows into L2
+            Cursor nc = c;
+            SeqSpan nq = q;
+            next_item<KV, SPARSE>(a, nc, nq);
+            const Tile nt = make_tile<KV, SPARSE>(a, nq, nc.tile);
+            for (int i = lane; i < (nt.nt << a.group_shift) * 4; i += 32)   // 128-byte lines
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + query_row(a, nq, nt, nc.h, i >> 2) * kHeadDim + (i & 3) * 64));
+        }
         const int all_hi = q.ctx + t.t0;                                        // every row sees up to here ..
         const int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;      // .. from here
         for (; u < seg; u += kTeams) {
@@ -523,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             if (!dead && key0 < t.hi && key0 + kWarpKeys > t.lo) {
                 const uint8_t *stage = smem + st * kStageBytes;
                 const bool whole = key0 >= all_lo && key0 + kWarpKeys - 1 <= all_hi;
-                cons.consume(stage, stage + kHalf, base, col, key0, t.lo, t.hi, whole, lane);
+                cons.consume(a, stage, stage + kHalf, base, col, key0, t.lo, t.hi, all_hi, whole, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -534,36 +573,38 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             }
         }
         u -= seg;
-        // Merge the eight warps: the upper four hand their rows to the lower four.
-        const int rows = t.nt * a.group;
-        cons.publish(ml, warp, lane);
+        // Merge the eight warps, scaled to the rows' maxima: the upper four hand their rows to the lower four.
+        const int rows = t.nt << a.group_shift;
+        cons.publish(mx, sums, warp, lane);
         consumer_sync();
         auto row_max = [&](int r) {
-            float m = ml[r];
+            float m = mx[r];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[w * kDecodeRows + r]);
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, mx[w * kDecodeRows + r]);
             return m;
-        };
-        auto row_sum = [&](int r, float m) {
-            float l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                l += ml[(kWarps + w) * kDecodeRows + r] * part_weight(ml[w * kDecodeRows + r], m);
-            return l;
         };
         {
             const int ra = 2 * (lane & 3);
-            const float wa = part_weight(ml[warp * kDecodeRows + ra], row_max(ra));
-            const float wb = part_weight(ml[warp * kDecodeRows + ra + 1], row_max(ra + 1));
+            const float wa = part_weight(mx[warp * kDecodeRows + ra], row_max(ra));
+            const float wb = part_weight(mx[warp * kDecodeRows + ra + 1], row_max(ra + 1));
+            if (tid < kDecodeRows) {
+                const float m = row_max(tid);
+                float l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) l += sums[w * kDecodeRows + tid] * part_weight(mx[w * kDecodeRows + tid], m);
+                mfin[tid] = m;
+                mfin[kDecodeRows + tid] = l;
+            }
             float *mine_buf = buf + (warp & (kBufs - 1)) * kBufFloats;
             if (warp >= kBufs)
                 cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kRowPad + d] = v * (r & 1 ? wb : wa); });
             consumer_sync();
-            if (warp < kBufs)
-                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kRowPad + d] += v * (r & 1 ? wb : wa); });
+            if (warp < kBufs) {   // all loads, then all stores: interleaved, each would wait for the one before
+                cons.each(lane, [&](int r, int d, float &v) { v = fmaf(v, r & 1 ? wb : wa, mine_buf[r * kRowPad + d]); });
+                cons.each(lane, [&](int r, int d, float &v) { mine_buf[r * kRowPad + d] = v; });
+            }
         }
         consumer_sync();
-        const long long item0 = x - c.off;
         const bool begins = c.off == 0, ends = c.off + seg == t.units;
         const float vscale = KV == KV_FP8 ? a.v_scale[c.h] : 1.f;
         const bool whole_item = begins && ends;
@@ -572,76 +613,70 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             const int r = i >> 6, d = (i & 63) * 4;
             float4 v = *reinterpret_cast<const float4 *>(buf + r * kRowPad + d);
 #pragma unroll
-            for (int i = 1; i < kBufs; ++i) {
-                const float4 w = *reinterpret_cast<const float4 *>(buf + i * kBufFloats + r * kRowPad + d);
+            for (int k = 1; k < kBufs; ++k) {
+                const float4 w = *reinterpret_cast<const float4 *>(buf + k * kBufFloats + r * kRowPad + d);
                 v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
             }
-            const float m = row_max(r), l = row_sum(r, m);
             if (whole_item) {
-                finish_row(a, q, t, c.h, r, d, v, m, l, vscale);
+                finish_row(a, q, t, c.h, r, d, v, mfin[r], mfin[kDecodeRows + r], vscale);
             } else {
                 *reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kDecodeRows + r) * kHeadDim + d) = v;
-                if (d == 0) a.part_ml[(size_t)slot * kDecodeRows + r] = make_float2(m, l);
+                if (d == 0) a.part_ml[(size_t)slot * kDecodeRows + r] = make_float2(mfin[r], mfin[kDecodeRows + r]);
             }
         }
         if (!whole_item) {
-            const int i0 = cta_of_unit(item0, T, n), i1 = cta_of_unit(item0 + t.units - 1, T, n), nseg = i1 - i0 + 1;
-            __threadfence();
+            const long long all = call[0], item0 = call[1] + x - c.off;
+            const int i0 = cta_of_unit(item0, all, misc[5]), nseg = cta_of_unit(item0 + t.units - 1, all, misc[5]) - i0 + 1;
             consumer_sync();
-            if (tid == 0) misc[4] = atomicAdd(&a.tickets[i0], 1) == nseg - 1;
+            if (tid == 0) {
+                __threadfence();   // the block's stores (ordered by the barrier) before the ticket
+                misc[4] = atomicAdd(&a.tickets[i0], 1) == nseg - 1;
+                __threadfence();   // the ticket before the other pieces' loads
+            }
             consumer_sync();
             if (misc[4]) {
-                __threadfence();
-                // Weights of the pieces, [rows][nseg] in the merge buffer: nseg <= CTAs.
+                // A thread's four dims of a row: sixteen pieces' values and (max, sum) in flight at a time, rescaled
+                // as the maximum moves -- the loads' latency, not their bytes, is what the merge waits for.
                 auto piece = [&](int j) { return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kDecodeRows; };
-                for (int r = warp; r < rows; r += kWarps) {
-                    float2 first = lane < nseg ? __ldcg(&a.part_ml[piece(lane) + r]) : make_float2(-INFINITY, 0.f);
-                    float m = first.x;
-                    for (int j = lane + 32; j < nseg; j += 32) m = fmaxf(m, __ldcg(&a.part_ml[piece(j) + r]).x);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    float l = 0.f;
-                    for (int j = lane; j < nseg; j += 32) {
-                        const float2 p = j < 32 ? first : __ldcg(&a.part_ml[piece(j) + r]);
-                        const float w = part_weight(p.x, m);
-                        buf[r * nseg + j] = w;
-                        l += w * p.y;
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    if (lane == 0) {
-                        ml[r] = m;
-                        ml[kDecodeRows + r] = l;
-                    }
-                }
-                consumer_sync();
-                // Eight pieces' loads in flight per row: their latency, not their bytes, is what the merge waits for.
                 for (int i = tid; i < rows * (kHeadDim / 4); i += kWarps * 32) {
                     const int r = i >> 6, d = (i & 63) * 4;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int j0 = 0; j0 < nseg; j0 += 8) {
-                        float4 p[8];
+                    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < nseg; j0 += 16) {
+                        float4 p[16];
+                        float2 g[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            p[k] = j0 + k < nseg ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + (piece(j0 + k) + r) * kHeadDim + d))
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < 16; ++k) {
+                            const size_t at = piece(min(j0 + k, nseg - 1)) + r;
+                            g[k] = __ldcg(&a.part_ml[at]);
+                            p[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kHeadDim + d));
+                        }
+                        float top = m;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float w = j0 + k < nseg ? buf[r * nseg + j0 + k] : 0.f;
+                        for (int k = 0; k < 16; ++k) top = fmaxf(top, g[k].x);
+                        const float w0 = part_weight(m, top);
+                        v = make_float4(v.x * w0, v.y * w0, v.z * w0, v.w * w0);
+                        l *= w0;
+                        m = top;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float w = j0 + k < nseg ? part_weight(g[k].x, m) : 0.f;
+                            l = fmaf(w, g[k].y, l);
                             v.x = fmaf(w, p[k].x, v.x);
                             v.y = fmaf(w, p[k].y, v.y);
                             v.z = fmaf(w, p[k].z, v.z);
                             v.w = fmaf(w, p[k].w, v.w);
                         }
                     }
-                    finish_row(a, q, t, c.h, r, d, v, ml[r], ml[kDecodeRows + r], vscale);
+                    finish_row(a, q, t, c.h, r, d, v, m, l, vscale);
                 }
                 if (tid == 0) a.tickets[i0] = 0;
             }
         }
-        consumer_sync();   // the merge buffer and ml are free again
+        consumer_sync();   // the merge buffers are free again
         x += seg;
-        if (x < x1) next_item<KV, SPARSE>(a, c, q);
+        if (x < share) next_item<KV, SPARSE>(a, c, q);
     }
 }
 

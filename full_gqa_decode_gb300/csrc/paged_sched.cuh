@@ -180,7 +180,8 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
             for (int i = 0; i < nt && !found; ++i) {
                 const int u = units(q, i);
                 if (rem < (long long)u * num_kv_heads) {
-                    c = {b, i, (int)(rem / u), (int)(rem % u)};
+                    // rem < units of one tile x kv heads: fewer than 2^32 for any pool that fits in memory
+                    c = {b, i, (int)((unsigned)rem / (unsigned)u), (int)((unsigned)rem % (unsigned)u)};
                     found = true;
                 }
                 rem -= (long long)u * num_kv_heads;
