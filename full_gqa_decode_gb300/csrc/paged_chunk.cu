@@ -14,9 +14,8 @@
 //
 // Tensor memory (512 columns in each CTA): scores in two buffers of 128
 // columns, the output of 256.  P, in 16 bits, takes the place of the scores
-// that it came from and is the A operand of the second product.  The MMA warp
-// runs one tile ahead: S(i) is issued before O += P(i-1) V(i-1), so the softmax
-// of one tile overlaps the products of its neighbours, across items too.
+// that it came from and is the A operand of the second product.  The softmax of
+// one tile overlaps the products of its neighbours, across items too.
 //
 // Roles of a CTA: eight softmax warps, two threads a row (64 scores each,
 // maxima exchanged through shared memory by pairs of warps); a copy warp; the
@@ -44,10 +43,10 @@ __host__ __device__ constexpr int chunk_threads(int kv) { return (kStageWarp + s
 constexpr int kQBytes = kCtaRows * kHeadDim * 2;      // 64 KiB
 constexpr int kSlotBytes = 32 * 1024;                 // this CTA's half of a K or V tile in 16 bits
 constexpr int kRawBytes = 16 * 1024;                  // ... in E4M3 codes
-__host__ __device__ constexpr int num_slots(int kv) { return kv == KV_FP8 ? 3 : 5; }
-constexpr int kRawSlots = 4;
+__host__ __device__ constexpr int num_slots(int kv) { return kv == KV_FP8 ? 4 : 5; }
+constexpr int kRawSlots = 2;
 constexpr int kRingBytes = 160 * 1024;
-static_assert(5 * kSlotBytes == kRingBytes && 3 * kSlotBytes + kRawSlots * kRawBytes == kRingBytes, "ring");
+static_assert(5 * kSlotBytes == kRingBytes && 4 * kSlotBytes + kRawSlots * kRawBytes == kRingBytes, "ring");
 constexpr int kXmOff = kQBytes + kRingBytes;          // [2][2][128] floats: maxima of both halves, by tile parity
 constexpr int kQexpOff = kXmOff + 2 * 2 * kCtaRows * 4;   // [4][128] bytes: E4M3 pages, exponents of the rows' q
 constexpr int kChunkBarOff = kQexpOff + 4 * kCtaRows;
@@ -59,19 +58,21 @@ constexpr int kMinTiles = 2;                          // shortest share of a pai
 constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512, kOutCol = 256;
 
+// The products run in blocks: S(0); S(1); then O += P(k) V(k) and S(k + 2), for k = 0, 1, ..  One commit ends a
+// block, and block i is over when S(i) is complete and O holds P(i - 2) V(i - 2): that tells the softmax that its
+// scores are there, and the others which slots are free.
+//
 // Barriers (index into the barrier area).
 enum : int {
     BAR_FULL = 0,      // [5] a slot's (E4M3: a raw slot's) copies have landed in this CTA
     BAR_READY = 5,     // [5] first CTA: both CTAs' halves of a slot are ready for the MMAs
-    BAR_EMPTY = 10,    // [5] the MMAs that read a slot are complete
-    BAR_RAW_FREE = 15, // [4] a raw slot has been converted
-    BAR_Q_FULL = 19,   // the query rows have landed in this CTA
-    BAR_Q_READY = 20,  // first CTA: both CTAs' query rows are ready
-    BAR_Q_EMPTY = 21,  // the MMAs that read the query rows are complete
-    BAR_S = 22,        // [2] scores are complete
-    BAR_P = 24,        // [2] first CTA: the weights of both CTAs are written
-    BAR_PV = 26,       // [2] a tile's output product is complete (by tile parity: a wait is never two phases behind)
-    BAR_O_FREE = 28,   // first CTA: both CTAs have read an item's output
+    BAR_BLOCK = 10,    // [2] a block of products is complete, by its parity
+    BAR_RAW_FREE = 12, // [2] a raw slot has been converted
+    BAR_Q_FULL = 14,   // the query rows have landed in this CTA
+    BAR_Q_READY = 15,  // first CTA: both CTAs' query rows are ready
+    BAR_Q_EMPTY = 16,  // the MMAs that read the query rows are complete
+    BAR_P = 17,        // [2] first CTA: the weights of both CTAs are written
+    BAR_O_FREE = 19,   // first CTA: both CTAs have read an item's output
 };
 
 struct ChunkTile {
@@ -164,7 +165,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8;
     constexpr int S = num_slots(KV), kStage = stage_warps(KV);
-    uint8_t *ring = smem + kQBytes, *raw = ring + 3 * kSlotBytes;
+    uint8_t *ring = smem + kQBytes, *raw = ring + 4 * kSlotBytes;
     float *xm = reinterpret_cast<float *>(smem + kXmOff);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChunkBarOff);
     int *misc = reinterpret_cast<int *>(smem + kChunkMiscOff);
@@ -263,16 +264,14 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         for (int i = 0; i < 5; ++i) {
             mbar_init(&bar[BAR_FULL + i], 1);
             mbar_init(&bar[BAR_READY + i], 2 * kStage);
-            mbar_init(&bar[BAR_EMPTY + i], 1);
         }
         for (int i = 0; i < kRawSlots; ++i) mbar_init(&bar[BAR_RAW_FREE + i], kStage);
         mbar_init(&bar[BAR_Q_FULL], 1);
         mbar_init(&bar[BAR_Q_READY], 2 * kStage);
         mbar_init(&bar[BAR_Q_EMPTY], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[BAR_S + i], 1);
+            mbar_init(&bar[BAR_BLOCK + i], 1);
             mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
-            mbar_init(&bar[BAR_PV + i], 1);
         }
         mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
         fence_mbar_init();
@@ -300,6 +299,9 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     w.start(a, c0, N);
     bool dead = false;
     const int ps = 1 << sq.page_shift;
+    // Whole-warp wait for the end of block i.  Every waiter waits for blocks in order and never two behind the last
+    // one over, so a parity is enough.
+    auto wait_block = [&](long long i) { wait_warp(&bar[BAR_BLOCK + (i & 1)], (uint32_t)(i >> 1) & 1, dead, err); };
 
     if (warp == kCopyWarp) {
         // ---- copies: K(0), K(1), V(0), K(2), V(1), ... ----
@@ -329,6 +331,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 nx.next(a);
                 pg_next = pages_of(nx);
             }
+            // bf16 pages: K(i) takes the slot of V(i - 4) and V(i - 1) that of K(i - 2), both read by block i - 2.
+            if (!kFp8 && i >= 3) wait_block(i - 2);
             if (i < N) {
                 if (w.fresh) {
                     if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
 #pragma unroll
             for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
                 if (kind == 0 ? i >= N : i == 0) continue;
-                if (!pos.first) wait_warp(&bar[(kFp8 ? BAR_RAW_FREE : BAR_EMPTY) + pos.st], pos.ph ^ 1, dead, err);
+                if (kFp8 && !pos.first) wait_warp(&bar[BAR_RAW_FREE + pos.st], pos.ph ^ 1, dead, err);
                 uint8_t *dst = kFp8 ? raw + pos.st * kRawBytes : ring + pos.st * kSlotBytes;
                 uint64_t *full = &bar[BAR_FULL + pos.st];
                 const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
@@ -384,64 +388,59 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             w = nx;
         }
     } else if (warp == kMmaWarp) {
-        // ---- products: S(0), S(1), O(0), S(2), O(1), ... ----
+        // ---- products, block by block ----
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdS = pair_idesc(128, !kFp8, 0), kIdO = pair_idesc(256, !kFp8, 1);
             const int rv_shift = kFp8 ? 7 : min(sq.page_shift, 7);
             const uint64_t qd0 = umma_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t kd0 = umma_desc(smem_u32(ring), 16, 1024, 2);
             const uint64_t vd0 = umma_desc(smem_u32(ring), 128u << rv_shift, 1024, 2);
+            uint32_t v_step[8];   // offsets of a V slot's 16-key steps
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                v_step[t] = (((uint32_t)(16 * t) >> rv_shift << rv_shift) * 256 + ((uint32_t)(16 * t) & ((1u << rv_shift) - 1)) * 128) >> 4;
             RingPos<S> pos;
             uint32_t seg = 0, oseg = 0;
-            bool fresh_o = true;
-            for (long long i = 0; i <= N; ++i) {
-                const bool fresh_s = w.fresh, last_s = w.last();
-                if (i < N) {
-                    if (fresh_s) {
-                        wait_thread(&bar[BAR_Q_READY], seg & 1, dead, err);
-                        ++seg;
+            bool fresh_o = false, fresh_next = false;   // whether tiles i - 2 and i - 1 begin a segment
+            for (long long i = 0; i < N + 2; ++i) {
+                const bool fresh_s = i < N && w.fresh, last_s = i < N && w.last();
+                if (i >= 2) {
+                    const long long j = i - 2;
+                    if (fresh_o) {
+                        if (oseg) wait_thread(&bar[BAR_O_FREE], (oseg - 1) & 1, dead, err);
+                        ++oseg;
                     }
-                    const int st = pos.st;
-                    wait_thread(&bar[BAR_READY + st], pos.ph, dead, err);
-                    pos.step();
+                    wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
+                    wait_thread(&bar[BAR_P + (j & 1)], (uint32_t)(j >> 1) & 1, dead, err);
                     tc_fence_after();
-                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * kSlotBytes >> 4);
+                    const uint64_t vd = vd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
+                    const uint32_t p = tmem + (uint32_t)(j & 1) * 128;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, !(fresh_o && t == 0));
+                    pos.step();
+                }
+                if (i < N) {
+                    if (fresh_s) wait_thread(&bar[BAR_Q_READY], seg++ & 1, dead, err);
+                    wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
+                    tc_fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
                     const uint32_t d = tmem + (uint32_t)(i & 1) * 128;
 #pragma unroll
                     for (int kk = 0; kk < 16; ++kk)
                         pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                                     kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
-                    pair_commit(&bar[BAR_EMPTY + st]);
-                    pair_commit(&bar[BAR_S + (i & 1)]);
-                    if (last_s) pair_commit(&bar[BAR_Q_EMPTY]);
-                }
-                if (i > 0) {
-                    const long long j = i - 1;
-                    if (fresh_o) {
-                        if (oseg) wait_thread(&bar[BAR_O_FREE], (oseg - 1) & 1, dead, err);
-                        ++oseg;
-                    }
-                    const int st = pos.st;
-                    wait_thread(&bar[BAR_READY + st], pos.ph, dead, err);
                     pos.step();
-                    wait_thread(&bar[BAR_P + (j & 1)], (uint32_t)(j >> 1) & 1, dead, err);
-                    tc_fence_after();
-                    const uint32_t p = tmem + (uint32_t)(j & 1) * 128;
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const uint32_t run = (uint32_t)(16 * t) >> rv_shift, in = (uint32_t)(16 * t) & ((1u << rv_shift) - 1);
-                        const uint32_t off = (uint32_t)st * kSlotBytes + (run << rv_shift) * 256 + in * 128;
-                        pair_mma_ts(tmem + kOutCol, p + 8 * t, vd0 + (uint64_t)(off >> 4), kIdO, !(fresh_o && t == 0));
-                    }
-                    pair_commit(&bar[BAR_EMPTY + st]);
-                    pair_commit(&bar[BAR_PV + (j & 1)]);
                 }
-                fresh_o = fresh_s;
+                pair_commit(&bar[BAR_BLOCK + (i & 1)]);
+                if (last_s) pair_commit(&bar[BAR_Q_EMPTY]);
+                fresh_o = fresh_next;
+                fresh_next = fresh_s;
                 if (i + 1 < N) w.next(a);
             }
         }
     } else if (warp >= kStageWarp) {
-        // ---- stages: hand K(0), K(1), V(0), ... on to the MMA warp ----
+        // ---- stages: hand K(0), K(1), V(0), ... on to the MMAs ----
         const int st_tid = tid - kStageWarp * 32;
         const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
         const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
@@ -490,7 +489,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 if (kFp8) {
                     const uint8_t *src = raw + raw_pos.st * kRawBytes;
                     wait_warp(&bar[BAR_FULL + raw_pos.st], raw_pos.ph, dead, err);
-                    if (!pos.first) wait_warp(&bar[BAR_EMPTY + pos.st], pos.ph ^ 1, dead, err);
+                    // K(i) takes the slot of K(i - 2), V(i - 1) that of V(i - 3) (read by block i - 1).
+                    if (kind == 0 ? i >= 3 : i >= 2) wait_block(kind == 0 ? i - 2 : i - 1);
                     // 1024 chunks of 16 codes: 64 keys x 16 (K), 128 keys x 8 (V); a warp's lanes take 32 rows of
                     // one chunk column, which the swizzle spreads over all banks.
 #pragma unroll
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             }
             const bool idle = (warp & 3) * 32 >= rows_here;   // none of this warp's rows exists
             const uint32_t buf = lanes + (uint32_t)(g & 1) * 128;
-            wait_warp(&bar[BAR_S + (g & 1)], (uint32_t)(g >> 1) & 1, dead, err);
+            wait_block(g);
             if (w.fresh) {
                 if (kFp8) {
                     const uint32_t ex = smem[kQexpOff + (seg & 3) * kCtaRows + row];
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     l *= alpha;
                 }
                 if (w.u != seg_u0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    wait_warp(&bar[BAR_PV + ((g - 1) & 1)], (uint32_t)((g - 1) >> 1) & 1, dead, err);
+                    wait_block(g + 1);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     l += x[(half ^ 1) * kCtaRows + row];
                     pair_sync();
                 }
-                wait_warp(&bar[BAR_PV + (g & 1)], (uint32_t)(g >> 1) & 1, dead, err);
+                wait_block(g + 2);
                 tc_fence_after();
                 const bool whole = seg_u0 == 0 && w.seg_end == w.t.units;
                 const bool live = row < rows_here;
