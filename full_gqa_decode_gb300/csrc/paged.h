@@ -51,6 +51,8 @@ struct PagedAttnArgs {
     const __nv_bfloat16 *q;    // rotated [num_tokens][Hq][D]
     const int32_t *selected;
     int32_t num_selected;
+    const uint8_t *k_codes, *v_codes;   // E4M3 pages (the chunk kernel reads them without a tensor map)
+    int64_t page_stride;                // elements
     const float *k_scale, *v_scale;
     const float *sink, *gate;
     __nv_bfloat16 *out;

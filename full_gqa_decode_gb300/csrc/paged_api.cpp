@@ -88,6 +88,9 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     a.q = static_cast<const __nv_bfloat16 *>(q_rot);
     a.selected = selected;
     a.num_selected = num_selected;
+    a.k_codes = static_cast<const uint8_t *>(c.k);
+    a.v_codes = static_cast<const uint8_t *>(c.v);
+    a.page_stride = c.page_stride;
     a.k_scale = c.k_scale;
     a.v_scale = c.v_scale;
     a.sink = sink;
@@ -111,13 +114,13 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     const int Hkv = ctx->cfg.num_kv_heads, all = kv_boxes_per_row(ctx->kv_type), ps = c.page_size;
     const bool fp8 = ctx->kv_type == KV_FP8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap km, vm, qm;
+    CUtensorMap km{}, vm{}, qm{};
     hd_status st;
     if (chunk) {
         const int krows = std::min(ps, kChunkKeys / 2), vrows = std::min(ps, kChunkKeys);
-        const int kgroups = fp8 || krows == kChunkKeys / 2 ? all : 1;
-        if (!encode_pages(&km, c.k, c, Hkv, ctx->kv_type, krows, kgroups) ||
-            !encode_pages(&vm, c.v, c, Hkv, ctx->kv_type, vrows, all / 2) ||
+        const int kgroups = krows == kChunkKeys / 2 ? all : 1;
+        if ((!fp8 && (!encode_pages(&km, c.k, c, Hkv, ctx->kv_type, krows, kgroups) ||
+                      !encode_pages(&vm, c.v, c, Hkv, ctx->kv_type, vrows, all / 2))) ||
             !encode_queries(&qm, q_rot, ctx->cfg.num_q_heads, seqs.num_tokens, ctx->group))
             return HD_ERR_CUDA;
         st = cuda_status(launch_paged_chunk(&qm, &km, &vm, a, s));

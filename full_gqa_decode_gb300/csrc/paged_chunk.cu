@@ -22,8 +22,8 @@
 // MMA warp (only the first CTA's issues; its barriers collect the arrivals of
 // both CTAs); and stage warps, which hand a landed stage on to the MMA warp:
 // with bf16 pages one warp, which only zeroes the V rows of positions that no
-// row sees (they may hold NaN); with E4M3 pages four warps, which convert the
-// codes to f16 (exact) in the layout of the MMAs.
+// row sees (they may hold NaN); with E4M3 pages four warps, which read the codes
+// and convert them to f16 (exact) in the layout of the MMAs.
 //
 // Rows keep the reference m of their weights until a score passes it by 8 (in
 // log2 units), and only then is the output in tensor memory rescaled: weights
@@ -42,12 +42,8 @@ __host__ __device__ constexpr int stage_warps(int kv) { return kv == KV_FP8 ? 4 
 __host__ __device__ constexpr int chunk_threads(int kv) { return (kStageWarp + stage_warps(kv)) * 32; }
 constexpr int kQBytes = kCtaRows * kHeadDim * 2;      // 64 KiB
 constexpr int kSlotBytes = 32 * 1024;                 // this CTA's half of a K or V tile in 16 bits
-constexpr int kRawBytes = 16 * 1024;                  // ... in E4M3 codes
-__host__ __device__ constexpr int num_slots(int kv) { return kv == KV_FP8 ? 4 : 5; }
-constexpr int kRawSlots = 2;
-constexpr int kRingBytes = 160 * 1024;
-static_assert(5 * kSlotBytes == kRingBytes && 4 * kSlotBytes + kRawSlots * kRawBytes == kRingBytes, "ring");
-constexpr int kXmOff = kQBytes + kRingBytes;          // [2][2][128] floats: maxima of both halves, by tile parity
+constexpr int kSlots = 5;
+constexpr int kXmOff = kQBytes + kSlots * kSlotBytes;          // [2][2][128] floats: maxima of both halves, by tile parity
 constexpr int kQexpOff = kXmOff + 2 * 2 * kCtaRows * 4;   // [4][128] bytes: E4M3 pages, exponents of the rows' q
 constexpr int kChunkBarOff = kQexpOff + 4 * kCtaRows;
 constexpr int kChunkBars = 32;
@@ -64,10 +60,9 @@ constexpr uint32_t kTmemCols = 512, kOutCol = 256;
 //
 // Barriers (index into the barrier area).
 enum : int {
-    BAR_FULL = 0,      // [5] a slot's (E4M3: a raw slot's) copies have landed in this CTA
+    BAR_FULL = 0,      // [5] a slot's copies have landed in this CTA (bf16 pages)
     BAR_READY = 5,     // [5] first CTA: both CTAs' halves of a slot are ready for the MMAs
     BAR_BLOCK = 10,    // [2] a block of products is complete, by its parity
-    BAR_RAW_FREE = 12, // [2] a raw slot has been converted
     BAR_Q_FULL = 14,   // the query rows have landed in this CTA
     BAR_Q_READY = 15,  // first CTA: both CTAs' query rows are ready
     BAR_Q_EMPTY = 16,  // the MMAs that read the query rows are complete
@@ -249,8 +244,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8;
-    constexpr int S = num_slots(KV), kStage = stage_warps(KV);
-    uint8_t *ring = smem + kQBytes, *raw = ring + 4 * kSlotBytes;
+    constexpr int kStage = stage_warps(KV);
+    uint8_t *ring = smem + kQBytes;
     float *xm = reinterpret_cast<float *>(smem + kXmOff);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChunkBarOff);
     int *misc = reinterpret_cast<int *>(smem + kChunkMiscOff);
@@ -261,11 +256,10 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     int32_t *err = sq.err;
 
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&bar[BAR_FULL + i], 1);
             mbar_init(&bar[BAR_READY + i], 2 * kStage);
         }
-        for (int i = 0; i < kRawSlots; ++i) mbar_init(&bar[BAR_RAW_FREE + i], kStage);
         mbar_init(&bar[BAR_Q_FULL], 1);
         mbar_init(&bar[BAR_Q_READY], 2 * kStage);
         mbar_init(&bar[BAR_Q_EMPTY], 1);
@@ -300,28 +294,39 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     bool dead = false;
     const int ps = 1 << sq.page_shift;
     // Whole-warp wait for the end of block i.  Every waiter waits for blocks in order and never two behind the last
-    // one over, so a parity is enough.
+    // one over (a later block needs what the waiter does next), so a parity is enough.
     auto wait_block = [&](long long i) { wait_warp(&bar[BAR_BLOCK + (i & 1)], (uint32_t)(i >> 1) & 1, dead, err); };
+    // Before operands K(i) and V(i - 1) are put into their slots.  From i = 3 on K(i) takes that of V(i - 4) and V(i - 1)
+    // that of K(i - 2), both read by block i - 2.  The last V (i = N) waits for block N - 1 instead: block N does
+    // without that V and could be over before a wait for N - 2, which its parity then could not tell.  For N = 3 that is
+    // block 2, with which block 0 shares its barrier and which only a wait for block 0 tells from it.
+    auto wait_slots = [&](long long i) {
+        if (i >= 3 || (i == 2 && N == 3)) wait_block(i < N ? i - 2 : N - 1);
+    };
+    // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
+    auto pages_of = [&](const Walk &x) {
+        const int pos = x.key0() + 16 * (lane & 7), first = pos & ~(ps - 1);
+        int page = sq.num_pages;
+        if (first < x.t.hi && first + ps > x.t.lo) {
+            page = sq.table[(size_t)x.b * sq.table_stride + (pos >> sq.page_shift)];
+            if (page < 0 || page >= sq.num_pages) {
+                atomicOr(err, HD_DEVERR_PAGE);
+                page = sq.num_pages;
+            }
+        }
+        return page;
+    };
 
     if (warp == kCopyWarp) {
-        // ---- copies: K(0), K(1), V(0), K(2), V(1), ... ----
+        // ---- copies: K(0), K(1), V(0), K(2), V(1), ..; each item's query rows before its first K.  E4M3 pages are
+        // read by the stage warps.
         const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
-        const int tok = kCtaRows / a.group;
-        // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
-        auto pages_of = [&](const Walk &x) {
-            const int pos = x.key0() + 16 * (lane & 7), first = pos & ~(ps - 1);
-            int page = sq.num_pages;
-            if (first < x.t.hi && first + ps > x.t.lo) {
-                page = sq.table[(size_t)x.b * sq.table_stride + (pos >> sq.page_shift)];
-                if (page < 0 || page >= sq.num_pages) {
-                    atomicOr(err, HD_DEVERR_PAGE);
-                    page = sq.num_pages;
-                }
-            }
-            return page;
-        };
-        int pg = pages_of(w), pg_v = 0, key_v = 0, h_v = 0;
-        RingPos<kFp8 ? kRawSlots : S> pos;
+        // bf16 pages of fewer than 64 slots: a K copy per column group, so that the 64 keys' rows of a group lie
+        // together as the MMA wants them.
+        const bool split = rk_shift < 6;
+        const int tok = kCtaRows >> a.group_shift;
+        int pg = kFp8 ? 0 : pages_of(w), pg_v = 0, key_v = 0, h_v = 0;
+        RingPos<kSlots> pos;
         int issued = 0;
         uint32_t seg = 0;
         for (long long i = 0; i <= N; ++i) {
@@ -329,57 +334,40 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             Walk nx = w;
             if (i + 1 < N) {
                 nx.next(a);
-                pg_next = pages_of(nx);
+                if (!kFp8) pg_next = pages_of(nx);
             }
-            // bf16 pages: K(i) takes the slot of V(i - 4) and V(i - 1) that of K(i - 2), both read by block i - 2.
-            if (!kFp8 && i >= 3) wait_block(i - 2);
-            if (i < N) {
-                if (w.fresh) {
-                    if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
-                    if (lane == 0 && !dead) {
-                        mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
-                        tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h * a.group, w.q.row0 + w.t.t0 + rank * tok, 0);
-                    }
-                    ++seg;
+            if (!kFp8) wait_slots(i);
+            if (i < N && w.fresh) {
+                if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
+                if (lane == 0 && !dead) {
+                    mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
+                    tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h << a.group_shift, w.q.row0 + w.t.t0 + rank * tok, 0);
                 }
+                ++seg;
             }
+            if (!kFp8) {
 #pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
-                if (kind == 0 ? i >= N : i == 0) continue;
-                if (kFp8 && !pos.first) wait_warp(&bar[BAR_RAW_FREE + pos.st], pos.ph ^ 1, dead, err);
-                uint8_t *dst = kFp8 ? raw + pos.st * kRawBytes : ring + pos.st * kSlotBytes;
-                uint64_t *full = &bar[BAR_FULL + pos.st];
-                const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
-                if (!drop && lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kRawBytes : kSlotBytes);
-                __syncwarp();
-                const int key0 = kind == 0 ? w.key0() + 64 * rank : key_v;
-                const int head = kind == 0 ? w.h : h_v, src_pg = kind == 0 ? pg : pg_v;
-                int run, col = 0, group16, total;
-                uint32_t off;
-                if (kind == 0) {
-                    // bf16 pages of fewer than 64 slots: a copy per column group, so that the 64 keys' rows of a
-                    // group lie together as the MMA wants them.
-                    const bool split = !kFp8 && rk_shift < 6;
-                    run = split ? lane >> 2 : lane;
-                    col = split ? lane & 3 : 0;
-                    total = (64 >> rk_shift) * (split ? 4 : 1);
-                    off = split ? col * 8192 + (run << rk_shift) * 128
-                                : (uint32_t)(run << rk_shift) * (kFp8 ? kHeadDim : 2 * kHeadDim);
-                    group16 = 4 * rank + ((run << rk_shift) >> 4);
-                } else {
-                    run = lane;
-                    total = 128 >> rv_shift;
-                    off = (uint32_t)(run << rv_shift) * (kFp8 ? 128 : 256);
-                    col = kFp8 ? rank : 2 * rank;
-                    group16 = (run << rv_shift) >> 4;
+                for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
+                    if (kind == 0 ? i >= N : i == 0) continue;
+                    uint8_t *dst = ring + pos.st * kSlotBytes;
+                    uint64_t *full = &bar[BAR_FULL + pos.st];
+                    const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
+                    if (!drop && lane == 0) mbar_arrive_expect_tx(full, kSlotBytes);
+                    __syncwarp();
+                    const int shift = kind == 0 ? rk_shift : rv_shift;
+                    const int run = kind == 0 && split ? lane >> 2 : lane;
+                    const int col = kind == 0 ? (split ? lane & 3 : 0) : 2 * rank;
+                    const int total = kind == 0 ? (64 >> rk_shift) * (split ? 4 : 1) : 128 >> rv_shift;
+                    const uint32_t off = kind == 0 ? (split ? col * 8192 + (run << shift) * 128 : 0) : (run << shift) * 256;
+                    const int first = (kind == 0 ? 64 * rank : 0) + (run << shift);   // of this copy's keys in the tile
+                    const int page = __shfl_sync(0xffffffffu, kind == 0 ? pg : pg_v, (first >> 4) & 7);
+                    if (!drop && lane < total) {
+                        const int slot = ((kind == 0 ? w.key0() : key_v) + first) & (ps - 1);
+                        tma_load_5d(dst + off, kind == 0 ? &maps.k : &maps.v, full, 0, slot, col, kind == 0 ? w.h : h_v, page);
+                    }
+                    ++issued;
+                    pos.step();
                 }
-                const int page = __shfl_sync(0xffffffffu, src_pg, group16 & 7);
-                if (!drop && lane < total) {
-                    const int slot = (key0 + (run << (kind == 0 ? rk_shift : rv_shift))) & (ps - 1);
-                    tma_load_5d(dst + off, kind == 0 ? &maps.k : &maps.v, full, 0, slot, col, head, page);
-                }
-                ++issued;
-                pos.step();
             }
             pg_v = pg;
             key_v = w.key0();
@@ -399,7 +387,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
 #pragma unroll
             for (int t = 0; t < 8; ++t)
                 v_step[t] = (((uint32_t)(16 * t) >> rv_shift << rv_shift) * 256 + ((uint32_t)(16 * t) & ((1u << rv_shift) - 1)) * 128) >> 4;
-            RingPos<S> pos;
+            RingPos<kSlots> pos;
             uint32_t seg = 0, oseg = 0;
             bool fresh_o = false, fresh_next = false;   // whether tiles i - 2 and i - 1 begin a segment
             for (long long i = 0; i < N + 2; ++i) {
@@ -443,12 +431,61 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         // ---- stages: hand K(0), K(1), V(0), ... on to the MMAs ----
         const int st_tid = tid - kStageWarp * 32;
         const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
-        const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
-        RingPos<S> pos;
-        RingPos<kRawSlots> raw_pos;
+        const int rv_shift = min(sq.page_shift, 7);
+        RingPos<kSlots> pos;
         uint32_t seg = 0;
         int key_v = 0, lo_v = 0, hi_v = 0;
+        // E4M3: the codes of the next K and V operands wait in registers, eight 16-byte chunks a thread -- each set is
+        // under way while the other is converted.  A warp's lanes take two (K) or four (V) whole rows at a time, in an
+        // order that makes both the reads whole lines and the f16 stores free of bank conflicts: of eight lanes, four
+        // take neighbouring chunks of a row and four those of the row beside it.
+        const int sw = warp - kStageWarp;
+        uint4 ck[8], cv[8];
+        const int row2 = (lane >> 2) & 1;
+        auto k_row = [&](int s) { return s * 8 + sw * 2 + row2; };                       // 64 keys x 16 chunks
+        auto v_row = [&](int s) { return s * 16 + sw * 4 + row2 + 2 * (lane >> 4); };    // 128 keys x 8 chunks
+        const int k_chunk = (lane & 3) | (lane >> 3 << 2), v_chunk = (lane & 3) | (lane >> 3 & 1) << 2;
+        auto load_k = [&](const Walk &x, int pg) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int key = 64 * rank + k_row(s), page = __shfl_sync(0xffffffffu, pg, key >> 4);
+                const size_t at = (size_t)page * a.page_stride +
+                                  (((size_t)x.h << sq.page_shift) + ((x.key0() + key) & (ps - 1))) * kHeadDim + 16 * k_chunk;
+                ck[s] = page < sq.num_pages ? __ldcg(reinterpret_cast<const uint4 *>(a.k_codes + at)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        auto load_v = [&](const Walk &x, int pg) {   // rows of positions that no query row sees: zero
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int key = v_row(s), page = __shfl_sync(0xffffffffu, pg, key >> 4), p = x.key0() + key;
+                const size_t at = (size_t)page * a.page_stride +
+                                  (((size_t)x.h << sq.page_shift) + (p & (ps - 1))) * kHeadDim + 128 * rank + 16 * v_chunk;
+                cv[s] = page < sq.num_pages && p >= x.t.lo && p < x.t.hi
+                            ? __ldcg(reinterpret_cast<const uint4 *>(a.v_codes + at)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        auto put = [&](uint8_t *slot, const uint4 &x, int row, int c, uint32_t col) {
+            const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] = e4m3x2_to_f16x2((uint16_t)(cw[j] & 0xFFFFu));
+                f[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(cw[j] >> 16));
+            }
+            uint8_t *dst = slot + (uint32_t)(c >> 2) * col + (uint32_t)row * 128;
+            *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3)) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+        };
+        int pg = 0;
+        if (kFp8) {
+            pg = pages_of(w);
+            load_k(w, pg);
+            load_v(w, pg);
+        }
         for (long long i = 0; i <= N; ++i) {
+            const int pg_w = pg;   // pages of tile i
+            Walk nx = w;
+            if (i + 1 < N) nx.next(a);
             if (i < N && w.fresh) {
                 wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
                 if (kFp8) {
@@ -482,37 +519,23 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 if (lane == 0) mbar_arrive_remote(q_ready);
                 ++seg;
             }
+            if (kFp8) wait_slots(i);
 #pragma unroll
             for (int kind = 0; kind < 2; ++kind) {
                 if (kind == 0 ? i >= N : i == 0) continue;
                 uint8_t *slot = ring + pos.st * kSlotBytes;
                 if (kFp8) {
-                    const uint8_t *src = raw + raw_pos.st * kRawBytes;
-                    wait_warp(&bar[BAR_FULL + raw_pos.st], raw_pos.ph, dead, err);
-                    // K(i) takes the slot of K(i - 2), V(i - 1) that of V(i - 3) (read by block i - 1).
-                    if (kind == 0 ? i >= 3 : i >= 2) wait_block(kind == 0 ? i - 2 : i - 1);
-                    // 1024 chunks of 16 codes: 64 keys x 16 (K), 128 keys x 8 (V); a warp's lanes take 32 rows of
-                    // one chunk column, which the swizzle spreads over all banks.
+                    if (kind == 0) {
 #pragma unroll
-                    for (int c0 = 0; c0 < 8; ++c0) {
-                        const int unit = c0 * (kStage * 32) + st_tid;
-                        const int row = kind == 0 ? unit & 63 : unit & 127, c = kind == 0 ? unit >> 6 : unit >> 7;
-                        const uint32_t at = kind == 0 ? (uint32_t)(row >> rk_shift << rk_shift) * kHeadDim +
-                                                            (uint32_t)(c >> 3) * (128u << rk_shift) +
-                                                            (uint32_t)(row & ((1 << rk_shift) - 1)) * 128
-                                                      : (uint32_t)row * 128;
-                        uint4 x = *reinterpret_cast<const uint4 *>(src + at + (((c & 7) ^ (row & 7)) << 4));
-                        if (kind == 1 && (key_v + row < lo_v || key_v + row >= hi_v)) x = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t f[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f[2 * j] = e4m3x2_to_f16x2((uint16_t)(cw[j] & 0xFFFFu));
-                            f[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(cw[j] >> 16));
+                        for (int s = 0; s < 8; ++s) put(slot, ck[s], k_row(s), k_chunk, 8192);
+                        if (i + 1 < N) {
+                            pg = pages_of(nx);
+                            load_k(nx, pg);
                         }
-                        uint8_t *dst = slot + (uint32_t)(c >> 2) * (kind == 0 ? 8192u : 16384u) + (uint32_t)row * 128;
-                        *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3)) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-                        *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) put(slot, cv[s], v_row(s), v_chunk, 16384);
+                        if (i < N) load_v(w, pg_w);
                     }
                 } else {
                     wait_warp(&bar[BAR_FULL + pos.st], pos.ph, dead, err);
@@ -529,17 +552,13 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    if (kFp8) mbar_arrive(&bar[BAR_RAW_FREE + raw_pos.st]);
-                    mbar_arrive_remote(ready0 + 8 * pos.st);
-                }
-                raw_pos.step();
+                if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
                 pos.step();
             }
             key_v = w.key0();
             lo_v = w.t.lo;
             hi_v = w.t.hi;
-            if (i + 1 < N) w.next(a);
+            w = nx;
         }
     } else {
         // ---- softmax: thread (row, half of the tile's keys) ----
