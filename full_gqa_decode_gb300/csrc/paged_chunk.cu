@@ -22,8 +22,9 @@
 // MMA warp (only the first CTA's issues; its barriers collect the arrivals of
 // both CTAs); and stage warps, which hand a landed stage on to the MMA warp:
 // with bf16 pages one warp, which only zeroes the V rows of positions that no
-// row sees (they may hold NaN); with E4M3 pages four warps, which read the codes
-// and convert them to f16 (exact) in the layout of the MMAs.
+// row sees (they may hold NaN); with E4M3 pages four warps for K and four for V,
+// which read the codes a tile ahead into registers and convert them to f16
+// (exact) in the layout of the MMAs.
 //
 // Rows keep the reference m of their weights until a score passes it by 8 (in
 // log2 units), and only then is the output in tensor memory rescaled: weights
@@ -37,9 +38,18 @@ namespace hd {
 namespace {
 
 constexpr int kTileRows = kChunkRows, kCtaRows = kTileRows / 2, kTileKeys = kChunkKeys, kKeyShift = 7;
-constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kStageWarp = kSoftWarps + 2;
+constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+// Stage warps: one behind the MMA warp (bf16); two groups of four, for K and for V operands, at the next multiple of
+// four warps (E4M3).  kStage: those that hand on one operand.
+__host__ __device__ constexpr int first_stage_warp(int kv) { return kv == KV_FP8 ? kSoftWarps + 4 : kSoftWarps + 2; }
 __host__ __device__ constexpr int stage_warps(int kv) { return kv == KV_FP8 ? 4 : 1; }
-__host__ __device__ constexpr int chunk_threads(int kv) { return (kStageWarp + stage_warps(kv)) * 32; }
+__host__ __device__ constexpr int chunk_threads(int kv) {
+    return (first_stage_warp(kv) + (kv == KV_FP8 ? 2 : 1) * stage_warps(kv)) * 32;
+}
+// E4M3: 640 threads launch with 96 registers each; the groups of four warps then share them out by need.
+// 256 x 128 + 128 x 56 + 256 x 80 <= 640 x 96.
+constexpr int kSoftRegs = 128, kMiscRegs = 56, kStageRegs = 80;
+static_assert(256 * kSoftRegs + 128 * kMiscRegs + 256 * kStageRegs <= 640 * 96, "a split above the launch's total never ends");
 constexpr int kQBytes = kCtaRows * kHeadDim * 2;      // 64 KiB
 constexpr int kSlotBytes = 32 * 1024;                 // this CTA's half of a K or V tile in 16 bits
 constexpr int kSlots = 5;
@@ -50,24 +60,33 @@ constexpr int kChunkBars = 32;
 constexpr int kChunkMiscOff = kChunkBarOff + kChunkBars * 8;
 constexpr int kChunkSmem = kChunkMiscOff + 64;
 constexpr int kMaxPairs = 96;                         // pieces of an item a warp can weigh in registers
-constexpr int kMinTiles = 2;                          // shortest share of a pair
+// What an item costs besides its key tiles, in tiles: its query rows and the drain of its output (about 3 us to a
+// tile's 1.7).  Shares are cut by tiles plus this; short items (the first rows of a causal prompt) would otherwise
+// pile up in a few shares.
+constexpr int kItemCost = 2;
+constexpr int kMinTiles = 2 + kItemCost;              // shortest share of a pair
 constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512, kOutCol = 256;
 
-// The products run in blocks: S(0); S(1); then O += P(k) V(k) and S(k + 2), for k = 0, 1, ..  One commit ends a
-// block, and block i is over when S(i) is complete and O holds P(i - 2) V(i - 2): that tells the softmax that its
-// scores are there, and the others which slots are free.
+// A segment -- a pair's part of an item, L key tiles -- runs in blocks of products: S(0); S(1) ; then O += P(k) V(k)
+// and S(k + 2) for k = 0, 1, ..; at its end two blocks of O alone.  One commit ends a block, and block b of a segment
+// is over when S(b) is complete and O holds P(b - 2) V(b - 2): it tells the softmax that its scores are there, and the
+// copies which slots are free.  Blocks are counted on through the segments, L + 2 for each; segments do not overlap,
+// as the next one's query rows take the place of this one's.
 //
-// Barriers (index into the barrier area).
+// Barriers (index into the barrier area).  A parity tells neighbouring phases apart only, so every wait is for a
+// phase that the barrier cannot yet have left behind: the phase after it needs something that the waiter does next.
 enum : int {
     BAR_FULL = 0,      // [5] a slot's copies have landed in this CTA (bf16 pages)
     BAR_READY = 5,     // [5] first CTA: both CTAs' halves of a slot are ready for the MMAs
-    BAR_BLOCK = 10,    // [2] a block of products is complete, by its parity
-    BAR_Q_FULL = 14,   // the query rows have landed in this CTA
-    BAR_Q_READY = 15,  // first CTA: both CTAs' query rows are ready
-    BAR_Q_EMPTY = 16,  // the MMAs that read the query rows are complete
-    BAR_P = 17,        // [2] first CTA: the weights of both CTAs are written
-    BAR_O_FREE = 19,   // first CTA: both CTAs have read an item's output
+    BAR_EMPTY = 10,    // [5] the MMAs that read a slot are complete (E4M3 pages)
+    BAR_BLOCK = 15,    // [2] a block of products is complete, by its parity
+    BAR_Q_FULL = 17,   // the query rows have landed in this CTA
+    BAR_Q_READY = 18,  // first CTA: both CTAs' query rows are ready
+    BAR_Q_EMPTY = 19,  // the MMAs that read the query rows are complete
+    BAR_P = 20,        // [2] first CTA: the weights of both CTAs are written, by the tile's parity
+    BAR_O_FULL = 22,   // a segment's output is complete
+    BAR_O_FREE = 23,   // first CTA: both CTAs have read it
 };
 
 struct ChunkTile {
@@ -88,35 +107,29 @@ __device__ __forceinline__ int num_chunk_tiles(const PagedAttnArgs &a, int n) {
     return ((n << a.group_shift) + kTileRows - 1) / kTileRows;
 }
 
-// A walk over the tiles of a pair's share, item by item.
-struct Walk {
-    int b, tile, h, u;   // u: key tile within the item
+// A walk over the segments of a pair's share.
+struct Segment {
+    int b, tile, h;      // the item
     SeqSpan q;
     ChunkTile t;
-    int seg_end;         // key tile of the item where this pair's share of it ends
-    long long left;      // tiles of the share from this one on
-    bool fresh;          // first tile of a segment
+    int u, L;            // its key tiles [u, u + L) of the item's
+    int off, take, left; // units (tiles and item costs): before the segment in the item, of the segment, still to take
+    int done;            // units of the share before this item's `off`
 
-    __device__ void start(const PagedAttnArgs &a, const Start &at, long long share) {
-        b = at.b;
-        tile = at.tile;
-        h = at.h;
-        u = at.off;
-        int bit;
-        q = seq_span(a.seqs, b, &bit);
-        t = make_chunk_tile(a, q, tile);
-        left = share;
-        seg_end = (int)min((long long)t.units, u + left);
-        fresh = true;
+    __device__ bool settle(const PagedAttnArgs &a) {   // the next stretch that holds key tiles; false: the share is over
+        for (;;) {
+            take = min(t.units + kItemCost - off, left);
+            u = max(off - kItemCost, 0);
+            L = max(off + take - kItemCost, 0) - u;
+            if (L > 0) return true;
+            if (!advance(a)) return false;
+        }
     }
-    __device__ bool last() const { return u + 1 == seg_end; }
-    __device__ int key0() const { return (t.u0 + u) << kKeyShift; }
-    __device__ void next(const PagedAttnArgs &a) {   // only while left > 1
-        --left;
-        fresh = false;
-        if (++u < seg_end) return;
-        u = 0;
-        fresh = true;
+    __device__ bool advance(const PagedAttnArgs &a) {
+        left -= take;
+        done += take;
+        if (left <= 0) return false;
+        off = 0;
         if (++h == a.num_kv_heads) {
             h = 0;
             if (++tile == num_chunk_tiles(a, q.n)) {
@@ -128,19 +141,34 @@ struct Walk {
             }
             t = make_chunk_tile(a, q, tile);
         }
-        seg_end = (int)min((long long)t.units, left);
+        return true;
     }
+    __device__ bool start(const PagedAttnArgs &a, const Start &at, int share) {
+        b = at.b;
+        tile = at.tile;
+        h = at.h;
+        off = at.off;
+        left = share;
+        done = 0;
+        int bit;
+        q = seq_span(a.seqs, b, &bit);
+        t = make_chunk_tile(a, q, tile);
+        return settle(a);
+    }
+    __device__ bool next(const PagedAttnArgs &a) { return advance(a) && settle(a); }
+    __device__ int key0(int k) const { return (t.u0 + u + k) << kKeyShift; }   // first position of its tile k
 };
 
 // Position in a ring of slots: index and the parity of its current round.
 template <int N>
 struct RingPos {
     int st = 0;
-    uint32_t ph = 0;   // parity of the round that fills the slot
-    bool first = true;
-    __device__ void step() {
-        if (++st == N) {
-            st = 0;
+    uint32_t ph = 0;     // parity of the round that fills the slot
+    bool first = true;   // whether that is the first round
+    __device__ void step(int n = 1) {
+        st += n;
+        if (st >= N) {
+            st -= N;
             ph ^= 1;
             first = false;
         }
@@ -239,17 +267,24 @@ struct ChunkMaps {
     CUtensorMap q, k, v;
 };
 
+// A 16-byte load that stays in its place: eight addresses at once would not fit the stage warps' registers.
+__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 template <int KV>
 __global__ void __launch_bounds__(chunk_threads(KV), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8;
-    constexpr int kStage = stage_warps(KV);
+    constexpr int kStage = stage_warps(KV), kStageWarp = first_stage_warp(KV);
     uint8_t *ring = smem + kQBytes;
     float *xm = reinterpret_cast<float *>(smem + kXmOff);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChunkBarOff);
     int *misc = reinterpret_cast<int *>(smem + kChunkMiscOff);
-    uint32_t *taddr_s = reinterpret_cast<uint32_t *>(misc + 8);
+    uint32_t *taddr_s = reinterpret_cast<uint32_t *>(misc + 10);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const PagedSeqs &sq = a.seqs;
@@ -259,6 +294,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&bar[BAR_FULL + i], 1);
             mbar_init(&bar[BAR_READY + i], 2 * kStage);
+            mbar_init(&bar[BAR_EMPTY + i], 1);
         }
         mbar_init(&bar[BAR_Q_FULL], 1);
         mbar_init(&bar[BAR_Q_READY], 2 * kStage);
@@ -267,45 +303,44 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             mbar_init(&bar[BAR_BLOCK + i], 1);
             mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
         }
+        mbar_init(&bar[BAR_O_FULL], 1);
         mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
         fence_mbar_init();
     }
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
-    // This pair's share of the call's key tiles.
+    // This pair's share of the call.
     long long x0, x1, T;
     int n, bad;
     const Start c0 = find_share(
         sq, a.num_kv_heads, pair, pairs, kMinTiles, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_chunk_tiles(a, tokens); },
-        [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units; });
+        [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units + kItemCost; });
     if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
     if (x0 >= x1) return;   // both CTAs of the pair
+    long long *call = reinterpret_cast<long long *>(misc + 6);   // T and x0, which only cut items need again
+    if (tid == 0) {
+        call[0] = T;
+        call[1] = x0;
+        misc[5] = n;
+    }
     if (warp == kMmaWarp) pair_alloc(taddr_s);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();   // the peer's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *taddr_s;
-    const long long N = x1 - x0;
-    Walk w;
-    w.start(a, c0, N);
+    const int share = (int)(x1 - x0);
+    Segment w;
+    bool more = w.start(a, c0, share);   // no role has work when the share holds item costs alone
     bool dead = false;
     const int ps = 1 << sq.page_shift;
-    // Whole-warp wait for the end of block i.  Every waiter waits for blocks in order and never two behind the last
-    // one over (a later block needs what the waiter does next), so a parity is enough.
-    auto wait_block = [&](long long i) { wait_warp(&bar[BAR_BLOCK + (i & 1)], (uint32_t)(i >> 1) & 1, dead, err); };
-    // Before operands K(i) and V(i - 1) are put into their slots.  From i = 3 on K(i) takes that of V(i - 4) and V(i - 1)
-    // that of K(i - 2), both read by block i - 2.  The last V (i = N) waits for block N - 1 instead: block N does
-    // without that V and could be over before a wait for N - 2, which its parity then could not tell.  For N = 3 that is
-    // block 2, with which block 0 shares its barrier and which only a wait for block 0 tells from it.
-    auto wait_slots = [&](long long i) {
-        if (i >= 3 || (i == 2 && N == 3)) wait_block(i < N ? i - 2 : N - 1);
-    };
+    // Whole-warp wait for the end of block i.
+    auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 1)], (uint32_t)(i >> 1) & 1, dead, err); };
     // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
-    auto pages_of = [&](const Walk &x) {
-        const int pos = x.key0() + 16 * (lane & 7), first = pos & ~(ps - 1);
+    auto pages_of = [&](const Segment &x, int k) {
+        const int pos = x.key0(k) + 16 * (lane & 7), first = pos & ~(ps - 1);
         int page = sq.num_pages;
         if (first < x.t.hi && first + ps > x.t.lo) {
             page = sq.table[(size_t)x.b * sq.table_stride + (pos >> sq.page_shift)];
@@ -317,38 +352,36 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         return page;
     };
 
+    // E4M3: each group of four warps takes its registers on entry to its role.
+    if (warp >= kSoftWarps && warp < kStageWarp) {
+    if (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMiscRegs));
+
     if (warp == kCopyWarp) {
-        // ---- copies: K(0), K(1), V(0), K(2), V(1), ..; each item's query rows before its first K.  E4M3 pages are
-        // read by the stage warps.
+        // ---- copies: a segment's query rows, then K(0), K(1), V(0), K(2), V(1), .., V(L - 1) (E4M3 pages: the stage
+        // warps read those) ----
         const int rk_shift = min(sq.page_shift, 6), rv_shift = min(sq.page_shift, 7);
         // bf16 pages of fewer than 64 slots: a K copy per column group, so that the 64 keys' rows of a group lie
         // together as the MMA wants them.
         const bool split = rk_shift < 6;
         const int tok = kCtaRows >> a.group_shift;
-        int pg = kFp8 ? 0 : pages_of(w), pg_v = 0, key_v = 0, h_v = 0;
         RingPos<kSlots> pos;
-        int issued = 0;
-        uint32_t seg = 0;
-        for (long long i = 0; i <= N; ++i) {
-            int pg_next = 0;
-            Walk nx = w;
-            if (i + 1 < N) {
-                nx.next(a);
-                if (!kFp8) pg_next = pages_of(nx);
+        int issued = 0, blocks = 0;   // blocks: before this segment
+        for (uint32_t seg = 0; more; ++seg) {
+            int pg = kFp8 ? 0 : pages_of(w, 0), pg_v = 0;
+            if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
+            if (lane == 0 && !dead) {
+                mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
+                tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h << a.group_shift, w.q.row0 + w.t.t0 + rank * tok, 0);
             }
-            if (!kFp8) wait_slots(i);
-            if (i < N && w.fresh) {
-                if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
-                if (lane == 0 && !dead) {
-                    mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
-                    tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h << a.group_shift, w.q.row0 + w.t.t0 + rank * tok, 0);
-                }
-                ++seg;
-            }
-            if (!kFp8) {
+            for (int i = 0; !kFp8 && i <= w.L; ++i) {
+                const int pg_next = i + 1 < w.L ? pages_of(w, i + 1) : 0;
 #pragma unroll
                 for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
-                    if (kind == 0 ? i >= N : i == 0) continue;
+                    if (kind == 0 ? i >= w.L : i == 0) continue;
+                    // The operand is read by block r, the slot's last one by block r - 2 or before; block r - 2 is also
+                    // the last whose end a parity can tell, as block r does not end without this copy.
+                    const int r = blocks + (kind == 0 ? i : i + 1);
+                    if (r >= 3) wait_block(r - 2);
                     uint8_t *dst = ring + pos.st * kSlotBytes;
                     uint64_t *full = &bar[BAR_FULL + pos.st];
                     const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
@@ -362,18 +395,22 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     const int first = (kind == 0 ? 64 * rank : 0) + (run << shift);   // of this copy's keys in the tile
                     const int page = __shfl_sync(0xffffffffu, kind == 0 ? pg : pg_v, (first >> 4) & 7);
                     if (!drop && lane < total) {
-                        const int slot = ((kind == 0 ? w.key0() : key_v) + first) & (ps - 1);
-                        tma_load_5d(dst + off, kind == 0 ? &maps.k : &maps.v, full, 0, slot, col, kind == 0 ? w.h : h_v, page);
+                        const int slot = (w.key0(kind == 0 ? i : i - 1) + first) & (ps - 1);
+                        tma_load_5d(dst + off, kind == 0 ? &maps.k : &maps.v, full, 0, slot, col, w.h, page);
                     }
                     ++issued;
                     pos.step();
                 }
+                pg_v = pg;
+                pg = pg_next;
             }
-            pg_v = pg;
-            key_v = w.key0();
-            h_v = w.h;
-            pg = pg_next;
-            w = nx;
+            blocks += w.L + 2;
+            more = w.next(a);
+            if (more && lane == 0)   // the next segment's query rows into L2
+                asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                                 reinterpret_cast<uint64_t>(&maps.q)),
+                             "r"(0), "r"(w.h << a.group_shift), "r"(w.q.row0 + w.t.t0 + rank * tok), "r"(0)
+                             : "memory");
         }
     } else if (warp == kMmaWarp) {
         // ---- products, block by block ----
@@ -388,82 +425,55 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             for (int t = 0; t < 8; ++t)
                 v_step[t] = (((uint32_t)(16 * t) >> rv_shift << rv_shift) * 256 + ((uint32_t)(16 * t) & ((1u << rv_shift) - 1)) * 128) >> 4;
             RingPos<kSlots> pos;
-            uint32_t seg = 0, oseg = 0;
-            bool fresh_o = false, fresh_next = false;   // whether tiles i - 2 and i - 1 begin a segment
-            for (long long i = 0; i < N + 2; ++i) {
-                const bool fresh_s = i < N && w.fresh, last_s = i < N && w.last();
-                if (i >= 2) {
-                    const long long j = i - 2;
-                    if (fresh_o) {
-                        if (oseg) wait_thread(&bar[BAR_O_FREE], (oseg - 1) & 1, dead, err);
-                        ++oseg;
+            int blocks = 0, tiles = 0;   // before this segment
+            for (uint32_t seg = 0; more; ++seg) {
+                for (int i = 0; i < w.L + 2; ++i) {
+                    if (i >= 2) {
+                        const int g = tiles + i - 2;
+                        if (i == 2 && seg) wait_thread(&bar[BAR_O_FREE], (seg - 1) & 1, dead, err);
+                        wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
+                        wait_thread(&bar[BAR_P + (g & 1)], (uint32_t)(g >> 1) & 1, dead, err);
+                        tc_fence_after();
+                        const uint64_t vd = vd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
+                        const uint32_t p = tmem + (uint32_t)(g & 1) * 128;
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, i > 2 || t > 0);
+                        if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
+                        pos.step();
                     }
-                    wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
-                    wait_thread(&bar[BAR_P + (j & 1)], (uint32_t)(j >> 1) & 1, dead, err);
-                    tc_fence_after();
-                    const uint64_t vd = vd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
-                    const uint32_t p = tmem + (uint32_t)(j & 1) * 128;
+                    if (i < w.L) {
+                        if (i == 0) wait_thread(&bar[BAR_Q_READY], seg & 1, dead, err);
+                        wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
+                        tc_fence_after();
+                        const uint64_t kd = kd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
+                        const uint32_t d = tmem + (uint32_t)((tiles + i) & 1) * 128;
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, !(fresh_o && t == 0));
-                    pos.step();
+                        for (int kk = 0; kk < 16; ++kk)
+                            pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                        kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                        if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
+                        pos.step();
+                    }
+                    pair_commit(&bar[BAR_BLOCK + ((blocks + i) & 1)]);
+                    if (i == w.L - 1) pair_commit(&bar[BAR_Q_EMPTY]);
+                    if (i == w.L + 1) pair_commit(&bar[BAR_O_FULL]);
                 }
-                if (i < N) {
-                    if (fresh_s) wait_thread(&bar[BAR_Q_READY], seg++ & 1, dead, err);
-                    wait_thread(&bar[BAR_READY + pos.st], pos.ph, dead, err);
-                    tc_fence_after();
-                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
-                    const uint32_t d = tmem + (uint32_t)(i & 1) * 128;
-#pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)
-                        pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                                    kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
-                    pos.step();
-                }
-                pair_commit(&bar[BAR_BLOCK + (i & 1)]);
-                if (last_s) pair_commit(&bar[BAR_Q_EMPTY]);
-                fresh_o = fresh_next;
-                fresh_next = fresh_s;
-                if (i + 1 < N) w.next(a);
+                blocks += w.L + 2;
+                tiles += w.L;
+                more = w.next(a);
             }
         }
-    } else if (warp >= kStageWarp) {
-        // ---- stages: hand K(0), K(1), V(0), ... on to the MMAs ----
-        const int st_tid = tid - kStageWarp * 32;
-        const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
-        const int rv_shift = min(sq.page_shift, 7);
-        RingPos<kSlots> pos;
-        uint32_t seg = 0;
-        int key_v = 0, lo_v = 0, hi_v = 0;
-        // E4M3: the codes of the next K and V operands wait in registers, eight 16-byte chunks a thread -- each set is
-        // under way while the other is converted.  A warp's lanes take two (K) or four (V) whole rows at a time, in an
-        // order that makes both the reads whole lines and the f16 stores free of bank conflicts: of eight lanes, four
-        // take neighbouring chunks of a row and four those of the row beside it.
-        const int sw = warp - kStageWarp;
-        uint4 ck[8], cv[8];
-        const int row2 = (lane >> 2) & 1;
-        auto k_row = [&](int s) { return s * 8 + sw * 2 + row2; };                       // 64 keys x 16 chunks
-        auto v_row = [&](int s) { return s * 16 + sw * 4 + row2 + 2 * (lane >> 4); };    // 128 keys x 8 chunks
-        const int k_chunk = (lane & 3) | (lane >> 3 << 2), v_chunk = (lane & 3) | (lane >> 3 & 1) << 2;
-        auto load_k = [&](const Walk &x, int pg) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int key = 64 * rank + k_row(s), page = __shfl_sync(0xffffffffu, pg, key >> 4);
-                const size_t at = (size_t)page * a.page_stride +
-                                  (((size_t)x.h << sq.page_shift) + ((x.key0() + key) & (ps - 1))) * kHeadDim + 16 * k_chunk;
-                ck[s] = page < sq.num_pages ? __ldcg(reinterpret_cast<const uint4 *>(a.k_codes + at)) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        auto load_v = [&](const Walk &x, int pg) {   // rows of positions that no query row sees: zero
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int key = v_row(s), page = __shfl_sync(0xffffffffu, pg, key >> 4), p = x.key0() + key;
-                const size_t at = (size_t)page * a.page_stride +
-                                  (((size_t)x.h << sq.page_shift) + (p & (ps - 1))) * kHeadDim + 128 * rank + 16 * v_chunk;
-                cv[s] = page < sq.num_pages && p >= x.t.lo && p < x.t.hi
-                            ? __ldcg(reinterpret_cast<const uint4 *>(a.v_codes + at)) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
+    }
+    } else if (kFp8 && warp >= kStageWarp) {
+        // ---- E4M3 operands ----
+        if (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStageRegs));
+        // The codes of the next operand wait in registers, eight 16-byte chunks a thread.  A warp's lanes take two (K)
+        // or four (V) whole rows at a time, in an order that makes both the reads whole lines and the f16 stores free
+        // of bank conflicts: of eight lanes, four take neighbouring chunks of a row and four those of the row beside it.
+        const int sw = (warp - kStageWarp) & 3, row2 = (lane >> 2) & 1;
+        const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0);
+        uint4 codes[8];
         auto put = [&](uint8_t *slot, const uint4 &x, int row, int c, uint32_t col) {
             const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
             uint32_t f[8];
@@ -476,22 +486,36 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3)) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
             *reinterpret_cast<uint4 *>(dst + (((2 * (c & 3) + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
         };
-        int pg = 0;
-        if (kFp8) {
-            pg = pages_of(w);
-            load_k(w, pg);
-            load_v(w, pg);
-        }
-        for (long long i = 0; i <= N; ++i) {
-            const int pg_w = pg;   // pages of tile i
-            Walk nx = w;
-            if (i + 1 < N) nx.next(a);
-            if (i < N && w.fresh) {
-                wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
-                if (kFp8) {
+        RingPos<kSlots> pos;
+        auto wait_slot = [&]() {
+            if (!pos.first) wait_warp(&bar[BAR_EMPTY + pos.st], pos.ph ^ 1, dead, err);
+        };
+        auto hand_on = [&]() {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
+        };
+        if (warp < kStageWarp + 4) {
+            // K(k), of a segment's loads the first and then number 2 k - 1: this CTA's 64 keys x 16 chunks.
+            const uint32_t q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
+            const int chunk = (lane & 3) | (lane >> 3 << 2);
+            auto load = [&](int k) {
+                const int pg = pages_of(w, k), key0 = w.key0(k);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int key = 64 * rank + s * 8 + sw * 2 + row2, page = __shfl_sync(0xffffffffu, pg, key >> 4);
+                    const size_t at = (size_t)page * a.page_stride +
+                                      (((size_t)w.h << sq.page_shift) + ((key0 + key) & (ps - 1))) * kHeadDim + 16 * chunk;
+                    codes[s] = page < sq.num_pages ? load_codes(a.k_codes + at) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            if (more) load(0);
+            for (uint32_t seg = 0; more; ++seg) {
+                {
                     // A thread's row of q in f16, scaled by the power of two that brings its largest value below 2
                     // (and by the sign of the K scale); the softmax multiplies the scores back.
-                    const int row = st_tid;
+                    wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
+                    const int row = sw * 32 + lane;
                     uint8_t *qrow = smem + row * 128;
                     uint32_t top = 0;
 #pragma unroll 8
@@ -513,95 +537,122 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         *at = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
                     }
                     smem[kQexpOff + (seg & 3) * kCtaRows + row] = (uint8_t)ex;
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(q_ready);
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(q_ready);
-                ++seg;
+                const int L = w.L;
+                for (int k = 0; k < L; ++k) {
+                    wait_slot();
+                    uint8_t *slot = ring + pos.st * kSlotBytes;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) put(slot, codes[s], s * 8 + sw * 2 + row2, chunk, 8192);
+                    hand_on();
+                    pos.step(k + 1 < L ? (k ? 2 : 1) : (k ? 3 : 2));   // to the next K, over the last V's at the end
+                    if (k + 1 < L) load(k + 1);
+                }
+                more = w.next(a);
+                if (more) load(0);
             }
-            if (kFp8) wait_slots(i);
+        } else {
+            // V(k), of a segment's loads number 2 k + 2 and the last: 128 keys x 8 chunks of this CTA's dims.  Rows of
+            // positions that no query row sees are zero, whatever their slots hold.
+            const int chunk = (lane & 3) | (lane >> 3 & 1) << 2, row4 = row2 + 2 * (lane >> 4);
+            auto load = [&](int k) {
+                const int pg = pages_of(w, k), key0 = w.key0(k);
 #pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-                if (kind == 0 ? i >= N : i == 0) continue;
-                uint8_t *slot = ring + pos.st * kSlotBytes;
-                if (kFp8) {
-                    if (kind == 0) {
+                for (int s = 0; s < 8; ++s) {
+                    const int key = s * 16 + sw * 4 + row4, page = __shfl_sync(0xffffffffu, pg, key >> 4), p = key0 + key;
+                    const size_t at = (size_t)page * a.page_stride +
+                                      (((size_t)w.h << sq.page_shift) + (p & (ps - 1))) * kHeadDim + 128 * rank + 16 * chunk;
+                    codes[s] = page < sq.num_pages && p >= w.t.lo && p < w.t.hi ? load_codes(a.v_codes + at)
+                                                                               : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            if (more) load(0);
+            while (more) {
+                const int L = w.L;
+                pos.step(L > 1 ? 2 : 1);
+                for (int k = 0; k < L; ++k) {
+                    wait_slot();
+                    uint8_t *slot = ring + pos.st * kSlotBytes;
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) put(slot, ck[s], k_row(s), k_chunk, 8192);
-                        if (i + 1 < N) {
-                            pg = pages_of(nx);
-                            load_k(nx, pg);
-                        }
-                    } else {
+                    for (int s = 0; s < 8; ++s) put(slot, codes[s], s * 16 + sw * 4 + row4, chunk, 16384);
+                    hand_on();
+                    pos.step(k + 2 < L ? 2 : 1);
+                    if (k + 1 < L) load(k + 1);
+                }
+                more = w.next(a);
+                if (more) load(0);
+            }
+        }
+    } else if (!kFp8 && warp == kStageWarp) {
+        // ---- bf16 stages: hand what has landed on to the MMAs ----
+        const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
+        const int rv_shift = min(sq.page_shift, 7);
+        RingPos<kSlots> pos;
+        for (uint32_t seg = 0; more; ++seg) {
+            wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(q_ready);
+            for (int i = 0; i <= w.L; ++i) {
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) put(slot, cv[s], v_row(s), v_chunk, 16384);
-                        if (i < N) load_v(w, pg_w);
-                    }
-                } else {
+                for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
+                    if (kind == 0 ? i >= w.L : i == 0) continue;
+                    uint8_t *slot = ring + pos.st * kSlotBytes;
                     wait_warp(&bar[BAR_FULL + pos.st], pos.ph, dead, err);
-                    if (kind == 1 && (key_v < lo_v || key_v + kTileKeys > hi_v)) {
+                    const int key0 = w.key0(i - 1);
+                    if (kind == 1 && (key0 < w.t.lo || key0 + kTileKeys > w.t.hi)) {
                         // Rows of positions that no query row sees: zero, whatever their slots hold.
                         for (int r = 0; r < kTileKeys; ++r) {
-                            if (key_v + r >= lo_v && key_v + r < hi_v) continue;
+                            if (key0 + r >= w.t.lo && key0 + r < w.t.hi) continue;
                             const uint32_t at = (uint32_t)(r >> rv_shift << rv_shift) * 256 +
                                                 (uint32_t)(r & ((1 << rv_shift) - 1)) * 128 +
                                                 (lane >> 3 & 1) * (128u << rv_shift) + (lane & 7) * 16;
                             if (lane < 16) *reinterpret_cast<uint4 *>(slot + at) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
+                    pos.step();
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
-                pos.step();
             }
-            key_v = w.key0();
-            lo_v = w.t.lo;
-            hi_v = w.t.hi;
-            w = nx;
+            more = w.next(a);
         }
-    } else {
+    } else if (warp < kSoftWarps) {
         // ---- softmax: thread (row, half of the tile's keys) ----
+        if (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // lane 32 (warp % 4) in the upper half-word
         const uint32_t p_bar = dsmem_addr(&bar[BAR_P], 0), o_free = dsmem_addr(&bar[BAR_O_FREE], 0);
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
         auto soft_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         const float lift = kFp8 ? 7.f : 0.f;
+        int blocks = 0, tiles = 0;   // before this segment
+        for (uint32_t seg = 0; more; ++seg) {
         float m = -INFINITY, l = 0.f, scale = kQScale;
-        int hi_pos = 0, lo_pos = 0, all_hi = 0, all_lo = 0, rows_here = 0;
-        long long item0 = x0 - w.u;   // first tile of the current item in the call's order
-        int seg_u0 = 0;
-        uint32_t seg = 0;
-        for (long long g = 0; g < N; ++g) {
-            if (w.fresh) {
-                m = -INFINITY;
-                l = 0.f;
-                const int r = rank * kCtaRows + row;
-                hi_pos = w.q.ctx + w.t.t0 + (r >> a.group_shift);
-                lo_pos = a.window ? hi_pos - a.window + 1 : 0;
-                all_hi = w.q.ctx + w.t.t0;
-                all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;
-                rows_here = w.t.nt * a.group - rank * kCtaRows;   // valid rows of this CTA
-                item0 = x0 + g - w.u;
-                seg_u0 = w.u;
-            }
-            const bool idle = (warp & 3) * 32 >= rows_here;   // none of this warp's rows exists
+        const int r = rank * kCtaRows + row;
+        const int hi_pos = w.q.ctx + w.t.t0 + (r >> a.group_shift), lo_pos = a.window ? hi_pos - a.window + 1 : 0;
+        const int all_hi = w.q.ctx + w.t.t0;                                            // every row sees up to here ..
+        const int all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;        // .. from here
+        const int rows_here = (w.t.nt << a.group_shift) - rank * kCtaRows;              // valid rows of this CTA
+        const bool idle = (warp & 3) * 32 >= rows_here;                                  // none of this warp's rows exists
+        for (int k = 0; k < w.L; ++k) {
+            const int g = tiles + k;
             const uint32_t buf = lanes + (uint32_t)(g & 1) * 128;
-            wait_block(g);
-            if (w.fresh) {
-                if (kFp8) {
-                    const uint32_t ex = smem[kQexpOff + (seg & 3) * kCtaRows + row];
-                    scale = fmaxf(__uint_as_float(ex << 23) * fabsf(a.k_scale[w.h] * kQScale), 1e-37f);
-                }
-                ++seg;
+            wait_block(blocks + k);
+            if (kFp8 && k == 0) {
+                const uint32_t ex = smem[kQexpOff + (seg & 3) * kCtaRows + row];
+                scale = fmaxf(__uint_as_float(ex << 23) * fabsf(a.k_scale[w.h] * kQScale), 1e-37f);
             }
             if (!idle) {
                 tc_fence_after();
                 float s[64];
                 tmem_ld32(buf + half * 64, *reinterpret_cast<float(*)[32]>(s));
                 tmem_ld32(buf + half * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
-                const int key0 = w.key0() + half * 64;
+                const int key0 = w.key0(k) + half * 64;
                 if (key0 < all_lo || key0 + 63 > all_hi) {
                     const int from = lo_pos - key0, to = hi_pos - key0;
 #pragma unroll
@@ -622,8 +673,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     m = top;
                     l *= alpha;
                 }
-                if (w.u != seg_u0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    wait_block(g + 1);
+                if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    wait_block(blocks + k + 1);   // O holds tile k - 1
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
@@ -653,26 +704,23 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(p_bar + 8 * (uint32_t)(g & 1));
 
-            if (w.last()) {
-                // ---- the segment's output ----
-                float *x = xm + ((g + 1) & 1) * 2 * kCtaRows;
+        }
+            // ---- the segment's output ----
+            {
+                float *x = xm + ((tiles + w.L) & 1) * 2 * kCtaRows;
                 if (!idle) {
                     x[half * kCtaRows + row] = l;
                     pair_sync();
                     l += x[(half ^ 1) * kCtaRows + row];
                     pair_sync();
                 }
-                wait_block(g + 2);
-                tc_fence_after();
-                const bool whole = seg_u0 == 0 && w.seg_end == w.t.units;
-                const bool live = row < rows_here;
-                const int r = rank * kCtaRows + row;
+                const bool whole = w.L == w.t.units, live = row < rows_here;
                 const float ml_m = m - lift;
-                const int slot = seg_u0 == 0 ? 2 * pair + 1 : 2 * pair;
+                const int slot = w.u == 0 ? 2 * pair + 1 : 2 * pair;
                 const size_t prow = (size_t)slot * kTileRows + r;
                 const float vscale = kFp8 ? a.v_scale[w.h] : 1.f;
-                const int head = w.h * a.group + r % a.group;
-                const size_t orow = (size_t)(w.q.row0 + w.t.t0 + r / a.group) * a.num_q_heads + head;
+                const int head = (w.h << a.group_shift) + (r & (a.group - 1));
+                const size_t orow = (size_t)(w.q.row0 + w.t.t0 + (r >> a.group_shift)) * a.num_q_heads + head;
                 float f = 1.f;
                 if (live) {
                     if (whole) {
@@ -683,23 +731,25 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         a.part_ml[prow] = make_float2(ml_m, l);
                     }
                 }
+                wait_warp(&bar[BAR_O_FULL], seg & 1, dead, err);
+                tc_fence_after();
                 if (!idle) {
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
                         float o[32];
                         tmem_ld32(lanes + kOutCol + half * 128 + c, o);
-                        if (!live) continue;
-                        if (whole) {
+                        if (live && whole) {
                             uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + half * 128 + c);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 dst[i] = make_uint4(pack_bf16(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16(o[8 * i + 2] * f, o[8 * i + 3] * f),
                                                     pack_bf16(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16(o[8 * i + 6] * f, o[8 * i + 7] * f));
-                        } else {
+                        } else if (live) {
                             float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * kHeadDim + half * 128 + c);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
+                        __syncwarp();
                     }
                 }
                 tc_fence_before();
@@ -707,13 +757,16 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 if (lane == 0) mbar_arrive_remote(o_free);
                 if (!whole) {
                     // The last of the item's pieces to arrive (for this CTA's rows) merges them.
-                    const int i0 = cta_of_unit(item0, T, n), nseg = cta_of_unit(item0 + w.t.units - 1, T, n) - i0 + 1;
-                    __threadfence();
+                    const long long all = call[0], from = call[1] + w.done - w.off + kItemCost;   // the item's first tile
+                    const int i0 = cta_of_unit(from, all, misc[5]), nseg = cta_of_unit(from + w.t.units - 1, all, misc[5]) - i0 + 1;
                     soft_sync();
-                    if (tid == 0) misc[4] = atomicAdd(&a.tickets[2 * i0 + rank], 1) == nseg - 1;
+                    if (tid == 0) {
+                        __threadfence();   // the block's stores (ordered by the barrier) before the ticket
+                        misc[4] = atomicAdd(&a.tickets[2 * i0 + rank], 1) == nseg - 1;
+                        __threadfence();   // the ticket before the other pieces' loads
+                    }
                     soft_sync();
                     if (misc[4]) {
-                        __threadfence();
                         for (int rr = warp; rr < min(rows_here, kCtaRows); rr += kSoftWarps) {
                             auto piece = [&](int j) {
                                 return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kTileRows + rank * kCtaRows + rr;
@@ -746,8 +799,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                                 v1.x = fmaf(wt, p1.x, v1.x); v1.y = fmaf(wt, p1.y, v1.y);
                                 v1.z = fmaf(wt, p1.z, v1.z); v1.w = fmaf(wt, p1.w, v1.w);
                             }
-                            const int rt = rank * kCtaRows + rr, hd_ = w.h * a.group + rt % a.group;
-                            const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + rt / a.group) * a.num_q_heads + hd_;
+                            const int rt = rank * kCtaRows + rr, hd_ = (w.h << a.group_shift) + (rt & (a.group - 1));
+                            const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + (rt >> a.group_shift)) * a.num_q_heads + hd_;
                             float lse;
                             const float ff = row_factor(a, out_row, hd_, top, sum, vscale, &lse);
                             if (lane == 0) a.lse[out_row] = lse;
@@ -760,7 +813,9 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     soft_sync();
                 }
             }
-            if (g + 1 < N) w.next(a);
+            blocks += w.L + 2;
+            tiles += w.L;
+            more = w.next(a);
         }
     }
     __syncwarp();
