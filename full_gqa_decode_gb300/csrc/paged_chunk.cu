@@ -59,7 +59,7 @@ constexpr int kChunkBarOff = kQexpOff + 4 * kCtaRows;
 constexpr int kChunkBars = 32;
 constexpr int kChunkMiscOff = kChunkBarOff + kChunkBars * 8;
 constexpr int kChunkSmem = kChunkMiscOff + 64;
-constexpr int kMaxPairs = 96;                         // pieces of an item a warp can weigh in registers
+constexpr int kMaxPairs = 96;
 // What an item costs besides its key tiles, in tiles: its query rows and the drain of its output (about 3 us to a
 // tile's 1.7).  Shares are cut by tiles plus this; short items (the first rows of a causal prompt) would otherwise
 // pile up in a few shares.
@@ -80,13 +80,13 @@ enum : int {
     BAR_FULL = 0,      // [5] a slot's copies have landed in this CTA (bf16 pages)
     BAR_READY = 5,     // [5] first CTA: both CTAs' halves of a slot are ready for the MMAs
     BAR_EMPTY = 10,    // [5] the MMAs that read a slot are complete (E4M3 pages)
-    BAR_BLOCK = 15,    // [2] a block of products is complete, by its parity
-    BAR_Q_FULL = 17,   // the query rows have landed in this CTA
-    BAR_Q_READY = 18,  // first CTA: both CTAs' query rows are ready
-    BAR_Q_EMPTY = 19,  // the MMAs that read the query rows are complete
-    BAR_P = 20,        // [2] first CTA: the weights of both CTAs are written, by the tile's parity
-    BAR_O_FULL = 22,   // a segment's output is complete
-    BAR_O_FREE = 23,   // first CTA: both CTAs have read it
+    BAR_BLOCK = 15,    // [4] a block of products is complete, by its number modulo 4
+    BAR_Q_FULL = 19,   // the query rows have landed in this CTA
+    BAR_Q_READY = 20,  // first CTA: both CTAs' query rows are ready
+    BAR_Q_EMPTY = 21,  // the MMAs that read the query rows are complete
+    BAR_P = 22,        // [2] first CTA: the weights of both CTAs are written, by the tile's parity
+    BAR_O_FULL = 24,   // a segment's output is complete
+    BAR_O_FREE = 25,   // first CTA: both CTAs have read it
 };
 
 struct ChunkTile {
@@ -274,6 +274,22 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
     return v;
 }
 
+// Four 16-byte pieces of each of four neighbouring lanes, transposed: lane q of four gets piece q of all four lanes.
+__device__ __forceinline__ void transpose4(uint4 (&e)[4], int lane) {
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & b) continue;
+            const bool up = lane & b;
+            const uint4 send = up ? e[j] : e[j | b];
+            const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, send.x, b), __shfl_xor_sync(0xffffffffu, send.y, b),
+                                         __shfl_xor_sync(0xffffffffu, send.z, b), __shfl_xor_sync(0xffffffffu, send.w, b));
+            if (up) e[j] = got;
+            else e[j | b] = got;
+        }
+}
+
 template <int KV>
 __global__ void __launch_bounds__(chunk_threads(KV), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
@@ -299,10 +315,8 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         mbar_init(&bar[BAR_Q_FULL], 1);
         mbar_init(&bar[BAR_Q_READY], 2 * kStage);
         mbar_init(&bar[BAR_Q_EMPTY], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[BAR_BLOCK + i], 1);
-            mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
-        }
+        for (int i = 0; i < 4; ++i) mbar_init(&bar[BAR_BLOCK + i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
         mbar_init(&bar[BAR_O_FULL], 1);
         mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
         fence_mbar_init();
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     bool dead = false;
     const int ps = 1 << sq.page_shift;
     // Whole-warp wait for the end of block i.
-    auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 1)], (uint32_t)(i >> 1) & 1, dead, err); };
+    auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 3)], (uint32_t)(i >> 2) & 1, dead, err); };
     // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
     auto pages_of = [&](const Segment &x, int k) {
         const int pos = x.key0(k) + 16 * (lane & 7), first = pos & ~(ps - 1);
@@ -366,6 +380,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         const int tok = kCtaRows >> a.group_shift;
         RingPos<kSlots> pos;
         int issued = 0, blocks = 0;   // blocks: before this segment
+        int last_read = -1;
         for (uint32_t seg = 0; more; ++seg) {
             int pg = kFp8 ? 0 : pages_of(w, 0), pg_v = 0;
             if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
@@ -378,10 +393,13 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
 #pragma unroll
                 for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
                     if (kind == 0 ? i >= w.L : i == 0) continue;
-                    // The operand is read by block r, the slot's last one by block r - 2 or before; block r - 2 is also
-                    // the last whose end a parity can tell, as block r does not end without this copy.
+                    // The operand is read by block r, the slot's last one by the block in lane `slot` of last_read.  A
+                    // barrier of four phases tells the end of block r - 4 or later, as block r does not end without
+                    // this copy.
                     const int r = blocks + (kind == 0 ? i : i + 1);
-                    if (r >= 3) wait_block(r - 2);
+                    const int before = max(__shfl_sync(0xffffffffu, last_read, pos.st), r - 4);
+                    if (before >= 0) wait_block(before);
+                    if (lane == pos.st) last_read = r;
                     uint8_t *dst = ring + pos.st * kSlotBytes;
                     uint64_t *full = &bar[BAR_FULL + pos.st];
                     const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
@@ -455,7 +473,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
                     }
-                    pair_commit(&bar[BAR_BLOCK + ((blocks + i) & 1)]);
+                    pair_commit(&bar[BAR_BLOCK + ((blocks + i) & 3)]);
                     if (i == w.L - 1) pair_commit(&bar[BAR_Q_EMPTY]);
                     if (i == w.L + 1) pair_commit(&bar[BAR_O_FULL]);
                 }
@@ -734,22 +752,47 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 wait_warp(&bar[BAR_O_FULL], seg & 1, dead, err);
                 tc_fence_after();
                 if (!idle) {
+                    // A lane holds a row; four lanes trade pieces so that each store writes 64 bytes of a row together
+                    // (a row a lane, 16 bytes at a time, took 4 us an item).
+                    const int r4 = row & ~3, piece = lane & 3;
+                    size_t row4[4];
+                    bool live4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        live4[j] = r4 + j < rows_here;
+                        const int rr = rank * kCtaRows + r4 + j;
+                        row4[j] = whole ? (size_t)(w.q.row0 + w.t.t0 + (rr >> a.group_shift)) * a.num_q_heads +
+                                              (w.h << a.group_shift) + (rr & (a.group - 1))
+                                        : (size_t)slot * kTileRows + rr;
+                    }
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
+                    for (int c = half * 128; c < half * 128 + 128; c += 32) {
                         float o[32];
-                        tmem_ld32(lanes + kOutCol + half * 128 + c, o);
-                        if (live && whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + half * 128 + c);
+                        tmem_ld32(lanes + kOutCol + c, o);
+                        uint4 e[4];
+                        if (whole) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                dst[i] = make_uint4(pack_bf16(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                                                    pack_bf16(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16(o[8 * i + 6] * f, o[8 * i + 7] * f));
-                        } else if (live) {
-                            float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * kHeadDim + half * 128 + c);
+                                e[i] = make_uint4(pack_bf16(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                                                  pack_bf16(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16(o[8 * i + 6] * f, o[8 * i + 7] * f));
+                            transpose4(e, lane);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                if (live4[j]) *reinterpret_cast<uint4 *>(a.out + row4[j] * kHeadDim + c + 8 * piece) = e[j];
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    e[i] = make_uint4(__float_as_uint(o[16 * p + 4 * i]), __float_as_uint(o[16 * p + 4 * i + 1]),
+                                                      __float_as_uint(o[16 * p + 4 * i + 2]), __float_as_uint(o[16 * p + 4 * i + 3]));
+                                transpose4(e, lane);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    if (live4[j])
+                                        *reinterpret_cast<uint4 *>(a.part_o + row4[j] * kHeadDim + c + 16 * p + 4 * piece) = e[j];
+                            }
                         }
-                        __syncwarp();
                     }
                 }
                 tc_fence_before();
@@ -767,46 +810,56 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     }
                     soft_sync();
                     if (misc[4]) {
-                        for (int rr = warp; rr < min(rows_here, kCtaRows); rr += kSoftWarps) {
-                            auto piece = [&](int j) {
-                                return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kTileRows + rank * kCtaRows + rr;
-                            };
-                            float2 ml[3];
-                            float top = -INFINITY;
+                        // A thread's four dims of a row, four rows at a time, two pieces' values and (max, sum) of each
+                        // in flight; rescaled as the maximum moves.
+                        const int d = (tid & 63) * 4, rows = min(rows_here, kCtaRows);
+                        auto piece = [&](int j) { return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kTileRows + rank * kCtaRows; };
+#pragma unroll 1
+                        for (int r0 = tid >> 6; r0 < rows; r0 += 16) {
+                            float4 v[4];
+                            float mm[4], ll[4];
 #pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                const int j = lane + 32 * k;
-                                ml[k] = j < nseg ? __ldcg(&a.part_ml[piece(j)]) : make_float2(-INFINITY, 0.f);
-                                top = fmaxf(top, ml[k].x);
+                            for (int i = 0; i < 4; ++i) {
+                                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                mm[i] = -INFINITY;
+                                ll[i] = 0.f;
+                            }
+#pragma unroll 1
+                            for (int j0 = 0; j0 < nseg; j0 += 2) {
+                                float4 p[4][2];
+                                float2 ml[4][2];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        const size_t at = piece(min(j0 + k, nseg - 1)) + min(r0 + 4 * i, rows - 1);
+                                        ml[i][k] = __ldcg(&a.part_ml[at]);
+                                        p[i][k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kHeadDim + d));
+                                    }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float top = fmaxf(mm[i], fmaxf(ml[i][0].x, ml[i][1].x));
+                                    const float w0 = part_weight(mm[i], top), wa = part_weight(ml[i][0].x, top);
+                                    const float wb = j0 + 1 < nseg ? part_weight(ml[i][1].x, top) : 0.f;
+                                    mm[i] = top;
+                                    ll[i] = ll[i] * w0 + wa * ml[i][0].y + wb * ml[i][1].y;
+                                    v[i].x = v[i].x * w0 + wa * p[i][0].x + wb * p[i][1].x;
+                                    v[i].y = v[i].y * w0 + wa * p[i][0].y + wb * p[i][1].y;
+                                    v[i].z = v[i].z * w0 + wa * p[i][0].z + wb * p[i][1].z;
+                                    v[i].w = v[i].w * w0 + wa * p[i][0].w + wb * p[i][1].w;
+                                }
                             }
 #pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            float sum = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                ml[k].x = part_weight(ml[k].x, top);
-                                sum += ml[k].x * ml[k].y;
+                            for (int i = 0; i < 4; ++i) {
+                                if (r0 + 4 * i >= rows) break;
+                                const int rt = rank * kCtaRows + r0 + 4 * i, hd_ = (w.h << a.group_shift) + (rt & (a.group - 1));
+                                const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + (rt >> a.group_shift)) * a.num_q_heads + hd_;
+                                float lse;
+                                const float ff = row_factor(a, out_row, hd_, mm[i], ll[i], vscale, &lse);
+                                if (d == 0) a.lse[out_row] = lse;
+                                *reinterpret_cast<uint2 *>(a.out + out_row * kHeadDim + d) =
+                                    make_uint2(pack_bf16(v[i].x * ff, v[i].y * ff), pack_bf16(v[i].z * ff, v[i].w * ff));
                             }
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                            float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-                            for (int j = 0; j < nseg; ++j) {
-                                const float wt = __shfl_sync(0xffffffffu, j < 32 ? ml[0].x : j < 64 ? ml[1].x : ml[2].x, j & 31);
-                                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + piece(j) * kHeadDim) + 2 * lane;
-                                const float4 p0 = __ldcg(src), p1 = __ldcg(src + 1);
-                                v0.x = fmaf(wt, p0.x, v0.x); v0.y = fmaf(wt, p0.y, v0.y);
-                                v0.z = fmaf(wt, p0.z, v0.z); v0.w = fmaf(wt, p0.w, v0.w);
-                                v1.x = fmaf(wt, p1.x, v1.x); v1.y = fmaf(wt, p1.y, v1.y);
-                                v1.z = fmaf(wt, p1.z, v1.z); v1.w = fmaf(wt, p1.w, v1.w);
-                            }
-                            const int rt = rank * kCtaRows + rr, hd_ = (w.h << a.group_shift) + (rt & (a.group - 1));
-                            const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + (rt >> a.group_shift)) * a.num_q_heads + hd_;
-                            float lse;
-                            const float ff = row_factor(a, out_row, hd_, top, sum, vscale, &lse);
-                            if (lane == 0) a.lse[out_row] = lse;
-                            reinterpret_cast<uint4 *>(a.out + out_row * kHeadDim)[lane] =
-                                make_uint4(pack_bf16(v0.x * ff, v0.y * ff), pack_bf16(v0.z * ff, v0.w * ff),
-                                           pack_bf16(v1.x * ff, v1.y * ff), pack_bf16(v1.z * ff, v1.w * ff));
                         }
                         if (tid == 0) a.tickets[2 * i0 + rank] = 0;
                     }

@@ -122,6 +122,8 @@ struct Start {
     int b, tile, h, off;
 };
 
+constexpr int kFewTiles = 4;   // of a sequence, that one lane counts
+
 // Share `who` of at most `workers` over all units of the call, each at least
 // `least` units: its first unit x0, its end x1 (x0 >= x1: none), the number of
 // shares n and the total T.  All threads of the block call it; `tmp`: 33 64-bit
@@ -139,15 +141,31 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
     const int per = (s.batch + of - 1) / of;
     const int b_lo = min(who_am * per, s.batch), b_hi = min(b_lo + per, s.batch);
     long long mine = 0, before;
-    int flags = 0;
+    int flags = 0, long_one = 0;
+    SeqSpan span{0, 0, 0};   // by_warp: this lane's sequence
     for (int b = b_lo; b < b_hi; ++b) {
         int bit;
-        const SeqSpan q = seq_span(s, b, &bit);
+        span = seq_span(s, b, &bit);
         flags |= bit;
-        const int nt = tiles(q.n);
-        for (int i = 0; i < nt; ++i) mine += (long long)units(q, i) * num_kv_heads;
+        const int nt = tiles(span.n);
+        if (by_warp && nt > kFewTiles) {
+            long_one = nt;
+            continue;
+        }
+        for (int i = 0; i < nt; ++i) mine += (long long)units(span, i) * num_kv_heads;
     }
     if (by_warp) {
+        // A sequence of many tiles is summed by all lanes.
+        for (unsigned todo = __ballot_sync(0xffffffffu, long_one); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1, nt = __shfl_sync(0xffffffffu, long_one, src);
+            const SeqSpan q{__shfl_sync(0xffffffffu, span.row0, src), __shfl_sync(0xffffffffu, span.n, src),
+                            __shfl_sync(0xffffffffu, span.ctx, src)};
+            long long sum = 0;
+            for (int i = lane; i < nt; i += 32) sum += units(q, i);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == src) mine = sum * num_kv_heads;
+        }
         long long v = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -170,12 +188,12 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
     *x1 = who < k ? (who + 1) * each + (who + 1) * rest / k : 0;
     Start c{0, 0, 0, 0};
     const bool here = before <= *x0 && *x0 < before + mine && *x0 < *x1;
-    if (here) {
+    if (here && !long_one) {
         long long rem = *x0 - before;
         bool found = false;
         for (int b = b_lo; b < b_hi && !found; ++b) {
             int bit;
-            const SeqSpan q = seq_span(s, b, &bit);
+            const SeqSpan q = by_warp ? span : seq_span(s, b, &bit);
             const int nt = tiles(q.n);
             for (int i = 0; i < nt && !found; ++i) {
                 const int u = units(q, i);
@@ -186,6 +204,31 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
                 }
                 rem -= (long long)u * num_kv_heads;
             }
+        }
+    }
+    const unsigned in_long = by_warp ? __ballot_sync(0xffffffffu, here && long_one) : 0u;
+    if (in_long) {   // 32 tiles at a time
+        const int src = __ffs(in_long) - 1, nt = __shfl_sync(0xffffffffu, long_one, src);
+        const SeqSpan q{__shfl_sync(0xffffffffu, span.row0, src), __shfl_sync(0xffffffffu, span.n, src),
+                        __shfl_sync(0xffffffffu, span.ctx, src)};
+        long long rem = __shfl_sync(0xffffffffu, *x0 - before, src);
+        for (int i0 = 0; i0 < nt; i0 += 32) {
+            const int u = i0 + lane < nt ? units(q, i0 + lane) : 0;
+            long long upto = (long long)u * num_kv_heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += t;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, rem < upto);
+            if (past) {
+                const int at_lane = __ffs(past) - 1;
+                const long long start = __shfl_sync(0xffffffffu, upto - (long long)u * num_kv_heads, at_lane);
+                const unsigned left = (unsigned)(rem - start), ut = (unsigned)__shfl_sync(0xffffffffu, u, at_lane);
+                if (lane == src) c = {src, i0 + at_lane, (int)(left / ut), (int)(left % ut)};
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, upto, 31);
         }
     }
     if (by_warp) {
