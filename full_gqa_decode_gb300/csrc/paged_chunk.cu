@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     long long x0, x1, T;
     int n, bad;
     const Start c0 = find_share(
-        sq, a.num_kv_heads, pair, pairs, kMinTiles, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
+        sq, a.num_kv_heads, pair, pairs, kMinTiles, 0, 0, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_chunk_tiles(a, tokens); },
         [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units + kItemCost; });
     if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);

@@ -124,15 +124,20 @@ struct Start {
 
 constexpr int kFewTiles = 4;   // of a sequence, that one lane counts
 
-// Share `who` of at most `workers` over all units of the call, each at least
-// `least` units: its first unit x0, its end x1 (x0 >= x1: none), the number of
-// shares n and the total T.  All threads of the block call it; `tmp`: 33 64-bit
-// words, `at`: 4 words of shared memory.  *bad: some sequence cannot be served.
+// Share `who` of at most `workers` over all units of the call: its first unit
+// x0, its end x1 (x0 >= x1: none), the number of shares n and the total T.
+// Shares have at least `least` units, unless `items` (about as many as there
+// are) asks for more shares.  With `snap`, in a call of at most `snap` units a
+// share on average, a border inside an item of at most `snap` units moves to the
+// nearer end of the item: merging a cut item costs more than the imbalance.  The
+// start may then lie at its item's end (off = its units).  All threads of the
+// block call it; `tmp`: 33 64-bit words, `at`: 5 words of shared memory.
+// *bad: some sequence cannot be served.
 //   tiles(n)      tiles of n new tokens
 //   units(q, i)   units of one kv head of tile i of span q
 template <class Tiles, class Units>
 __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads, int who, int workers, int least,
-                                            long long *tmp, int *at, long long *x0, long long *x1, long long *T, int *n,
+                                            int items, int snap, long long *tmp, int *at, long long *x0, long long *x1, long long *T, int *n,
                                             int *bad, Tiles tiles, Units units) {
     const int lane = threadIdx.x & 31;
     // Up to 32 sequences every warp works it out by itself; above, the block together.
@@ -179,72 +184,100 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
         *bad = __syncthreads_or(flags);
         before = block_prefix(mine, tmp, T);
     }
-    *n = *T >= (long long)workers * least ? workers : max((int)*T / least, 1);
+    *n = *T >= (long long)workers * least ? workers : max(max((int)*T / least, min(min(items, workers), (int)*T)), 1);
     // T who / n from one division (of 32 bits where T allows): n^2 is small.
     const int k = *n;
     const long long each = *T < 0x80000000LL ? (int)*T / k : *T / k;
     const int rest = (int)(*T - each * k);
     *x0 = who < k ? who * each + who * rest / k : 0;
     *x1 = who < k ? (who + 1) * each + (who + 1) * rest / k : 0;
-    Start c{0, 0, 0, 0};
-    const bool here = before <= *x0 && *x0 < before + mine && *x0 < *x1;
-    if (here && !long_one) {
-        long long rem = *x0 - before;
-        bool found = false;
-        for (int b = b_lo; b < b_hi && !found; ++b) {
-            int bit;
-            const SeqSpan q = by_warp ? span : seq_span(s, b, &bit);
-            const int nt = tiles(q.n);
-            for (int i = 0; i < nt && !found; ++i) {
-                const int u = units(q, i);
-                if (rem < (long long)u * num_kv_heads) {
-                    // rem < units of one tile x kv heads: fewer than 2^32 for any pool that fits in memory
-                    c = {b, i, (int)((unsigned)rem / (unsigned)u), (int)((unsigned)rem % (unsigned)u)};
-                    found = true;
+    const bool any = *x0 < *x1, snaps = snap > 0 && *T <= (long long)k * snap;
+
+    // The item that holds unit x < T, and its units in *item.
+    auto locate = [&](long long x, int *item) {
+        Start c{0, 0, 0, 0};
+        int cu = 1;
+        const bool here = before <= x && x < before + mine;
+        if (here && !long_one) {
+            long long rem = x - before;
+            bool found = false;
+            for (int b = b_lo; b < b_hi && !found; ++b) {
+                int bit;
+                const SeqSpan q = by_warp ? span : seq_span(s, b, &bit);
+                const int nt = tiles(q.n);
+                for (int i = 0; i < nt && !found; ++i) {
+                    const int u = units(q, i);
+                    if (rem < (long long)u * num_kv_heads) {
+                        // rem < units of one tile x kv heads: fewer than 2^32 for any pool that fits in memory
+                        c = {b, i, (int)((unsigned)rem / (unsigned)u), (int)((unsigned)rem % (unsigned)u)};
+                        cu = u;
+                        found = true;
+                    }
+                    rem -= (long long)u * num_kv_heads;
                 }
-                rem -= (long long)u * num_kv_heads;
             }
         }
-    }
-    const unsigned in_long = by_warp ? __ballot_sync(0xffffffffu, here && long_one) : 0u;
-    if (in_long) {   // 32 tiles at a time
-        const int src = __ffs(in_long) - 1, nt = __shfl_sync(0xffffffffu, long_one, src);
-        const SeqSpan q{__shfl_sync(0xffffffffu, span.row0, src), __shfl_sync(0xffffffffu, span.n, src),
-                        __shfl_sync(0xffffffffu, span.ctx, src)};
-        long long rem = __shfl_sync(0xffffffffu, *x0 - before, src);
-        for (int i0 = 0; i0 < nt; i0 += 32) {
-            const int u = i0 + lane < nt ? units(q, i0 + lane) : 0;
-            long long upto = (long long)u * num_kv_heads;
+        const unsigned in_long = by_warp ? __ballot_sync(0xffffffffu, here && long_one) : 0u;
+        if (in_long) {   // 32 tiles at a time
+            const int src = __ffs(in_long) - 1, nt = __shfl_sync(0xffffffffu, long_one, src);
+            const SeqSpan q{__shfl_sync(0xffffffffu, span.row0, src), __shfl_sync(0xffffffffu, span.n, src),
+                            __shfl_sync(0xffffffffu, span.ctx, src)};
+            long long rem = __shfl_sync(0xffffffffu, x - before, src);
+            for (int i0 = 0; i0 < nt; i0 += 32) {
+                const int u = i0 + lane < nt ? units(q, i0 + lane) : 0;
+                long long upto = (long long)u * num_kv_heads;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += t;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += t;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, rem < upto);
+                if (past) {
+                    const int at_lane = __ffs(past) - 1;
+                    const long long start = __shfl_sync(0xffffffffu, upto - (long long)u * num_kv_heads, at_lane);
+                    const unsigned left = (unsigned)(rem - start), ut = (unsigned)__shfl_sync(0xffffffffu, u, at_lane);
+                    if (lane == src) {
+                        c = {src, i0 + at_lane, (int)(left / ut), (int)(left % ut)};
+                        cu = (int)ut;
+                    }
+                    break;
+                }
+                rem -= __shfl_sync(0xffffffffu, upto, 31);
             }
-            const unsigned past = __ballot_sync(0xffffffffu, rem < upto);
-            if (past) {
-                const int at_lane = __ffs(past) - 1;
-                const long long start = __shfl_sync(0xffffffffu, upto - (long long)u * num_kv_heads, at_lane);
-                const unsigned left = (unsigned)(rem - start), ut = (unsigned)__shfl_sync(0xffffffffu, u, at_lane);
-                if (lane == src) c = {src, i0 + at_lane, (int)(left / ut), (int)(left % ut)};
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, upto, 31);
         }
-    }
-    if (by_warp) {
-        const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-        if (src >= 0)
+        if (by_warp) {
+            const int src = max(__ffs(__ballot_sync(0xffffffffu, here)) - 1, 0);
             c = {__shfl_sync(0xffffffffu, c.b, src), __shfl_sync(0xffffffffu, c.tile, src),
                  __shfl_sync(0xffffffffu, c.h, src), __shfl_sync(0xffffffffu, c.off, src)};
-    } else {
-        if (here) {
-            at[0] = c.b;
-            at[1] = c.tile;
-            at[2] = c.h;
-            at[3] = c.off;
+            cu = __shfl_sync(0xffffffffu, cu, src);
+        } else {
+            __syncthreads();
+            if (here) {
+                at[0] = c.b;
+                at[1] = c.tile;
+                at[2] = c.h;
+                at[3] = c.off;
+                at[4] = cu;
+            }
+            __syncthreads();
+            c = {at[0], at[1], at[2], at[3]};
+            cu = at[4];
         }
-        __syncthreads();
-        if (*x0 < *x1) c = {at[0], at[1], at[2], at[3]};
+        *item = cu;
+        return c;
+    };
+    Start c{0, 0, 0, 0};
+    int item;
+    if (!any) return c;
+    if (snaps && *x1 < *T) {
+        c = locate(*x1, &item);
+        if (item <= snap) *x1 += 2 * c.off < item ? -c.off : item - c.off;
+    }
+    c = locate(*x0, &item);
+    if (snaps && item <= snap) {
+        const int to = 2 * c.off < item ? 0 : item;
+        *x0 += to - c.off;
+        c.off = to;
     }
     return c;
 }
