@@ -119,6 +119,6 @@ cudaError_t launch_paged_decode(const CUtensorMap *kmap, const CUtensorMap *vmap
 // boxes of chunk_k_rows / chunk_v_rows slots (paged_api.cpp).
 cudaError_t launch_paged_chunk(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
                                const PagedAttnArgs &a, cudaStream_t s);
-cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, cudaStream_t s);
+cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, int num_sms, cudaStream_t s);
 
 }  // namespace hd

@@ -237,7 +237,7 @@ hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, 
     a.keep_first = keep_first;
     a.keep_last = keep_last;
     a.selected = selected;
-    st = cuda_status(launch_paged_select(a, (int)blocks, static_cast<cudaStream_t>(stream)));
+    st = cuda_status(launch_paged_select(a, (int)blocks, ctx->num_sms, static_cast<cudaStream_t>(stream)));
     if (st == HD_OK) ctx->launches += 2;
     return st;
 }

@@ -18,6 +18,8 @@
 // none more than are wanted -- are scored again with twice the digits:
 // products split exactly by an fma, sums by the error-free addition of Knuth
 // (The Art of Computer Programming, vol. 2, 4.2.2).  Ties go to the lower block.
+#include <algorithm>
+
 #include "paged_sched.cuh"
 
 namespace hd {
@@ -25,8 +27,7 @@ namespace {
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kBlocksPerWarp = 16;                                   // of one score CTA
-constexpr int kBlocksPerCta = kScoreWarps * kBlocksPerWarp;
+constexpr int kMaxBlocksPerWarp = 32;                                // of one score CTA; a multiple of kInFlight
 constexpr int kInFlight = 4;                                         // blocks whose bounds a warp loads at once
 constexpr int kPickThreads = 512;
 constexpr float kErrUnits = 32.f * 5.9604645e-8f;
@@ -114,8 +115,9 @@ __device__ __forceinline__ bool kept(const PagedSelectArgs &a, int i, int last) 
     return i < a.keep_first || i > last - a.keep_last;
 }
 
-// Grid: (row, kv head, chunk of kBlocksPerCta blocks), the chunk fastest.  Scores go out as (score, A).
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ PagedSelectArgs a, int chunks) {
+// Grid: (row, kv head, chunk of 8 x per_warp blocks), the chunk fastest.  Scores go out as (score, A).
+__global__ void __launch_bounds__(kScoreThreads, 4) page_score_kernel(const __grid_constant__ PagedSelectArgs a, int chunks,
+                                                                     int per_warp) {
     wait_for_previous_kernel();
     let_next_kernel_start();
     const PagedSeqs &sq = a.seqs;
@@ -126,59 +128,72 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
     const SeqSpan q = span_of_row(sq, r, &bit, &b);
     if (q.n == 0) return;
     const int last = (q.ctx + r - q.row0) >> sq.page_shift;
-    const int blk0 = chunk * kBlocksPerCta + warp * kBlocksPerWarp;
+    const int blk0 = (chunk * kScoreWarps + warp) * per_warp;
     if (blk0 > last) return;
-    const int mine = blk0 + (lane & (kBlocksPerWarp - 1));
-    int page = mine <= last ? sq.table[(size_t)b * sq.table_stride + mine] : 0;
+    const int mine = blk0 + lane;
+    int page = lane < per_warp && mine <= last ? sq.table[(size_t)b * sq.table_stride + mine] : 0;
     const bool valid = page >= 0 && page < sq.num_pages;
     if (!valid) {
         atomicOr(sq.err, HD_DEVERR_PAGE);
         page = 0;
     }
-    QuerySums s;
-    sum_queries(a, r, h, lane, s);
-    float2 out = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int i0 = 0; i0 < kBlocksPerWarp; i0 += kInFlight) {
-        if (blk0 + i0 > last) break;
-        uint4 lo[kInFlight], hi[kInFlight];
+    const uint4 *lo_hi = bounds_of(a, 0, h, lane);
+    const size_t per_page = (size_t)a.num_kv_heads * (2 * kHeadDim / 8);   // 16-byte words
+    uint4 lo[kInFlight], hi[kInFlight];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            const uint4 *p = bounds_of(a, __shfl_sync(0xffffffffu, page, i0 + i), h, lane);
+            const uint4 *p = lo_hi + __shfl_sync(0xffffffffu, page, i0 + i) * per_page;
             const bool need = blk0 + i0 + i <= last;
             lo[i] = need ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
             hi[i] = need ? __ldg(p + 32) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float v[kInFlight], m[kInFlight];
+    };
+    load(0);   // under way while the queries are summed
+    QuerySums s;
+    sum_queries(a, r, h, lane, s);
+    const unsigned good = __ballot_sync(0xffffffffu, valid);
+    float *scores = reinterpret_cast<float *>(a.scores + (size_t)rh * a.score_stride);
+#pragma unroll 1
+    for (int i0 = 0; i0 < per_warp; i0 += kInFlight) {
+        if (blk0 + i0 > last) break;
+        if (i0) load(i0);
+        float x[2 * kInFlight];   // score and A of each block
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            float l8[8], h8[8];
+            float l8[8], h8[8], v = 0.f, m = 0.f;
             unpack_bf16x8(lo[i], l8);
             unpack_bf16x8(hi[i], h8);
-            v[i] = m[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i] = fmaf(s.ph[j], h8[j], v[i]);
-                m[i] = fmaf(s.ph[j], fabsf(h8[j]), m[i]);
-                v[i] = fmaf(s.nh[j], l8[j], v[i]);
-                m[i] = fmaf(-s.nh[j], fabsf(l8[j]), m[i]);
+                v = fmaf(s.ph[j], h8[j], v);
+                m = fmaf(s.ph[j], fabsf(h8[j]), m);
+                v = fmaf(s.nh[j], l8[j], v);
+                m = fmaf(-s.nh[j], fabsf(l8[j]), m);
+            }
+            x[2 * i] = v;
+            x[2 * i + 1] = m;
+        }
+        // Sum the eight values over the lanes, halving the values a lane is left with at each of the first three steps.
+        static_assert(kInFlight == 4, "three halvings leave one value");
+#pragma unroll
+        for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+                x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < kInFlight; ++i) {
-                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-                m[i] += __shfl_xor_sync(0xffffffffu, m[i], o);
-            }
-#pragma unroll
-        for (int i = 0; i < kInFlight; ++i)
-            if (lane == i0 + i) out = make_float2(v[i], m[i]);
-    }
-    if (lane < kBlocksPerWarp && mine <= last) {
-        if (!valid) out = make_float2(-INFINITY, 0.f);
-        if (kept(a, mine, last)) out = make_float2(INFINITY, 0.f);
-        a.scores[(size_t)rh * a.score_stride + mine] = out;
+        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+        const int at = i0 + (lane >> 3), blk = blk0 + at, second = lane >> 2 & 1;   // lane's block, score or A
+        if ((lane & 3) == 0 && at < per_warp && blk <= last) {
+            float y = x[0];
+            if (!(good >> at & 1)) y = second ? 0.f : -INFINITY;
+            if (kept(a, blk, last)) y = second ? 0.f : INFINITY;
+            scores[2 * blk + second] = y;
+        }
     }
 }
 
@@ -361,7 +376,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_co
 
 }  // namespace
 
-cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, cudaStream_t s) {
+cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, int num_sms, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (!done_on_device(done, &dev)) {
@@ -370,10 +385,15 @@ cudaError_t launch_paged_select(const PagedSelectArgs &a, int max_blocks, cudaSt
         if (e != cudaSuccess) return e;
         mark_done_on_device(done, dev);
     }
-    const int chunks = (max_blocks + kBlocksPerCta - 1) / kBlocksPerCta;
+    // A warp's blocks: enough warps to fill the SMs one and a half times over (32 each), then longer runs, which share
+    // a look-up of the position and the sums of the queries (4 rows of 2049 blocks at 2 kv heads: 4 blocks 8.9 us,
+    // 16 blocks 10.9 us; 64 rows of up to 1025: 20 blocks).
     const long long rh = (long long)a.seqs.num_tokens * a.num_kv_heads;
+    const long long even = (rh * max_blocks + 48LL * num_sms - 1) / (48LL * num_sms);
+    const int per_warp = (int)std::min<long long>(kMaxBlocksPerWarp, (even + kInFlight - 1) / kInFlight * kInFlight);
+    const int chunks = (max_blocks + kScoreWarps * per_warp - 1) / (kScoreWarps * per_warp);
     if (rh * chunks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_overlapping(page_score_kernel, dim3((unsigned)(rh * chunks)), kScoreThreads, 0, 1, s, a, chunks);
+    const cudaError_t e = launch_overlapping(page_score_kernel, dim3((unsigned)(rh * chunks)), kScoreThreads, 0, 1, s, a, chunks, per_warp);
     if (e != cudaSuccess) return e;
     return launch_overlapping(page_pick_kernel, dim3((unsigned)rh), kPickThreads, (size_t)max_blocks * 12, 1, s, a, max_blocks);
 }
