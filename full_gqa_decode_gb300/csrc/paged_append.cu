@@ -11,10 +11,16 @@
 // in shared memory, and meet the bounds that the page had (a run that starts
 // at slot 0 starts them anew).  No atomics, so results never depend on order.
 //
-// The written key is the exact rotation rounded once (rope_round.cuh for
-// bf16).  An E4M3 entry is e4m3(y / scale): binary32 with an error bound,
-// binary64 next to a rounding border -- GB300 runs binary64 at a sixtieth of
-// the binary32 rate, and evaluating every key there would bound the call.
+// The written key is the exact rotation, rounded to binary64 and then to the
+// entry's type.  GB300 runs binary64 at a sixtieth of the binary32 rate, so
+// every value is first enclosed in binary32: an interval that holds the exact
+// value, from the error bounds of its two or three operations.  Rounding is
+// monotone, so when both ends round to the same entry that is the entry; only
+// the others are evaluated in binary64 (about one bf16 value in four thousand,
+// one E4M3 value in a hundred thousand).  The call is bound by the instructions
+// of this, not by its bytes: testing each value's distance from the rounding's
+// midpoint instead took twice as many (9026 tokens at 16 heads, E4M3: 71 us,
+// so 37 us).
 #include <cuda_fp8.h>
 
 #include "e4m3.cuh"
@@ -26,36 +32,107 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kQueryHeads = 4;   // heads of a row that one warp rotates
+constexpr int kQueryHeads = 4;   // heads of a row that one warp rotates (9026 tokens at 16 heads: 2 44 us, 4 37 us)
 
-// The binary64 paths are calls: inlined at every use they make the kernel wait for its instructions (append of 9026
-// tokens at 16 heads: 94 us inlined, 87 us so).
-__device__ __noinline__ uint8_t e4m3_rotated_f64(float a, float c, float b, float sn, float s) {
+// The binary64 paths are calls: inlined at every use they make the kernel wait for its instructions.
+__device__ __noinline__ uint32_t e4m3_rotated_f64(float a, float c, float b, float sn, float s) {
     const double y = __dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)sn));
     return e4m3_from_f64(__ddiv_rn(y, (double)s));
 }
-__device__ __noinline__ float rotated_f64(float a, float c, float b, float s) {
-    return f64_to_bf16_value(__dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)s)));
+__device__ __noinline__ uint32_t rotated_f64(float a, float c, float b, float s) {
+    return __float_as_uint(f64_to_bf16_value(__dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)s)))) >> 16;
 }
 
-// e4m3(fl64(y / s)) for y = a c - b sn (the exact rotation, rounded once to
-// binary64), bit for bit.  In binary32: q = RN(b sn), y32 = fma(a, c, -q) with
-// |y32 - y| <= 2^-24 (|y32| + |q|), and t = RN(y32 / s) adds 2^-24 |t|.  In
-// units of t's E4M3 quantum that sum is at most `err` (1% over it for the
-// second-order terms).  The code is that of t unless t lies within err of a
-// midpoint, its sign is in doubt, or it is no ordinary number -- then binary64
-// decides.  inv = |1 / s|.  (c, sn) = (1, 0): the value a itself.
-__device__ __forceinline__ uint8_t e4m3_rotated(float a, float c, float b, float sn, float s, float inv) {
-    const float q = b * sn, y = fmaf(a, c, -q);
-    const float t = __fdiv_rn(y, s), mag = fabsf(t);
-    if (mag < 1e30f && mag > 1e-30f && fabsf(y) > 1e-30f) {
-        const int e = max((int)(__float_as_uint(mag) >> 23) - 127, -6);
-        const float per = __uint_as_float((uint32_t)(127 + 3 - e) << 23);   // 1 / quantum
-        const float u = mag * per;                                           // exact
-        const float err = 6.02e-8f * (mag + (fabsf(y) + fabsf(q)) * inv) * per;
-        if (fabsf(u - truncf(u) - 0.5f) > err && u > err) return __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+// bf16 of a c - b s, rounded once, for two pairs (a, b).  q = RN(b s) and y = fma(a, c, -q) are off by 2^-24 (|y| + |q|)
+// and, where they are subnormal, 2^-149; the interval's own ends are rounded by 2^-24 |y|.  e covers all of it.
+__device__ __forceinline__ uint32_t rotated_bf16x2(float a0, float b0, float a1, float b1, float c0, float s0, float c1, float s1) {
+    constexpr float kRel = 1.2e-7f;   // over 2^-23
+    constexpr float kAbs = 5.6e-45f;  // 2^-147
+    const float q0 = b0 * s0, q1 = b1 * s1, y0 = fmaf(a0, c0, -q0), y1 = fmaf(a1, c1, -q1);
+    const float e0 = fmaf(fabsf(y0) + fabsf(q0), kRel, kAbs), e1 = fmaf(fabsf(y1) + fabsf(q1), kRel, kAbs);
+    uint32_t lo = pack_bf16(y0 - e0, y1 - e1);
+    const uint32_t differ = lo ^ pack_bf16(y0 + e0, y1 + e1);
+    if (differ & 0xFFFFu) lo = (lo & 0xFFFF0000u) | rotated_f64(a0, c0, b0, s0);
+    if (differ >> 16) lo = (lo & 0xFFFFu) | rotated_f64(a1, c1, b1, s1) << 16;
+    return lo;
+}
+
+// A scale's reciprocal, and the bounds that go with it.
+struct Recip {
+    float s, inv;   // inv = RN(1 / s)
+    float rel, abs;
+    uint32_t odd;   // all ones: the reciprocal is no normal number
+};
+__device__ __forceinline__ Recip recip_of(float s) {
+    Recip r;
+    r.s = s;
+    r.inv = 1.f / s;
+    const float m = fabsf(r.inv);
+    r.odd = m > 1.2e-38f && m < 3e38f ? 0u : 0xFFFFFFFFu;
+    r.rel = 2.4e-7f * m;   // over 2^-22 |1 / s|
+    r.abs = fmaf(m, 7.2e-43f, 7.2e-43f);
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, __NV_E4M3);
+    return l | h << 16;
+}
+
+// Four codes e4m3(fl64(y / s)) for y = a c - b sn rounded to binary64.  With y and q as above, y inv is off by
+// 2^-24 |inv| (2 |y| + |q|), an interval's end rounded by 2^-24 |y inv|: within rel (|y| + |q|).  abs keeps values whose
+// sign a subnormal y may have lost on both sides of zero.
+__device__ __forceinline__ uint32_t e4m3_rotated(const float (&a)[4], const float (&b)[4], const float (&c)[4],
+                                                 const float (&sn)[4], float sign, const Recip &r) {
+    float lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float q = sign * b[j] * sn[j], y = fmaf(a[j], c[j], -q);
+        const float e = fmaf(fabsf(y) + fabsf(q), r.rel, r.abs);
+        lo[j] = fmaf(y, r.inv, -e);
+        hi[j] = fmaf(y, r.inv, e);
     }
-    return e4m3_rotated_f64(a, c, b, sn, s);
+    uint32_t code = e4m3x4(lo[0], lo[1], lo[2], lo[3]);
+    if ((code ^ e4m3x4(hi[0], hi[1], hi[2], hi[3])) | r.odd) {
+        code = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code |= e4m3_rotated_f64(a[j], c[j], sign * b[j], sn[j], r.s) << (8 * j);
+    }
+    return code;
+}
+// Four codes e4m3(fl64(a / s)).  a inv carries a's sign to the last.
+__device__ __forceinline__ uint32_t e4m3_plain(const float (&a)[4], const Recip &r) {
+    float lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float e = fabsf(a[j]) * r.rel;
+        lo[j] = fmaf(a[j], r.inv, -e);
+        hi[j] = fmaf(a[j], r.inv, e);
+    }
+    uint32_t code = e4m3x4(lo[0], lo[1], lo[2], lo[3]);
+    if ((code ^ e4m3x4(hi[0], hi[1], hi[2], hi[3])) | r.odd) {
+        code = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code |= e4m3_rotated_f64(a[j], 1.f, 0.f, 0.f, r.s) << (8 * j);
+    }
+    return code;
+}
+
+// Elementwise minimum and maximum of two bf16 or two f16, numbers before NaN.
+template <bool BF16>
+__device__ __forceinline__ void widen2(uint32_t &lo, uint32_t &hi, uint32_t x) {
+    if (BF16) {
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(x));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(x));
+    } else {
+        asm("min.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(x));
+        asm("max.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(x));
+    }
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t x;
+    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(x) : "r"(codes));
+    return x;
 }
 
 // A lane's eight dims of a row: two runs of four, at d0 and d1.
@@ -74,10 +151,6 @@ __device__ __forceinline__ void unpack4(uint2 w, float (&x)[4]) {
     x[2] = __uint_as_float(w.y << 16);
     x[3] = __uint_as_float(w.y & 0xFFFF0000u);
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) { unpack4(*reinterpret_cast<const uint2 *>(p), x); }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4]) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-}
 __device__ __forceinline__ void load_angles(const float2 *cs, int i, float (&c)[4], float (&s)[4]) {
     const float4 u = __ldg(reinterpret_cast<const float4 *>(cs + i)), v = __ldg(reinterpret_cast<const float4 *>(cs + i + 2));
     c[0] = u.x; s[0] = u.y; c[1] = u.z; s[1] = u.w;
@@ -85,24 +158,19 @@ __device__ __forceinline__ void load_angles(const float2 *cs, int i, float (&c)[
 }
 
 // Rotates a lane's dims in place, each value rounded once to bf16.
-__device__ __forceinline__ void rotate_bf16(float (&x)[4], float (&y)[4], const float (&c)[4], const float (&s)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float a = x[j], b = y[j];
-        float u, v;
-        const bool sure = rotated_bf16_sure(a, c[j], b, s[j], &u) & rotated_bf16_sure(b, c[j], -a, s[j], &v);
-        if (!sure) {
-            u = rotated_f64(a, c[j], b, s[j]);
-            v = rotated_f64(b, c[j], -a, s[j]);
-        }
-        x[j] = u;
-        y[j] = v;
-    }
+__device__ __forceinline__ void rotate_bf16(uint2 &x, uint2 &y, const float (&c)[4], const float (&s)[4]) {
+    float a[4], b[4];
+    unpack4(x, a);
+    unpack4(y, b);
+    x.x = rotated_bf16x2(a[0], b[0], a[1], b[1], c[0], s[0], c[1], s[1]);
+    x.y = rotated_bf16x2(a[2], b[2], a[3], b[3], c[2], s[2], c[3], s[3]);
+    y.x = rotated_bf16x2(b[0], -a[0], b[1], -a[1], c[0], s[0], c[1], s[1]);
+    y.y = rotated_bf16x2(b[2], -a[2], b[3], -a[3], c[2], s[2], c[3], s[3]);
 }
 
 // Grid: [0, runs) x kv heads: runs of keys and values; the CTAs behind them:
 // query rows, a warp each.
-__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int runs) {
+__global__ void __launch_bounds__(kThreads, 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int runs) {
     const PagedSeqs &sq = a.seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rot = a.rotary_dim, half = rot >> 1, ps = 1 << sq.page_shift;
@@ -137,14 +205,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < kQueryHeads; ++i) {
             if (i >= heads) break;
-            if (ld.i >= 0) {
-                float u[4], v[4];
-                unpack4(x[i], u);
-                unpack4(y[i], v);
-                rotate_bf16(u, v, c, s);
-                x[i] = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
-                y[i] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            }
+            if (ld.i >= 0) rotate_bf16(x[i], y[i], c, s);
             *reinterpret_cast<uint2 *>(dst + i * kHeadDim + ld.d0) = x[i];
             *reinterpret_cast<uint2 *>(dst + i * kHeadDim + ld.d1) = y[i];
         }
@@ -199,76 +260,68 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_
     }
     const int p0 = max(q.ctx, block << sq.page_shift), p1 = min(q.ctx + q.n, (block + 1) << sq.page_shift);
     const bool fp8 = a.kv_type == KV_FP8;
-    const float ks = fp8 ? a.k_scale[h] : 1.f, vs = fp8 ? a.v_scale[h] : 1.f;
-    const float kinv = fp8 ? fabsf(1.f / ks) : 1.f, vinv = fp8 ? fabsf(1.f / vs) : 1.f;
-    float lo[8], hi[8];
+    const Recip kr = recip_of(fp8 ? a.k_scale[h] : 1.f), vr = recip_of(fp8 ? a.v_scale[h] : 1.f);
+    uint32_t lo[4], hi[4];   // of the keys' dims: bf16 pairs, or f16 pairs, which hold every E4M3 value
+    const uint32_t inf = fp8 ? 0x7C007C00u : 0x7F807F80u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        lo[j] = INFINITY;
-        hi[j] = -INFINITY;
+    for (int j = 0; j < 4; ++j) {
+        lo[j] = inf;
+        hi[j] = inf | 0x80008000u;
     }
     for (int p = p0 + warp; p < p1; p += kWarps) {
         const int r = q.row0 + p - q.ctx;
         const __nv_bfloat16 *ksrc = a.k + (size_t)r * a.k_stride + h * kHeadDim;
         const __nv_bfloat16 *vsrc = a.v + (size_t)r * a.v_stride + h * kHeadDim;
         const size_t o = (size_t)page * a.page_stride + ((size_t)h * ps + (p & (ps - 1))) * kHeadDim;
-        float x[4], y[4], c[4], s[4];
-        load4(ksrc + ld.d0, x);
-        load4(ksrc + ld.d1, y);
+        uint2 x = *reinterpret_cast<const uint2 *>(ksrc + ld.d0), y = *reinterpret_cast<const uint2 *>(ksrc + ld.d1);
         const uint4 v = *reinterpret_cast<const uint4 *>(vsrc + 8 * lane);
+        float c[4], s[4];
         if (ld.i >= 0) load_angles(a.rope + (size_t)p * half, ld.i, c, s);
         if (fp8) {
-            uint32_t cx = 0, cy = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u = x[j], w = y[j];
-                uint8_t kx, ky;
-                if (ld.i >= 0) {
-                    kx = e4m3_rotated(u, c[j], w, s[j], ks, kinv);
-                    ky = e4m3_rotated(w, c[j], -u, s[j], ks, kinv);
-                } else {
-                    kx = e4m3_rotated(u, 1.f, 0.f, 0.f, ks, kinv);
-                    ky = e4m3_rotated(w, 1.f, 0.f, 0.f, ks, kinv);
-                }
-                cx |= (uint32_t)kx << (8 * j);
-                cy |= (uint32_t)ky << (8 * j);
-                x[j] = e4m3_to_f32(kx);
-                y[j] = e4m3_to_f32(ky);
+            float u[4], w[4], f[8];
+            unpack4(x, u);
+            unpack4(y, w);
+            uint32_t cx, cy;
+            if (ld.i >= 0) {
+                cx = e4m3_rotated(u, w, c, s, 1.f, kr);
+                cy = e4m3_rotated(w, u, c, s, -1.f, kr);
+            } else {
+                cx = e4m3_plain(u, kr);
+                cy = e4m3_plain(w, kr);
             }
             uint8_t *kd = static_cast<uint8_t *>(a.cache_k) + o;
             *reinterpret_cast<uint32_t *>(kd + ld.d0) = cx;
             *reinterpret_cast<uint32_t *>(kd + ld.d1) = cy;
-            float f[8];
             unpack_bf16x8(v, f);
-            uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w0 |= (uint32_t)e4m3_rotated(f[j], 1.f, 0.f, 0.f, vs, vinv) << (8 * j);
-                w1 |= (uint32_t)e4m3_rotated(f[4 + j], 1.f, 0.f, 0.f, vs, vinv) << (8 * j);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache_v) + o + 8 * lane) = make_uint2(w0, w1);
+            const float v0[4] = {f[0], f[1], f[2], f[3]}, v1[4] = {f[4], f[5], f[6], f[7]};
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.cache_v) + o + 8 * lane) =
+                make_uint2(e4m3_plain(v0, vr), e4m3_plain(v1, vr));
+            widen2<false>(lo[0], hi[0], e4m3x2_to_f16x2(cx & 0xFFFFu));
+            widen2<false>(lo[1], hi[1], e4m3x2_to_f16x2(cx >> 16));
+            widen2<false>(lo[2], hi[2], e4m3x2_to_f16x2(cy & 0xFFFFu));
+            widen2<false>(lo[3], hi[3], e4m3x2_to_f16x2(cy >> 16));
         } else {
             if (ld.i >= 0) rotate_bf16(x, y, c, s);
             __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(a.cache_k) + o;
-            store4(kd + ld.d0, x);
-            store4(kd + ld.d1, y);
+            *reinterpret_cast<uint2 *>(kd + ld.d0) = x;
+            *reinterpret_cast<uint2 *>(kd + ld.d1) = y;
             *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache_v) + o + 8 * lane) = v;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            lo[j] = fminf(lo[j], x[j]);
-            hi[j] = fmaxf(hi[j], x[j]);
-            lo[4 + j] = fminf(lo[4 + j], y[j]);
-            hi[4 + j] = fmaxf(hi[4 + j], y[j]);
+            widen2<true>(lo[0], hi[0], x.x);
+            widen2<true>(lo[1], hi[1], x.y);
+            widen2<true>(lo[2], hi[2], y.x);
+            widen2<true>(lo[3], hi[3], y.y);
         }
     }
     if (!a.bounds) return;
+    auto pair = [&](uint32_t w) {
+        return fp8 ? __half22float2(*reinterpret_cast<const __half2 *>(&w))
+                   : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    };
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        edge[0][warp][ld.d0 + j] = lo[j];
-        edge[0][warp][ld.d1 + j] = lo[4 + j];
-        edge[1][warp][ld.d0 + j] = hi[j];
-        edge[1][warp][ld.d1 + j] = hi[4 + j];
+        const int d = (j < 2 ? ld.d0 : ld.d1) + 2 * (j & 1);
+        *reinterpret_cast<float2 *>(&edge[0][warp][d]) = pair(lo[j]);
+        *reinterpret_cast<float2 *>(&edge[1][warp][d]) = pair(hi[j]);
     }
     __syncthreads();
     __nv_bfloat16 *bd = a.bounds + ((size_t)page * a.num_kv_heads + h) * 2 * kHeadDim;

@@ -31,23 +31,17 @@ __device__ __forceinline__ float f64_to_bf16_value(double x) {
 // exact value round to the same bf16.  Values near the midpoint (ties among
 // them), zero, subnormal, infinite or NaN results, and heavy cancellation (the
 // bound over 2^13 units) take the binary64 path.
-//
-// The binary32 evaluation: y, and whether its bf16 rounding is that of the exact value.
-__device__ __forceinline__ bool rotated_bf16_sure(float a, float c, float b, float s, float *y_out) {
+__device__ __forceinline__ float rotated_bf16(float a, float c, float b, float s) {
     const float q = b * s;
     const float y = fmaf(a, c, -q);
     const uint32_t yb = __float_as_uint(y), qb = __float_as_uint(q);
     const int ey = (int)((yb >> 23) & 0xFFu);
     const int eq = max((int)((qb >> 23) & 0xFFu), 1);   // subnormal q: the smallest binade's spacing
     const int d = eq - ey;
-    *y_out = y;
-    if (ey == 0 || ey == 255 || d > 13) return false;
-    const int bound = 2 + (d > 0 ? (1 << d) : 1);     // > ulp(y)/2 + ulp(q)/2 in units of ulp(y)
-    return abs((int)(yb & 0xFFFFu) - 0x8000) > bound;
-}
-__device__ __forceinline__ float rotated_bf16(float a, float c, float b, float s) {
-    float y;
-    if (rotated_bf16_sure(a, c, b, s, &y)) return __bfloat162float(__float2bfloat16_rn(y));
+    if (ey != 0 && ey != 255 && d <= 13) {
+        const int bound = 2 + (d > 0 ? (1 << d) : 1);     // > ulp(y)/2 + ulp(q)/2 in units of ulp(y)
+        if (abs((int)(yb & 0xFFFFu) - 0x8000) > bound) return __bfloat162float(__float2bfloat16_rn(y));
+    }
     return f64_to_bf16_value(__dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)s)));
 }
 
