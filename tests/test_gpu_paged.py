@@ -109,6 +109,48 @@ def test_append_is_bit_exact(hd, orc, spans, layer_type, kv, page):
     assert np.array_equal(synth.bits(bounds)[~touched], synth.bits(held)[~touched]), "bounds of the other pages"
 
 
+@pytest.mark.parametrize("scales", [(0.37, 1.0), (2.0 ** -130, -0.5), (3e38, 2.0 ** -126)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_append_of_hard_values_is_bit_exact(hd, orc, kv, scales):
+    """Entries of every binade from subnormals to the largest, pairs whose rotation cancels, infinities, zeros of
+    either sign; scales whose reciprocal is no normal binary32 number."""
+    case = PagedCase(14, [(5, 40), (1, 3), (900, 5)], page=16, kv=kv, appended=False)
+    rng = case.rng
+
+    def values(heads):
+        bits = rng.integers(0, 0x7F80, (case.rows, heads, D)) | rng.integers(0, 2, (case.rows, heads, D)) << 15
+        x = torch.from_numpy(bits.astype(np.uint16).view(np.int16)).view(torch.bfloat16)
+        half = synth.ROPE[FULL][0] // 2
+        for r in range(0, case.rows, 2):   # x1 c - x2 s near zero, at ordinary magnitudes
+            cs, sn = orc.rope_angles(case.token(r)[1], 2 * half, synth.ROPE[FULL][1])
+            x2 = rng.standard_normal((heads, half)).astype(np.float32)
+            x[r, :, half : 2 * half] = torch.from_numpy(x2).bfloat16()
+            ratio = (sn / np.where(cs == 0, 1, cs)).astype(np.float64)
+            x[r, :, :half] = (x[r, :, half : 2 * half].double() * torch.from_numpy(ratio)).bfloat16()
+        x[1, :, :6] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), 0.0, -0.0], dtype=torch.bfloat16)
+        x[3, :, half : half + 2] = 0.0
+        x[3, :, :2] = -0.0
+        return x
+
+    q, k, v = values(case.q_heads), values(case.kv_heads), values(case.kv_heads)
+    if kv == "e4m3":
+        case.k_scale = torch.tensor(scales, dtype=torch.float32)
+        case.v_scale = torch.tensor(scales[::-1], dtype=torch.float32)
+    bounds = torch.zeros(case.pool, case.kv_heads, 2, D, dtype=torch.bfloat16)
+    kp, vp, bd, qr = reference_append(orc, case, FULL, q, k, v, bounds)
+    d = case.device()
+    bounds = bounds.cuda()
+    ctx = context(hd, kv=kv)
+    q_rot = torch.zeros(case.rows, case.q_heads, D, dtype=torch.bfloat16, device="cuda")
+    hd.rope_append_paged(ctx, 1, case.batch_of(hd, d), q.cuda(), k.cuda(), v.cuda(), q_rot, cache_of(hd, d, bounds))
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    assert_bits_equal(d["k"], kp, "K pages")
+    assert_bits_equal(d["v"], vp, "V pages")
+    assert_bits_equal(q_rot, qr, "rotated queries")
+    assert np.array_equal(bounds.float().cpu().numpy(), bd), "bounds"
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_append_of_parts_of_wider_rows_and_in_place(hd, orc, kv):
     case = PagedCase(12, [(3, 20), (100, 1), (64, 64)], kv=kv, appended=False)
