@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     int n, bad;
     const Start c0 = find_share(
         sq, a.num_kv_heads, cta, gridDim.x, min_units(KV),
-        (SPARSE ? sq.num_tokens : sq.batch) * a.num_kv_heads, kSnap, reinterpret_cast<long long *>(buf), misc, &x0, &x1, &T, &n, &bad,
+        (SPARSE ? sq.num_tokens : sq.batch) * a.num_kv_heads, kSnap, kSnap, reinterpret_cast<long long *>(buf), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_tiles<KV, SPARSE>(a, tokens); },
         [&](const SeqSpan &q, int i) { return make_tile<KV, SPARSE>(a, q, i).units; });
     if (bad) fill_bad_rows(a, cta, gridDim.x);

@@ -127,7 +127,7 @@ constexpr int kFewTiles = 4;   // of a sequence, that one lane counts
 // Share `who` of at most `workers` over all units of the call: its first unit
 // x0, its end x1 (x0 >= x1: none), the number of shares n and the total T.
 // Shares have at least `least` units, unless `items` (about as many as there
-// are) asks for more shares.  With `snap`, in a call of at most `snap` units a
+// are) asks for more shares.  With `snap`, in a call of at most `mean` units a
 // share on average, a border inside an item of at most `snap` units moves to the
 // nearer end of the item: merging a cut item costs more than the imbalance.  The
 // start may then lie at its item's end (off = its units).  All threads of the
@@ -137,7 +137,7 @@ constexpr int kFewTiles = 4;   // of a sequence, that one lane counts
 //   units(q, i)   units of one kv head of tile i of span q
 template <class Tiles, class Units>
 __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads, int who, int workers, int least,
-                                            int items, int snap, long long *tmp, int *at, long long *x0, long long *x1, long long *T, int *n,
+                                            int items, int snap, int mean, long long *tmp, int *at, long long *x0, long long *x1, long long *T, int *n,
                                             int *bad, Tiles tiles, Units units) {
     const int lane = threadIdx.x & 31;
     // Up to 32 sequences every warp works it out by itself; above, the block together.
@@ -191,7 +191,7 @@ __device__ __forceinline__ Start find_share(const PagedSeqs &s, int num_kv_heads
     const int rest = (int)(*T - each * k);
     *x0 = who < k ? who * each + who * rest / k : 0;
     *x1 = who < k ? (who + 1) * each + (who + 1) * rest / k : 0;
-    const bool any = *x0 < *x1, snaps = snap > 0 && *T <= (long long)k * snap;
+    const bool any = *x0 < *x1, snaps = *T <= (long long)k * mean;
 
     // The item that holds unit x < T, and its units in *item.
     auto locate = [&](long long x, int *item) {
