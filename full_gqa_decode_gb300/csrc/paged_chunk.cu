@@ -66,7 +66,7 @@ constexpr int kMaxPairs = 96;
 // tile's 1.7).  Shares are cut by tiles plus this; short items (the first rows of a causal prompt) would otherwise
 // pile up in a few shares.
 constexpr int kItemCost = 2;
-// Items of up to this many units are not cut: the merge of an item takes the time of ten tiles (5 prompts of up to 4099
+// Items of up to this many units are not cut: the merge of an item takes the time of seven tiles (5 prompts of up to 4099
 // tokens in 512-key windows: 119 us cut evenly, 104 us whole).
 constexpr int kSnap = 16;
 constexpr int kMinTiles = 2 + kItemCost;              // shortest share of a pair
@@ -815,54 +815,65 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     }
                     soft_sync();
                     if (misc[4]) {
-                        // A thread's four dims of a row, four rows at a time, two pieces' values and (max, sum) of each
-                        // in flight; rescaled as the maximum moves.
+                        // First each row's maximum and factor, by a thread a row; then the outputs, a thread's four dims of
+                        // kMergeRows rows and two pieces at a time in flight.
                         const int d = (tid & 63) * 4, rows = min(rows_here, kCtaRows);
                         auto piece = [&](int j) { return (size_t)(j ? 2 * (i0 + j) : 2 * i0 + 1) * kTileRows + rank * kCtaRows; };
-#pragma unroll 1
-                        for (int r0 = tid >> 6; r0 < rows; r0 += 16) {
-                            float4 v[4];
-                            float mm[4], ll[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                mm[i] = -INFINITY;
-                                ll[i] = 0.f;
+                        auto out_row = [&](int rr) {
+                            const int rt = rank * kCtaRows + rr;
+                            return (size_t)(w.q.row0 + w.t.t0 + (rt >> a.group_shift)) * a.num_q_heads +
+                                   (w.h << a.group_shift) + (rt & (a.group - 1));
+                        };
+                        if (half == 0 && live) {
+                            float mm = -INFINITY, ll = 0.f;
+#pragma unroll 2
+                            for (int j = 0; j < nseg; ++j) {
+                                const float2 ml = __ldcg(&a.part_ml[piece(j) + row]);
+                                const float top = fmaxf(mm, ml.x);
+                                ll = ll * part_weight(mm, top) + ml.y * part_weight(ml.x, top);
+                                mm = top;
                             }
+                            float lse;
+                            xm[kCtaRows + row] = row_factor(a, orow, head, mm, ll, vscale, &lse);
+                            xm[row] = mm;
+                            a.lse[orow] = lse;
+                        }
+                        soft_sync();
+                        constexpr int kMergeRows = kFp8 ? 4 : 8;
+#pragma unroll 1
+                        for (int r0 = tid >> 6; r0 < rows; r0 += 4 * kMergeRows) {
+                            float4 v[kMergeRows];
+#pragma unroll
+                            for (int i = 0; i < kMergeRows; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
                             for (int j0 = 0; j0 < nseg; j0 += 2) {
-                                float4 p[4][2];
-                                float2 ml[4][2];
+                                float4 p[kMergeRows][2];
+                                float pm[kMergeRows][2];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
+                                for (int i = 0; i < kMergeRows; ++i)
 #pragma unroll
                                     for (int k = 0; k < 2; ++k) {
                                         const size_t at = piece(min(j0 + k, nseg - 1)) + min(r0 + 4 * i, rows - 1);
-                                        ml[i][k] = __ldcg(&a.part_ml[at]);
+                                        pm[i][k] = __ldcg(&a.part_ml[at].x);
                                         p[i][k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kHeadDim + d));
                                     }
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float top = fmaxf(mm[i], fmaxf(ml[i][0].x, ml[i][1].x));
-                                    const float w0 = part_weight(mm[i], top), wa = part_weight(ml[i][0].x, top);
-                                    const float wb = j0 + 1 < nseg ? part_weight(ml[i][1].x, top) : 0.f;
-                                    mm[i] = top;
-                                    ll[i] = ll[i] * w0 + wa * ml[i][0].y + wb * ml[i][1].y;
-                                    v[i].x = v[i].x * w0 + wa * p[i][0].x + wb * p[i][1].x;
-                                    v[i].y = v[i].y * w0 + wa * p[i][0].y + wb * p[i][1].y;
-                                    v[i].z = v[i].z * w0 + wa * p[i][0].z + wb * p[i][1].z;
-                                    v[i].w = v[i].w * w0 + wa * p[i][0].w + wb * p[i][1].w;
+                                for (int i = 0; i < kMergeRows; ++i) {
+                                    const float top = xm[min(r0 + 4 * i, rows - 1)];
+                                    const float wa = part_weight(pm[i][0], top);
+                                    const float wb = j0 + 1 < nseg ? part_weight(pm[i][1], top) : 0.f;
+                                    v[i].x += wa * p[i][0].x + wb * p[i][1].x;
+                                    v[i].y += wa * p[i][0].y + wb * p[i][1].y;
+                                    v[i].z += wa * p[i][0].z + wb * p[i][1].z;
+                                    v[i].w += wa * p[i][0].w + wb * p[i][1].w;
                                 }
                             }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (r0 + 4 * i >= rows) break;
-                                const int rt = rank * kCtaRows + r0 + 4 * i, hd_ = (w.h << a.group_shift) + (rt & (a.group - 1));
-                                const size_t out_row = (size_t)(w.q.row0 + w.t.t0 + (rt >> a.group_shift)) * a.num_q_heads + hd_;
-                                float lse;
-                                const float ff = row_factor(a, out_row, hd_, mm[i], ll[i], vscale, &lse);
-                                if (d == 0) a.lse[out_row] = lse;
-                                *reinterpret_cast<uint2 *>(a.out + out_row * kHeadDim + d) =
+                            for (int i = 0; i < kMergeRows; ++i) {
+                                const int rr = r0 + 4 * i;
+                                if (rr >= rows) break;
+                                const float ff = xm[kCtaRows + rr];
+                                *reinterpret_cast<uint2 *>(a.out + out_row(rr) * kHeadDim + d) =
                                     make_uint2(pack_bf16(v[i].x * ff, v[i].y * ff), pack_bf16(v[i].z * ff, v[i].w * ff));
                             }
                         }
