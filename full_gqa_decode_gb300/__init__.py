@@ -519,15 +519,15 @@ def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype, device, strided
     """A tensor of a paged call: its shape, type and device; contiguous, or (strided) contiguous rows."""
     if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not (t.is_contiguous() or (strided and t.stride(2) == 1 and t.stride(1) == shape[2])):
+    if not (t.is_contiguous() or (strided and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]))):
         raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
 
 
 def _check_paged(ctx: Context, batch: PagedBatch, cache: PagedCache) -> None:
     if cache.num_kv_heads != ctx.cfg.num_kv_heads or cache.fp8 != (ctx.cfg.kv_dtype == HD_KV_FP8_E4M3):
         raise ValueError("the pages' kv heads and element type must be the context's")
-    if batch.device != cache.device:
-        raise ValueError("the batch and the pages must be on one device")
+    if batch.device != cache.device or cache.device.index != torch.cuda.current_device():
+        raise ValueError("the batch and the pages must be on the current device")
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -545,6 +545,8 @@ def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_ro
     _check_rows("k", k, kv, torch.bfloat16, dev, True)
     _check_rows("v", v, kv, torch.bfloat16, dev, True)
     qs = 0
+    if (q is None) != (q_rot is None):
+        raise ValueError("q and q_rot go together")
     if q is not None:
         _check_rows("q", q, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev, True)
         _check_rows("q_rot", q_rot, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev)

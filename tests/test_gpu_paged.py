@@ -300,6 +300,100 @@ def test_rows_behind_the_last_sequence_stay(hd, orc):
     assert hd.hybrid_decode_device_errors(ctx) == 0
 
 
+def many_spans(seed, long_one):
+    rng = np.random.default_rng(seed)
+    spans = [(int(c), int(n)) for c, n in zip(rng.integers(0, 150, 300), rng.integers(0, 4, 300))]
+    if long_one:
+        spans[137] = (33, 90)
+    return spans
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("long_one", [False, True])
+def test_more_sequences_than_a_block_has_threads(hd, orc, kv, long_one):
+    """300 sequences of 0 to 3 new tokens, with a chunk among them or without: append, attention, choice of blocks."""
+    case = PagedCase(57, many_spans(57, long_one), group=2, page=16, kv=kv, appended=False)
+    ctx, d = context(hd, 2, 2, kv, max_batch=300, max_context=300), case.device()
+    k, v = (synth.normal_bf16(case.rng, (case.rows, 2, D)) for _ in range(2))
+    held = page_bounds(case)
+    held = torch.where(torch.isinf(held), torch.tensor(float("nan"), dtype=torch.bfloat16), held)
+    kp, vp, bd, _ = reference_append(orc, case, FULL, None, k, v, held)
+    bounds = held.cuda()
+    batch, cache = case.batch_of(hd, d), cache_of(hd, d, bounds)
+    hd.rope_append_paged(ctx, 1, batch, None, k.cuda(), v.cuda(), None, cache)
+    assert_bits_equal(d["k"], kp, "K pages")
+    assert_bits_equal(d["v"], vp, "V pages")
+    case.k, case.v = d["k"].cpu(), d["v"].cpu()
+    rows = list(range(0, case.rows, 7)) + [case.rows - 1]
+    out, lse = run_attn(hd, ctx, case, d)
+    assert_rows(reference_rows(orc, case, rows), out, lse)
+    selected = torch.empty(case.rows, 2, 3, dtype=torch.int32, device="cuda")
+    hd.select_pages(ctx, 1, batch, d["q"], cache, selected, 1, 1)
+    want = reference_selection(case, torch.from_numpy(bd), 3, 1, 1)
+    assert np.array_equal(selected.cpu().numpy(), want)
+    out, lse = run_attn(hd, ctx, case, d, selected=selected)
+    assert_rows(reference_rows(orc, case, rows, selected=want), out, lse)
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+
+
+def test_rows_before_the_first_sequence_stay(hd, orc):
+    case = PagedCase(58, [(100, 3), (7, 20), (300, 1)])
+    ctx, d = context(hd), case.device()
+    n = case.rows + 4
+    d["offsets"] = d["offsets"] + 4
+    q = torch.cat([torch.full((4, case.q_heads, D), float("nan"), dtype=torch.bfloat16, device="cuda"), d["q"]])
+    for max_tokens in (20, 500):
+        out = torch.full((n, case.q_heads, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((n, case.q_heads), 7.0, device="cuda")
+        hd.attn_paged(ctx, 1, case.batch_of(hd, d, num_tokens=n, max_tokens=max_tokens), q, cache_of(hd, d), None, out, lse)
+        assert_rows(reference_rows(orc, case), out[4:], lse[4:])
+        assert (out[:4] == 7.0).all() and (lse[:4] == 7.0).all()
+    selected = torch.full((n, 2, 2), 99, dtype=torch.int32, device="cuda")
+    bounds = page_bounds(case)
+    hd.select_pages(ctx, 1, case.batch_of(hd, d, num_tokens=n), q, cache_of(hd, d, bounds.cuda()), selected)
+    assert (selected[:4] == 99).all()
+    assert np.array_equal(selected[4:].cpu().numpy(), reference_selection(case, bounds, 2, 1, 1))
+    q_rot = torch.full_like(q, 5.0)
+    k = torch.zeros(n, 2, D, dtype=torch.bfloat16, device="cuda")
+    hd.rope_append_paged(ctx, 1, case.batch_of(hd, d, num_tokens=n), q, k, k, q_rot, cache_of(hd, d))
+    assert (q_rot[:4] == 5.0).all() and not (q_rot[4:] == 5.0).any(-1).any(-1).all()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 70])
+def test_sequences_that_share_their_first_pages(hd, orc, kv, n):
+    case = PagedCase(59, [(640, n), (640, n), (700, n)], kv=kv)
+    case.table[1, :9] = case.table[0, :9]
+    case.table[2, :8] = case.table[0, :8]
+    check_attn(hd, orc, case)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_offsets_past_32_bits(hd, orc, n):
+    """Pages 2^31 + 64 elements apart: the second starts beyond 4 GiB."""
+    case = PagedCase(64, [(100, n)], page=64, spare=1, appended=False)
+    assert case.table[0, :2].max() >= 1
+    gap, H = 2 ** 31 + 64, case.kv_heads
+    d = case.device()
+    pool = {}
+    for name in ("k", "v"):
+        flat = torch.empty((case.pool - 1) * gap + H * 64 * D, dtype=torch.bfloat16, device="cuda")
+        pool[name] = flat.as_strided((case.pool, H, 64, D), (gap, 64 * D, D, 1))
+        pool[name].copy_(d[name])
+        d[name] = pool[name]
+    ctx = context(hd)
+    k, v = (synth.normal_bf16(case.rng, (case.rows, H, D)) for _ in range(2))
+    kp, vp, _, _ = reference_append(orc, case, FULL, None, k, v)
+    hd.rope_append_paged(ctx, 1, case.batch_of(hd, d), None, k.cuda(), v.cuda(), None, cache_of(hd, d))
+    assert_bits_equal(d["k"].contiguous(), kp, "K pages")
+    assert_bits_equal(d["v"].contiguous(), vp, "V pages")
+    case.k, case.v = d["k"].cpu().contiguous(), d["v"].cpu().contiguous()
+    out, lse = run_attn(hd, ctx, case, d)
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    assert_rows(reference_rows(orc, case), out, lse)
+
+
 # ------------------------------------------------------------ page selection --
 
 def page_bounds(case):
@@ -478,6 +572,25 @@ def test_on_another_stream(hd, orc):
     assert_rows(reference_rows(orc, case), out, lse)
 
 
+def test_two_contexts_at_once(hd, orc):
+    """Calls of two contexts in flight together on two streams, long ones, again and again."""
+    cases = [PagedCase(97, [(19000, 1), (300, 1), (9000, 1)]), PagedCase(98, [(9000, 130), (0, 300)])]
+    ctxs = [context(hd), context(hd, max_batch=8)]
+    dev, streams = [c.device() for c in cases], [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    first = [run_attn(hd, x, c, d) for x, c, d in zip(ctxs, cases, dev)]
+    outs = [[(torch.empty_like(o), torch.empty_like(l)) for o, l in first] for _ in range(6)]
+    torch.cuda.synchronize()
+    for row in outs:
+        for x, c, d, s, (out, lse) in zip(ctxs, cases, dev, streams, row):
+            hd.attn_paged(x, 1, c.batch_of(hd, d), d["q"], cache_of(hd, d), None, out, lse, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for c, f in zip(cases, first):
+        assert_rows(reference_rows(orc, c, range(0, c.rows, 40)), *f)
+    for row in outs:
+        assert all(torch.equal(a, b) for got, f in zip(row, first) for a, b in zip(got, f))
+
+
 # ---------------------------------------------------------------- bad values --
 
 def test_bad_sequences_are_flagged_and_the_rest_served(hd, orc):
@@ -500,6 +613,23 @@ def test_bad_sequences_are_flagged_and_the_rest_served(hd, orc):
         assert np.array_equal(synth.bits(before[0][mine]), synth.bits(d["k"][mine]))
         d["k"].copy_(before[0])
         d["v"].copy_(before[1])
+
+
+def test_bad_single_tokens_are_flagged(hd, orc):
+    case = PagedCase(96, [(100, 1), (50, 1), (700, 1)], page=16, single=True)
+    ctx, d, bounds = context(hd, max_context=1000), case.device(), page_bounds(case).cuda()
+    want = reference_selection(case, bounds.cpu(), 3, 1, 1)
+    for value, bit in ((-1, 1), (1001, 4), (900, 2)):
+        d["context"] = torch.tensor([100, value, 700], dtype=torch.int32, device="cuda")
+        selected = torch.full((3, 2, 3), 99, dtype=torch.int32, device="cuda")
+        hd.select_pages(ctx, 1, case.batch_of(hd, d), d["q"], cache_of(hd, d, bounds), selected)
+        assert hd.hybrid_decode_device_errors(ctx) == bit
+        assert (selected[1] == -1).all() and np.array_equal(selected[::2].cpu().numpy(), want[::2])
+        for chosen in (None, selected):
+            out, lse = run_attn(hd, ctx, case, d, selected=chosen)
+            assert hd.hybrid_decode_device_errors(ctx) == bit
+            assert torch.isnan(out[1].float()).all() and torch.isnan(lse[1]).all()
+            assert_rows(reference_rows(orc, case, [0, 2], selected=None if chosen is None else want), out, lse)
 
 
 def test_bad_offsets_are_flagged(hd, orc):
@@ -545,3 +675,46 @@ def test_lost_copy_times_out_and_the_context_recovers(hd, orc):
     assert hd.hybrid_decode_device_errors(ctx) & 8
     hd.hybrid_decode_inject_lost_copy(ctx, -1)
     check_attn(hd, orc, case)
+
+
+def test_refusals(hd):
+    def refused(status, f, *args, **kw):   # 1: invalid argument, 2: unsupported, 3: capacity, 5: state
+        with pytest.raises(hd.HDError) as e:
+            f(*args, **kw)
+        assert e.value.status == status
+
+    case = PagedCase(94, [(100, 1), (300, 1)], page=16, single=True)
+    ctx, d = context(hd), case.device()
+    batch, bounds = case.batch_of(hd, d), page_bounds(case).cuda()
+    cache, plain = cache_of(hd, d, bounds), cache_of(hd, d)
+    q, out = d["q"], torch.empty_like(d["q"])
+    lse = torch.empty(2, 8, device="cuda")
+    sel = torch.empty(2, 2, 4, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(2, 2, D, dtype=torch.bfloat16, device="cuda")
+    refused(5, hd.select_pages, ctx, 0, batch, q, cache, sel)
+    refused(5, hd.attn_selected_pages, ctx, 0, batch, q, cache, sel, None, out, lse)
+    refused(1, hd.select_pages, ctx, 1, batch, q, plain, sel)
+    refused(1, hd.select_pages, ctx, 1, batch, q, cache, sel, 3, 2)
+    refused(1, hd.select_pages, ctx, 1, batch, q, cache, sel, -1, 2)
+    refused(1, hd.attn_paged, ctx, 2, batch, q, cache, None, out, lse)
+    refused(1, hd.rope_append_paged, ctx, 1, batch, None, torch.zeros(2, 4 + 2 * D, dtype=torch.bfloat16,
+            device="cuda")[:, :2 * D].view(2, 2, D), kv, None, cache)
+    odd = torch.zeros(2 * 2 * D + 8, dtype=torch.bfloat16, device="cuda")[4:4 + 2 * 2 * D].view(2, 2, D)
+    refused(1, hd.rope_append_paged, ctx, 1, batch, None, odd, kv, None, cache)
+    small = context(hd, max_batch=1, max_context=16)
+    refused(3, hd.attn_paged, small, 1, batch, q, cache, None, out, lse)
+    many = PagedCase(95, [(0, 64)] * 1, page=16)
+    m = many.device()
+    wide = torch.empty(4096, 8, D, dtype=torch.bfloat16, device="cuda")
+    refused(3, hd.select_pages, context(hd, max_batch=1, max_context=262144), 1,
+            hd.paged_batch(torch.zeros(1, 16384, dtype=torch.int32, device="cuda"), m["context"], m["offsets"],
+                           num_tokens=4096, max_tokens=4096),
+            wide, cache_of(hd, m, page_bounds(many).cuda()), torch.empty(4096, 2, 4, dtype=torch.int32, device="cuda"))
+    ctx8 = hd.hybrid_decode_init(hd.Config(layer_types=[FULL], num_q_heads=8, num_kv_heads=2, max_batch=2, max_context=400,
+                                           sliding_window=64, rotary_dim_full=36))
+    refused(2, hd.rope_append_paged, ctx8, 0, batch, None, kv, kv, None, cache)
+    ctx8.close()
+    for bad in (dict(q=q, q_rot=None), dict(q=None, q_rot=out)):
+        with pytest.raises(ValueError):
+            hd.rope_append_paged(ctx, 1, batch, bad["q"], kv, kv, bad["q_rot"], cache)
+    assert hd.hybrid_decode_device_errors(ctx) == 0

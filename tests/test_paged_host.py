@@ -85,3 +85,31 @@ def test_binding_refuses_host_tensors(hd):
         hd.paged_batch(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         hd.paged_batch(torch.zeros(3, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+
+
+def test_binding_refuses_pages_of_another_device(hd, monkeypatch):
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ctx = SimpleNamespace(cfg=SimpleNamespace(num_kv_heads=2, kv_dtype=hd.HD_KV_BF16))
+    b, c = descriptors(hd)
+    there, here = torch.device("cuda", 1), torch.device("cuda", 0)
+
+    def pair(batch_device, cache_device):
+        cache = hd.PagedCache(c, (), (4, 2, 64, 256), cache_device)
+        cache.fp8 = False
+        return hd.PagedBatch(b, (), batch_device), cache
+
+    hd._check_paged(ctx, *pair(here, here))
+    for devices in ((there, there), (here, there), (there, here)):
+        with pytest.raises(ValueError):
+            hd._check_paged(ctx, *pair(*devices))
+
+
+def test_binding_checks_rows(hd):
+    one = torch.zeros(5, 2, 256, dtype=torch.bfloat16)[:, :1]          # one head of wider rows
+    hd._check_rows("k", one, (5, 1, 256), torch.bfloat16, one.device, True)
+    with pytest.raises(ValueError):
+        hd._check_rows("k", one, (5, 1, 256), torch.bfloat16, one.device)
+    for bad in (torch.zeros(5, 1, 512, dtype=torch.bfloat16)[..., ::2], one.float(), one[:4]):
+        with pytest.raises(ValueError):
+            hd._check_rows("k", bad, (5, 1, 256), torch.bfloat16, one.device, True)
