@@ -7,7 +7,9 @@ library and raises if it has not been built -- there is no fallback.
 
 Names follow the C entry points: ``hybrid_decode_init``, ``rope_append_kv``,
 ``decode_attn_sliding``, ``decode_attn_full``, ``decode_step`` (plus
-``hybrid_decode_destroy`` and the helpers).  Each call raises ``HDError``
+``hybrid_decode_destroy`` and the helpers); over paged caches ``paged_cache``,
+``paged_batch``, ``rope_append_paged``, ``attn_paged``, ``select_pages`` and
+``attn_selected_pages``.  Each call raises ``HDError``
 carrying the hd_status when the library rejects it.
 """
 from __future__ import annotations
