@@ -244,6 +244,16 @@ def test_chunks(hd, orc, spans, group, kv, page, window):
     check_attn(hd, orc, case, rows=rows, sink=sinks(case), gate=gate)
 
 
+@pytest.mark.parametrize("rows", [128, 132])   # at group 4: all of one CTA, and a few of its peer
+@pytest.mark.parametrize("kv,page", [("bf16", 16), ("bf16", 32), ("bf16", 128), ("e4m3", 16), ("e4m3", 64)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_chunks_of_one_ctas_rows_and_just_more(hd, orc, rows, kv, page, window):
+    n = rows // 4
+    case = PagedCase(60, [(700, n), (0, n - 1), (4000, 1), (129, 5), (63, n)], page=page, kv=kv, window=window)
+    check_attn(hd, orc, case, rows=list(range(0, case.rows, 3)) + [case.rows - 1], sink=sinks(case),
+               ctx=context(hd, kv=kv, window=window or 512))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_small_window(hd, orc, kv):
     """A window shorter than a page and than a tile of new tokens."""
