@@ -86,7 +86,8 @@ __device__ __forceinline__ SeqSpan span_of_row(const PagedSeqs &s, int r, int *b
 }
 
 // Block-wide prefix sum of 64-bit counts; `tmp`: [33] in shared
-// memory.  Returns this thread's exclusive prefix and the total.
+// memory, which every thread reads last: callers owe a barrier before `tmp` is
+// written again.  Returns this thread's exclusive prefix and the total.
 __device__ __forceinline__ long long block_prefix(long long x, long long *tmp, long long *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
     long long v = x;

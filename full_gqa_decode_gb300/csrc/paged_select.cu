@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_co
         equal += x == 1;
     }
     long long total;
+    __syncthreads();   // the first count's readers of scan are through
     const long long before = block_prefix((long long)chosen << 32 | equal, scan, &total);
     chosen = (int)(before >> 32);
     equal = (int)(before & 0xFFFFFFFF);
