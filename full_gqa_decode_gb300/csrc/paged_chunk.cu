@@ -95,6 +95,7 @@ enum : int {
     BAR_P = 22,        // [2] first CTA: the weights of both CTAs are written, by the tile's parity
     BAR_O_FULL = 24,   // a segment's output is complete
     BAR_O_FREE = 25,   // first CTA: both CTAs have read it
+    BAR_DRAIN = 26,    // every MMA of the pair is complete (its only phase, at the end)
 };
 
 struct ChunkTile {
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         for (int i = 0; i < 2; ++i) mbar_init(&bar[BAR_P + i], 2 * kSoftWarps);
         mbar_init(&bar[BAR_O_FULL], 1);
         mbar_init(&bar[BAR_O_FREE], 2 * kSoftWarps);
+        mbar_init(&bar[BAR_DRAIN], 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -390,10 +392,17 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         const int tok = kCtaRows >> a.group_shift;
         RingPos<kSlots> pos;
         int issued = 0, blocks = 0;   // blocks: before this segment
+        int copied = 0;               // operands whose copies were issued: the first so many
+        uint32_t q_copied = 0;        // segments whose query rows were
         int last_read = -1;
         for (uint32_t seg = 0; more; ++seg) {
             int pg = kFp8 ? 0 : pages_of(w, 0), pg_v = 0;
-            if (seg) wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
+            if (seg) {
+                wait_warp(&bar[BAR_Q_EMPTY], (seg - 1) & 1, dead, err);
+                // A barrier whose copy has not landed must not be armed again: so after a wait of others ran out.
+                dead = __any_sync(0xffffffffu, dead || !mbar_try_wait(&bar[BAR_Q_FULL], (seg - 1) & 1));
+            }
+            if (!dead) ++q_copied;
             if (lane == 0 && !dead) {
                 mbar_arrive_expect_tx(&bar[BAR_Q_FULL], kQBytes);
                 tma_load_4d(smem, &maps.q, &bar[BAR_Q_FULL], 0, w.h << a.group_shift, w.q.row0 + w.t.t0 + rank * tok, 0);
@@ -412,7 +421,9 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     if (lane == pos.st) last_read = r;
                     uint8_t *dst = ring + pos.st * kSlotBytes;
                     uint64_t *full = &bar[BAR_FULL + pos.st];
+                    if (!pos.first) dead = __any_sync(0xffffffffu, dead || !mbar_try_wait(full, pos.ph ^ 1));
                     const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
+                    if (!drop) ++copied;
                     if (!drop && lane == 0) mbar_arrive_expect_tx(full, kSlotBytes);
                     __syncwarp();
                     const int shift = kind == 0 ? rk_shift : rv_shift;
@@ -440,8 +451,13 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                              "r"(0), "r"(w.h << a.group_shift), "r"(w.q.row0 + w.t.t0 + rank * tok), "r"(0)
                              : "memory");
         }
+        // This CTA's copies land before it leaves, whoever still waits for them: a lane per slot, and one for the rows.
+        bool landed = true;
+        if (lane < kSlots && lane < copied) landed = mbar_wait(&bar[BAR_FULL + lane], (uint32_t)((copied - 1 - lane) / kSlots) & 1);
+        if (lane == kSlots && q_copied) landed = mbar_wait(&bar[BAR_Q_FULL], (q_copied - 1) & 1);
+        if (!landed) atomicOr(err, HD_DEVERR_WAIT_TIMEOUT);
     } else if (warp == kMmaWarp) {
-        // ---- products, block by block ----
+        // ---- products, block by block; once a wait has run out the commits go on alone, for those who wait for them ----
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdS = pair_idesc(128, !kFp8, 0), kIdO = pair_idesc(256, !kFp8, 1);
             const int rv_shift = kFp8 ? 7 : min(sq.page_shift, 7);
@@ -464,9 +480,11 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         tc_fence_after();
                         const uint64_t vd = vd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
                         const uint32_t p = tmem + (uint32_t)(g & 1) * 128;
+                        if (!dead) {
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, i > 2 || t > 0);
+                            for (int t = 0; t < 8; ++t)
+                                pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, i > 2 || t > 0);
+                        }
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
                     }
@@ -476,10 +494,12 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         tc_fence_after();
                         const uint64_t kd = kd0 + (uint64_t)((uint32_t)pos.st * kSlotBytes >> 4);
                         const uint32_t d = tmem + (uint32_t)((tiles + i) & 1) * 128;
+                        if (!dead) {
 #pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)
-                            pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                                        kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                            for (int kk = 0; kk < 16; ++kk)
+                                pair_mma_ss(d, qd0 + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                            kd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                        }
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
                     }
@@ -491,6 +511,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 tiles += w.L;
                 more = w.next(a);
             }
+            pair_commit(&bar[BAR_DRAIN]);
         }
     }
     } else if (kFp8 && warp >= kStageWarp) {
@@ -518,10 +539,16 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         auto wait_slot = [&]() {
             if (!pos.first) wait_warp(&bar[BAR_EMPTY + pos.st], pos.ph ^ 1, dead, err);
         };
+        int number = 0;   // of the operand at pos, as the copy warp counts them
+        auto to_operand = [&](int n) {
+            pos.step(n);
+            number += n;
+        };
         auto hand_on = [&]() {
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
+            const bool drop = a.drop_stage >= 0 && number >= a.drop_stage;
+            if (lane == 0 && !drop) mbar_arrive_remote(ready0 + 8 * pos.st);
         };
         if (warp < kStageWarp + 4) {
             // K(k), of a segment's loads the first and then number 2 k - 1: this CTA's 64 keys x 16 chunks.
@@ -576,7 +603,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
 #pragma unroll
                     for (int s = 0; s < 8; ++s) put(slot, codes[s], s * 8 + sw * 2 + row2, chunk, 8192);
                     hand_on();
-                    pos.step(k + 1 < L ? (k ? 2 : 1) : (k ? 3 : 2));   // to the next K, over the last V's at the end
+                    to_operand(k + 1 < L ? (k ? 2 : 1) : (k ? 3 : 2));   // to the next K, over the last V's at the end
                     if (k + 1 < L) load(k + 1);
                 }
                 more = w.next(a);
@@ -600,14 +627,14 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             if (more) load(0);
             while (more) {
                 const int L = w.L;
-                pos.step(L > 1 ? 2 : 1);
+                to_operand(L > 1 ? 2 : 1);
                 for (int k = 0; k < L; ++k) {
                     wait_slot();
                     uint8_t *slot = ring + pos.st * kSlotBytes;
 #pragma unroll
                     for (int s = 0; s < 8; ++s) put(slot, codes[s], s * 16 + sw * 4 + row4, chunk, 16384);
                     hand_on();
-                    pos.step(k + 2 < L ? 2 : 1);
+                    to_operand(k + 2 < L ? 2 : 1);
                     if (k + 1 < L) load(k + 1);
                 }
                 more = w.next(a);
@@ -893,12 +920,16 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         }
     }
     __syncwarp();
-    // No CTA leaves while its peer's MMAs or arrivals may still reach it.
+    // No CTA leaves, and no tensor memory is freed, while MMAs of the pair or its peer's arrivals may still reach it: when
+    // waits have run out, nobody else has waited for the last ones.
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
-    tc_fence_after();
-    if (warp == kMmaWarp) pair_dealloc(tmem);
+    if (warp == kMmaWarp) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar[BAR_DRAIN], 0)) && lane == 0) atomicOr(err, HD_DEVERR_WAIT_TIMEOUT);
+        tc_fence_after();
+        pair_dealloc(tmem);
+    }
 }
 
 template <int KV>

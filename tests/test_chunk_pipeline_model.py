@@ -6,7 +6,9 @@ interleavings.  It checks that
   * a product reads the operands it is meant to, in both CTAs, and nobody
     overwrites a slot, the query rows, a score buffer or the output in use;
   * no barrier is armed while its copy is still on the way (a fault on a GPU);
-  * the pair always comes to its end.
+  * the pair always comes to its end;
+  * when waits run out, a CTA leaves only after its copies have landed and the
+    pair's products are complete.
 
 The rules in the model are the kernel's, statement for statement; the test of
 the source names those that the model rests on, so that a change there asks for
@@ -45,6 +47,11 @@ def test_the_model_follows_the_source():
         "if (i == w.L + 1) pair_commit(&bar[BAR_O_FULL]);", "blocks += w.L + 2;",
         # the E4M3 stage warps' way through the ring
         "(k + 1 < L ? (k ? 2 : 1) : (k ? 3 : 2));", "(L > 1 ? 2 : 1);", "(k + 2 < L ? 2 : 1);",
+        # once a wait has run out: no barrier armed unseen, no way out before copies and products are through
+        "dead = __any_sync(0xffffffffu, dead || !mbar_try_wait(&bar[BAR_Q_FULL], (seg - 1) & 1));",
+        "if (!pos.first) dead = __any_sync(0xffffffffu, dead || !mbar_try_wait(full, pos.ph ^ 1));",
+        "mbar_wait(&bar[BAR_FULL + lane], (uint32_t)((copied - 1 - lane) / kSlots) & 1);",
+        "mbar_wait(&bar[BAR_Q_FULL], (q_copied - 1) & 1);", "pair_commit(&bar[BAR_DRAIN]);", "mbar_wait(&bar[BAR_DRAIN], 0)",
     ):
         assert " ".join(rule.split()) in text, rule
 
@@ -169,7 +176,7 @@ class Pair:
         """A wait with a limit, which `role` does not make any more once one ran out."""
         if role.dead or barrier.over(parity):
             return
-        yield lambda: barrier.over(parity) or self.gave_up or role.timed_out
+        yield lambda: barrier.over(parity) or role.timed_out
         if not barrier.over(parity):
             role.dead = True
 
@@ -389,9 +396,17 @@ def sequences(seed, n):
 
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_every_interleaving_tried_holds(e4m3):
-    for i, tiles in enumerate(sequences(1, 500)):
+    for i, tiles in enumerate(sequences(1, 250)):
         for seed in range(4):
             Pair(tiles, e4m3, 1000 * i + seed).run()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pairs_whose_waits_run_out_leave_nothing_under_way(e4m3):
+    for i, tiles in enumerate(sequences(2, 200)):
+        Pair(tiles, e4m3, i, lost=i % (2 * sum(tiles))).run()
+        for seed in range(3):
+            Pair(tiles, e4m3, 1000 * i + seed, impatient=True).run()
 
 
 @pytest.mark.parametrize("mutant,e4m3", [("last block only", False), ("rows early", False), ("rows early", True),
@@ -402,3 +417,11 @@ def test_mutants_fail(mutant, e4m3):
         for i, tiles in enumerate(sequences(3, 300)):
             for seed in range(4):
                 Pair(tiles, e4m3, 1000 * i + seed, mutant=mutant).run()
+
+
+@pytest.mark.parametrize("mutant,e4m3", [("leave at once", False), ("leave at once", True), ("arm unseen", False)])
+def test_mutants_fail_once_waits_run_out(mutant, e4m3):
+    with pytest.raises(Wrong):
+        for i, tiles in enumerate(sequences(3, 300)):
+            for seed in range(4):
+                Pair(tiles, e4m3, 1000 * i + seed, impatient=True, mutant=mutant).run()
