@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         int st = 0, odd = 0;   // ring slot, and kRing in the ring's odd rounds
         uint32_t ph = 0;
         bool dead = false;
-        int issued = 0;
+        int issued = 0, copied = 0;   // stages; those whose copies were issued, the first so many
         while (x < share) {
             const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
             const int seg = min(t.units - c.off, share - x);
@@ -505,8 +505,12 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                 for (int i = 0; i < cnt; i += copies) {   // copies divides 32
                     uint8_t *dst = smem + st * kStageBytes;
                     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1));
+                    // A barrier whose copies have not landed must not be armed again: so after a wait of its team ran out.
+                    if (!dead && issued >= kFulls)
+                        dead = !__all_sync(0xffffffffu, mbar_try_wait(&full[st + odd], (uint32_t)(issued / kFulls - 1) & 1));
                     const bool drop = dead || (a.drop_stage >= 0 && issued >= a.drop_stage);
                     if (!drop) {
+                        ++copied;
                         const bool mine = lane >= i && lane < i + (int)copies;
                         if (SPARSE && mine) runs[st * 4 + lane - i] = pos;
                         __syncwarp();
@@ -529,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             x += seg;
             if (x < share) next_item<KV, SPARSE>(a, c, q);
         }
-        if (dead && lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
+        // The copies land before the CTA leaves, whoever still waits for them: a lane per barrier.
+        if (lane < kFulls && lane < copied && !mbar_wait(&full[lane], (uint32_t)((copied - 1 - lane) / kFulls) & 1)) dead = true;
+        if (__any_sync(0xffffffffu, dead) && lane == 0) atomicOr(sq.err, HD_DEVERR_WAIT_TIMEOUT);
         return;
     }
 

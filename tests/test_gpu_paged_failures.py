@@ -45,3 +45,11 @@ def lose_copies(hd, orc, case, ctx, stage):
 def test_chunks(hd, orc, kv, spans, stage):
     """Stage 3 leaves a block of two operands half loaded, stage 6 a ring that has gone round."""
     lose_copies(hd, orc, PagedCase(110 + stage, spans, kv=kv), context(hd, kv=kv), stage)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("stage", [0, 5, 14])
+def test_single_tokens(hd, orc, kv, stage):
+    """Stage 5 leaves the ring's last slot empty, stage 14 is in the second round of the barriers."""
+    lose_copies(hd, orc, PagedCase(120 + stage, [(19000, 1), (300, 1), (9000, 1), (18000, 1)] * 2, kv=kv, single=True),
+                context(hd, kv=kv), stage)
