@@ -499,7 +499,7 @@ def paged_batch(block_table: torch.Tensor, context: torch.Tensor, token_offsets:
     """Describe the sequences of a paged call: int32 CUDA tensors ``block_table`` [batch, max_blocks],
     ``context`` [batch] (previous tokens) and ``token_offsets`` [batch + 1] (None: one new token per
     sequence).  ``num_tokens``: rows of q / k / v / out (default: the batch); ``max_tokens`` and
-    ``max_context``: bounds on a sequence's new tokens and context (0: what the context serves)."""
+    ``max_context``: bounds on a sequence's new tokens and context (0: the configuration's)."""
     batch = context.shape[0]
     if context.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, max_blocks] and context [batch]")

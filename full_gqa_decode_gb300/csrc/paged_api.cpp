@@ -36,7 +36,7 @@ hd_status check_paged(const hd_ctx *ctx, int layer, const hd_paged_batch *b, con
     s->num_tokens = b->num_tokens;
     s->max_tokens = b->max_tokens;
     s->max_blocks = b->max_blocks;
-    s->max_context = b->max_context ? b->max_context : std::max(ctx->cfg.max_context - b->max_tokens + 1, 0);
+    s->max_context = b->max_context ? b->max_context : ctx->cfg.max_context;   // seq_span looks at context + tokens too
     s->max_position = ctx->cfg.max_context;
     s->page_shift = shift;
     s->num_pages = c->num_pages;

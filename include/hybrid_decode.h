@@ -440,11 +440,11 @@ hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_head
  * allocates.  hd_paged_cache and hd_paged_batch are read during the call only.
  *
  * Bad values on the device: a sequence with bad token_offsets, more than
- * max_tokens tokens, a context below 0 or above max_context, or a position past
- * the block table or the rotary table is flagged (HD_DEVERR_*), not stored, and
- * gets NaN out / lse; a needed page outside the pool is flagged, skipped by the
- * append and read as zeros by the attention.  Rows of out / lse / q_rot /
- * selected that belong to no sequence stay as they are. */
+ * max_tokens tokens, a context below 0 or above the call's max_context, or a
+ * position past the block table or the rotary table is flagged (HD_DEVERR_*),
+ * not stored, and gets NaN out / lse; a needed page outside the pool is flagged,
+ * skipped by the append and read as zeros by the attention.  Rows of out / lse /
+ * q_rot / selected that belong to no sequence stay as they are. */
 
 /* A pool of pages.  k / v: page p starts at p * page_stride elements; within it
  * [num_kv_heads][page_size][head_dim], bf16 or E4M3 codes.  page_size: 16, 32,
@@ -473,9 +473,10 @@ typedef struct {
  * allowed); NULL: one token each, row b.  num_tokens: rows of the tensors.
  * With num_tokens 0 a call does nothing and the row tensors may be NULL.
  * max_tokens: a bound on any sequence's new tokens; max_context: a bound on
- * context[b] (0: the largest the context serves, max_context - max_tokens + 1).
- * The bounds pick kernels and grid sizes; results agree within the stated
- * tolerances whatever they are. */
+ * context[b] (0: the configuration's).  Whatever the bounds, a sequence is
+ * served when its last new token's position is at most the configuration's
+ * max_context; they pick kernels and grid sizes, and results agree within the
+ * stated tolerances whatever they are. */
 typedef struct {
     const int32_t *block_table;
     const int32_t *context;
