@@ -21,7 +21,7 @@ struct SeqSpan {
     int row0, n, ctx;
 };
 
-// Row range of sequence b, or false (and *bit) when its offsets cannot be used.
+// Row range of sequence b, or false (and *bit) when its offsets cannot be used: then the rows among them that exist.
 __device__ __forceinline__ bool seq_rows(const PagedSeqs &s, int b, int *row0, int *n, int *bit) {
     *row0 = b;
     *n = 1;
@@ -31,6 +31,8 @@ __device__ __forceinline__ bool seq_rows(const PagedSeqs &s, int b, int *row0, i
         *n = 0;
         if (lo < 0 || hi < lo || hi > s.num_tokens) {
             *bit = HD_DEVERR_TOKEN_OFFSETS;
+            *row0 = max(lo, 0);
+            *n = max(min(hi, s.num_tokens) - *row0, 0);
             return false;
         }
         *n = hi - lo;
@@ -44,9 +46,9 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedSeqs &s, int b, int *bit,
     SeqSpan q{0, 0, 0};
     *bit = 0;
     int n = 0;
-    if (!seq_rows(s, b, &q.row0, &n, bit)) return q;
+    const bool usable = seq_rows(s, b, &q.row0, &n, bit);
     if (rows) *rows = n;
-    if (n == 0) return q;
+    if (!usable || n == 0) return q;
     q.ctx = s.context[b];
     if (n > s.max_tokens) *bit = HD_DEVERR_TOKEN_OFFSETS;
     else if (q.ctx < 0) *bit = HD_DEVERR_CONTEXT_NEGATIVE;

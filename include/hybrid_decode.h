@@ -442,7 +442,8 @@ hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_head
  * Bad values on the device: a sequence with bad token_offsets, more than
  * max_tokens tokens, a context below 0 or above the call's max_context, or a
  * position past the block table or the rotary table is flagged (HD_DEVERR_*),
- * not stored, and gets NaN out / lse; a needed page outside the pool is flagged,
+ * not stored, and gets NaN out / lse and a list of -1 (in those of its rows that
+ * exist, when the offsets leave the tensors); a needed page outside the pool is flagged,
  * skipped by the append and read as zeros by the attention.  Rows of out / lse /
  * q_rot / selected that belong to no sequence stay as they are. */
 

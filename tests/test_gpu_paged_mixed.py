@@ -48,3 +48,25 @@ def test_running_sequences_at_the_end_of_the_range_beside_a_prompt(hd, orc, kv):
     d["context"][2] = 991
     run_attn(hd, ctx, case, d)
     assert hd.hybrid_decode_device_errors(ctx) == 4
+
+
+@pytest.mark.parametrize("max_tokens", [4, 40])   # single kernel of few rows, and the one of chunks
+def test_rows_that_bad_offsets_name_are_nan(hd, orc, max_tokens):
+    """Offsets that leave the tensors: the sequence's rows inside them, and no others."""
+    case = PagedCase(131, [(100, 3), (50, 2), (200, 4)], group=1 if max_tokens == 4 else 4)
+    ctx, d = context(hd, case.group), case.device()
+    bounds = page_bounds(case)
+    want = reference_selection(case, bounds, 3, 1, 1)
+    for offs, bad in (([0, 3, 5, 900], range(5, 9)), ([-4, 3, 5, 9], range(0, 3)), ([0, 3, 5, -1], range(0))):
+        d["offsets"] = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        out, lse = run_attn(hd, ctx, case, d, max_tokens=max_tokens)
+        assert hd.hybrid_decode_device_errors(ctx) == 16, offs
+        selected = torch.full((case.rows, 2, 3), 99, dtype=torch.int32, device="cuda")
+        hd.select_pages(ctx, 1, case.batch_of(hd, d, max_tokens=max_tokens), d["q"], cache_of(hd, d, bounds.cuda()), selected)
+        assert hd.hybrid_decode_device_errors(ctx) == 16, offs
+        for r in range(case.rows):
+            if r in bad:
+                assert torch.isnan(out[r].float()).all() and torch.isnan(lse[r]).all() and (selected[r] == -1).all()
+        good = [r for r in range(5 if offs[3] != 9 else 9) if r not in bad]
+        assert_rows(reference_rows(orc, case, good), out, lse)
+        assert np.array_equal(selected[good].cpu().numpy(), want[good])
