@@ -175,7 +175,6 @@ void free_ctx(hd_ctx *ctx) {
     cudaFree(ctx->stage_v);
     cudaFree(ctx->counters);
     cudaFree(ctx->err);
-    cudaFree(ctx->paged_ws);
     cudaFree(ctx->paged_tickets);
     for (auto e : ctx->ev_begin) cudaEventDestroy(e);
     for (auto e : ctx->ev_end) cudaEventDestroy(e);
@@ -619,6 +618,11 @@ hd_status hybrid_decode_init(const hd_config *cfg, hd_ctx **out_ctx) {
         if (ch > 1) fused += (int64_t)B * Hkv * kMaxRows * ch;
     }
     ctx->part_rows = std::max<int64_t>(slots * Hkv * kMaxRows, std::min<int64_t>(fused, 1LL << 20));
+    // The paged calls' workspace is the same memory: calls on one context are ordered.
+    const int64_t row_bytes = kHeadDim * sizeof(float);
+    const int64_t paged = std::max(paged_partial_bytes(ctx->num_sms),
+                                   any_full ? paged_rank_bytes(B, Hkv, cfg->max_context) : 0);
+    ctx->part_rows = std::max(ctx->part_rows, (paged + row_bytes - 1) / row_bytes);
     const size_t counters = (size_t)cfg->num_layers * B * Hkv * sizeof(int32_t);
     bool ok = cudaMalloc(&ctx->part_o, (size_t)ctx->part_rows * kHeadDim * sizeof(float)) == cudaSuccess &&
               cudaMalloc(&ctx->part_ml, (size_t)ctx->part_rows * sizeof(float2)) == cudaSuccess &&
@@ -627,10 +631,7 @@ hd_status hybrid_decode_init(const hd_config *cfg, hd_ctx **out_ctx) {
               cudaMalloc(&ctx->err, sizeof(int32_t)) == cudaSuccess &&
               cudaMemset(ctx->err, 0, sizeof(int32_t)) == cudaSuccess;
     const size_t stage = (size_t)cfg->num_layers * B * Hkv * kHeadDim * kv_elem_bytes(ctx->kv_type);
-    ctx->paged_ws_bytes = std::max(paged_partial_bytes(ctx->num_sms),
-                                   any_full ? paged_rank_bytes(B, Hkv, cfg->max_context) : 0);
     ok = ok && kDecodeCtasPerSm * ctx->num_sms <= kPagedTickets &&
-         cudaMalloc(&ctx->paged_ws, (size_t)ctx->paged_ws_bytes) == cudaSuccess &&
          cudaMalloc(&ctx->paged_tickets, kPagedTickets * sizeof(int32_t)) == cudaSuccess &&
          cudaMemset(ctx->paged_tickets, 0, kPagedTickets * sizeof(int32_t)) == cudaSuccess;
     ok = ok && cudaMalloc(&ctx->stage_k, stage) == cudaSuccess && cudaMalloc(&ctx->stage_v, stage) == cudaSuccess;

@@ -60,13 +60,14 @@ struct hd_ctx {
     float2 *part_ml = nullptr;
     int64_t part_slots = 0;              // single-layer calls: capacity in (sequence, chunk) pairs
     int64_t part_rows = 0;               // capacity in partial rows ([256] floats + (m, l) each)
+    // Paged calls take part_o as bytes: partial rows and (m, l) of cut items, or scores of blocks.
+    uint8_t *paged_ws() const { return reinterpret_cast<uint8_t *>(part_o); }
+    int64_t paged_ws_bytes() const { return part_rows * hd::kHeadDim * (int64_t)sizeof(float); }
     uint8_t *stage_k = nullptr;          // [num_layers][max_batch][Hkv][D] entries of the cache type
     uint8_t *stage_v = nullptr;
     int kv_type = hd::KV_BF16;
     int32_t *counters = nullptr;         // [num_layers][max_batch][Hkv] chunk tickets, zero between calls
     int32_t *err = nullptr;
-    uint8_t *paged_ws = nullptr;         // paged calls: partial rows of cut items, or scores of blocks
-    int64_t paged_ws_bytes = 0;
     int32_t *paged_tickets = nullptr;    // [kPagedTickets], zero between calls
     int consumer = hd::CONSUMER_MMA;
     int cluster_max = 0;                 // largest cluster the single-layer kernel runs with (0: none)

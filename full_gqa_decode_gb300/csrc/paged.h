@@ -78,7 +78,7 @@ struct PagedSelectArgs {
     int32_t *selected;
 };
 
-// Workspace of the paged calls: two partial tiles per CTA (decode) or pair of CTAs
+// What the paged calls need of the context's workspace: two partial tiles per CTA (decode) or pair of CTAs
 // (chunks) of the attention grid, or a score per (sequence, kv head, block) of max_batch single-token rows.
 constexpr int64_t paged_partial_rows(int num_sms, bool chunk) {
     return chunk ? (int64_t)2 * (num_sms / 2) * kChunkRows : (int64_t)2 * kDecodeCtasPerSm * num_sms * kDecodeRows;

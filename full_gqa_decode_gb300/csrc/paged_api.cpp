@@ -109,8 +109,8 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     // single tokens; lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
     const bool chunk = !selected && (int64_t)seqs.max_tokens * ctx->group > kDecodeRows;
     const int64_t rows = paged_partial_rows(ctx->num_sms, chunk);
-    a.part_o = reinterpret_cast<float *>(ctx->paged_ws);
-    a.part_ml = reinterpret_cast<float2 *>(ctx->paged_ws + rows * kHeadDim * 4);
+    a.part_o = reinterpret_cast<float *>(ctx->paged_ws());
+    a.part_ml = reinterpret_cast<float2 *>(ctx->paged_ws() + rows * kHeadDim * 4);
     const int Hkv = ctx->cfg.num_kv_heads, all = kv_boxes_per_row(ctx->kv_type), ps = c.page_size;
     const bool fp8 = ctx->kv_type == KV_FP8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -223,12 +223,12 @@ hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, 
     const int64_t last = std::min<int64_t>((int64_t)a.seqs.max_context + batch->max_tokens - 1, ctx->cfg.max_context);
     const int64_t blocks = std::min<int64_t>((last >> a.seqs.page_shift) + 1, batch->max_blocks);
     if (blocks > kMaxSelectBlocks ||
-        (int64_t)batch->num_tokens * ctx->cfg.num_kv_heads * blocks * 8 > ctx->paged_ws_bytes)
+        (int64_t)batch->num_tokens * ctx->cfg.num_kv_heads * blocks * 8 > ctx->paged_ws_bytes())
         return HD_ERR_CAPACITY;
     a.q = static_cast<const __nv_bfloat16 *>(q_rot);
     a.bounds = static_cast<const __nv_bfloat16 *>(cache->bounds);
     a.k_scale = cache->k_scale;
-    a.scores = reinterpret_cast<float2 *>(ctx->paged_ws);
+    a.scores = reinterpret_cast<float2 *>(ctx->paged_ws());
     a.score_stride = (int32_t)blocks;
     a.num_q_heads = ctx->cfg.num_q_heads;
     a.num_kv_heads = ctx->cfg.num_kv_heads;

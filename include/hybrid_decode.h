@@ -435,9 +435,12 @@ hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_head
  * non-finite entry among the positions of a chunk can reach every row of that
  * chunk.
  *
- * These calls share the context's workspace: order all calls on one context,
- * captured graphs among them, on one stream.  They can be captured, and none
- * allocates.  hd_paged_cache and hd_paged_batch are read during the call only.
+ * These calls share the context's workspace with each other and with the
+ * per-sequence calls (split-K partials; init makes it at least 40 MB, or the
+ * scores of max_batch rows, see select_pages, where the per-sequence calls need
+ * less): order all calls on one context, captured graphs among them, on one
+ * stream.  They can be captured, and none allocates.  hd_paged_cache and
+ * hd_paged_batch are read during the call only.
  *
  * Bad values on the device: a sequence with bad token_offsets, more than
  * max_tokens tokens, a context below 0 or above the call's max_context, or a
@@ -537,8 +540,8 @@ hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, co
  * HD_ERR_STATE for a sliding layer; HD_ERR_INVALID_ARG without bounds, with
  * num_selected < 1 or keep_first + keep_last > num_selected; HD_ERR_CAPACITY
  * above 16384 blocks a sequence, or when the scores (8 bytes for each row, kv head
- * and block of max_context) exceed the context's workspace, which holds
- * those of max_batch rows of max_context. */
+ * and block of max_context) exceed the context's workspace, which holds at
+ * least those of max_batch rows of max_context. */
 hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
                        const hd_paged_cache *cache, int32_t num_selected, int32_t keep_first, int32_t keep_last,
                        int32_t *selected, void *stream);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import synth
-from harness import FULL, assert_bits_equal
+from harness import FULL, SLIDING, assert_bits_equal
 from paged_harness import D, PagedCase, assert_rows, reference_append, reference_rows
 from test_gpu_paged import cache_of, context, page_bounds, reference_selection, run_attn, sinks
 
@@ -70,3 +70,18 @@ def test_rows_that_bad_offsets_name_are_nan(hd, orc, max_tokens):
         good = [r for r in range(5 if offs[3] != 9 else 9) if r not in bad]
         assert_rows(reference_rows(orc, case, good), out, lse)
         assert np.array_equal(selected[good].cpu().numpy(), want[good])
+
+
+def test_a_context_takes_no_memory_of_its_own_for_paged_calls(hd):
+    """The paged calls' workspace is the split-K partials': rows of 1032 bytes, 32 per kv head for each of a full batch's
+    2048-key chunks and four more per SM."""
+    kw = dict(layer_types=[FULL], num_q_heads=8, num_kv_heads=2, max_batch=16, max_context=4096)
+    hd.hybrid_decode_init(hd.Config(**kw)).close()
+    before = torch.cuda.mem_get_info()[0]
+    ctx = hd.hybrid_decode_init(hd.Config(**kw))
+    taken = before - torch.cuda.mem_get_info()[0]
+    ctx.close()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    partials = (16 * 3 + 4 * sms) * 2 * 32 * 1032
+    tables = 4097 * 32 * 8
+    assert taken <= partials + tables + (8 << 20), (taken, partials, tables)   # and little else, in pieces of 2 MB
