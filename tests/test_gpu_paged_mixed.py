@@ -85,3 +85,74 @@ def test_a_context_takes_no_memory_of_its_own_for_paged_calls(hd):
     partials = (16 * 3 + 4 * sms) * 2 * 32 * 1032
     tables = 4097 * 32 * 8
     assert taken <= partials + tables + (8 << 20), (taken, partials, tables)   # and little else, in pieces of 2 MB
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("fused", [True, False])
+def test_steps_and_paged_calls_take_turns_on_a_stream(hd, kv, fused):
+    """decode_step (one grid, or layers as programmatic dependents) and paged calls, which overlap their neighbours'
+    launches and share a workspace, one after the other without a wait: bit for bit what each gives alone."""
+    B, types = 3, [SLIDING, FULL, SLIDING, FULL]
+    ctx = hd.hybrid_decode_init(hd.Config(layer_types=types, num_q_heads=8, num_kv_heads=2, max_batch=8, max_context=9000,
+                                          kv_dtype=hd.HD_KV_FP8_E4M3 if kv == "e4m3" else hd.HD_KV_BF16))
+    hd.hybrid_decode_set_step_fusion(ctx, fused)
+    rng = synth.generator(140)
+    contexts = torch.tensor([8000, 5, 4100], dtype=torch.int32, device="cuda")
+    scales = dict(k_scale=synth.kv_scales(rng, 2).cuda(), v_scale=synth.kv_scales(rng, 2).cuda()) if kv == "e4m3" else {}
+    layers = []
+    for t in types:
+        cap = 511 if t == SLIDING else 9001
+        kc, vc = (synth.normal_bf16(rng, (B, 2, cap, D)) for _ in range(2))
+        if kv == "e4m3":
+            kc, vc = synth.e4m3_codes(kc.float()), synth.e4m3_codes(vc.float())
+        layers.append([kc.cuda(), vc.cuda()] + [synth.normal_bf16(rng, (B, h, D)).cuda() for h in (8, 2, 2)])
+    chunk = PagedCase(141, [(8000, 70), (0, 40)], kv=kv, appended=False)
+    single = PagedCase(142, [(8000, 1), (900, 1), (4000, 1)], kv=kv, single=True, appended=False)
+    news = {c: [synth.normal_bf16(c.rng, (c.rows, 2, D)).cuda() for _ in range(2)] for c in (chunk, single)}
+    bounds = {c: torch.nan_to_num(page_bounds(c)).cuda() for c in (chunk, single)}
+
+    def step(results):
+        io, keep = [], []
+        for kc, vc, q, k, v in layers:
+            kc, vc = kc.clone(), vc.clone()
+            out, lse = torch.empty(B, 8, D, dtype=torch.bfloat16, device="cuda"), torch.empty(B, 8, device="cuda")
+            io.append(hd.layer_io(q, k, v, hd.kv_cache(kc, vc, **scales), None, out, lse))
+            keep += [out, lse, kc, vc]
+        results.append(keep)
+        return lambda: hd.decode_step(ctx, contexts, io, batch=B)
+
+    def paged(results, case):
+        d = case.device()
+        k, v = news[case]
+        cache, batch = cache_of(hd, d, bounds[case].clone()), case.batch_of(hd, d)
+        q_rot, out = torch.empty_like(d["q"]), torch.empty_like(d["q"])
+        picked = torch.empty_like(out)
+        lse, lse2 = (torch.empty(case.rows, 8, device="cuda") for _ in range(2))
+        selected = torch.empty(case.rows, 2, 6, dtype=torch.int32, device="cuda")
+        results.append([q_rot, out, lse, picked, lse2, selected, d["k"], d["v"]])
+
+        def call():
+            hd.rope_append_paged(ctx, 1, batch, d["q"], k, v, q_rot, cache)
+            hd.attn_paged(ctx, 1, batch, q_rot, cache, None, out, lse)
+            hd.select_pages(ctx, 1, batch, q_rot, cache, selected)
+            hd.attn_selected_pages(ctx, 1, batch, q_rot, cache, selected, None, picked, lse2)
+        return call
+
+    def all_of(results):
+        return [f for _ in range(3) for f in (step(results), paged(results, chunk), step(results), step(results),
+                                              paged(results, single), paged(results, chunk))]
+
+    alone, together = [], []
+    for f in all_of(alone):
+        f()
+        torch.cuda.synchronize()
+    calls = all_of(together)
+    torch.cuda.synchronize()
+    for f in calls:
+        f()
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    for a, b in zip(alone, together):
+        for x, y in zip(a, b):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    ctx.close()
