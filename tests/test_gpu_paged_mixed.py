@@ -156,3 +156,30 @@ def test_steps_and_paged_calls_take_turns_on_a_stream(hd, kv, fused):
         for x, y in zip(a, b):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     ctx.close()
+
+
+@pytest.mark.parametrize("group,spans", [(4, [(700, 1), (4000, 1), (0, 1), (511, 1)]), (4, [(700, 2), (3999, 1), (0, 2), (511, 2)]),
+                                         (8, [(700, 1), (4000, 1), (0, 1), (63, 1)]), (1, [(700, 7), (0, 8), (4000, 3), (510, 8)])])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 512])
+def test_results_hold_on_both_sides_of_the_choice_of_kernel(hd, orc, group, spans, kv, window):
+    """max_tokens x group up to 8 is served by the kernel of few rows, more by the one of chunks."""
+    case = PagedCase(150 + group, spans, group=group, kv=kv, window=window)
+    ctx, d, sink = context(hd, group, kv=kv), case.device(), sinks(case)
+    want = reference_rows(orc, case, sink=sink)
+    for max_tokens in (8 // group, 8 // group + 1, 300):
+        out, lse = run_attn(hd, ctx, case, d, sink=sink, max_tokens=max_tokens)
+        assert hd.hybrid_decode_device_errors(ctx) == 0
+        assert_rows(want, out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_choice_of_blocks_does_not_depend_on_the_bounds(hd, kv):
+    case = PagedCase(155, [(3000, 2), (17, 1), (1600, 3)], page=16, kv=kv)
+    ctx, d, bounds = context(hd, kv=kv), case.device(), page_bounds(case)
+    want = reference_selection(case, bounds, 9, 1, 2)
+    for kw in ({}, {"max_context": 3000}, {"max_tokens": 500}, {"max_context": 20000, "max_tokens": 64}):
+        selected = torch.full((case.rows, 2, 9), 99, dtype=torch.int32, device="cuda")
+        hd.select_pages(ctx, 1, case.batch_of(hd, d, **kw), d["q"], cache_of(hd, d, bounds.cuda()), selected, 1, 2)
+        assert np.array_equal(selected.cpu().numpy(), want), kw
+    assert hd.hybrid_decode_device_errors(ctx) == 0
