@@ -173,6 +173,12 @@ hd_status rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *ba
     if (k_stride % 8 || v_stride % 8 || k_stride < Hkv * kHeadDim || v_stride < Hkv * kHeadDim ||
         (q && (q_stride % 8 || q_stride < Hq * kHeadDim)))
         return HD_ERR_INVALID_ARG;
+    // q_rot in place of q, row by row, or apart from it: elsewhere its rows would lie over rows not yet rotated.
+    const auto *src = static_cast<const uint8_t *>(q), *dst = static_cast<const uint8_t *>(q_rot);
+    const int64_t row = Hq * kHeadDim * 2, rows = batch->num_tokens;
+    if (q && src < dst + rows * row && dst < src + (rows - 1) * q_stride * 2 + row &&
+        !(src == dst && (rows == 1 || q_stride == Hq * kHeadDim)))
+        return HD_ERR_INVALID_ARG;
     const bool sliding = ctx->layer_types[layer] == HD_SLIDING;
     const DeviceTable &tab = sliding ? ctx->table_sliding : ctx->table_full;
     if (tab.rotary_dim % 8) return HD_ERR_UNSUPPORTED;

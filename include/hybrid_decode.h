@@ -507,7 +507,8 @@ hd_status hd_validate_paged(const hd_config *cfg, const hd_paged_batch *batch, c
  * slot 0 is written starts anew) unless cache->bounds is NULL.
  *   q       bf16 [num_tokens][num_q_heads][head_dim], rows q_stride elements apart
  *   k, v    bf16 [num_tokens][num_kv_heads][head_dim], rows k_stride / v_stride apart
- *   q_rot   bf16 [num_tokens][num_q_heads][head_dim], contiguous; may be q itself
+ *   q_rot   bf16 [num_tokens][num_q_heads][head_dim], contiguous; q itself, when
+ *           its rows are contiguous too, or apart from it
  * (parts of one projection's rows are taken in place).  q and q_rot may both be
  * NULL.  Strides are multiples of 8 elements, pointers 16-byte aligned.  Pages
  * must not be shared by sequences that write them in one call.

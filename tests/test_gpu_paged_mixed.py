@@ -183,3 +183,20 @@ def test_choice_of_blocks_does_not_depend_on_the_bounds(hd, kv):
         hd.select_pages(ctx, 1, case.batch_of(hd, d, **kw), d["q"], cache_of(hd, d, bounds.cuda()), selected, 1, 2)
         assert np.array_equal(selected.cpu().numpy(), want), kw
     assert hd.hybrid_decode_device_errors(ctx) == 0
+
+
+def test_queries_are_not_rotated_over_rows_of_others(hd):
+    """q_rot at q's own address while q's rows are wider: the rows of the one lie over other rows of the other."""
+    case = PagedCase(156, [(5, 3)])
+    ctx, d = context(hd), case.device()
+    wide = torch.zeros(3, 10, D, dtype=torch.bfloat16, device="cuda")
+    q, kv = wide[:, :8], torch.zeros(3, 2, D, dtype=torch.bfloat16, device="cuda")
+    q_rot = wide.view(-1)[: 3 * 8 * D].view(3, 8, D)
+    batch, cache = case.batch_of(hd, d), cache_of(hd, d)
+    for where in (q_rot, wide.view(-1)[D: D + 3 * 8 * D].view(3, 8, D)):
+        with pytest.raises(hd.HDError) as e:
+            hd.rope_append_paged(ctx, 1, batch, q, kv, kv, where, cache)
+        assert e.value.status == 1
+    one = case.batch_of(hd, dict(d, offsets=torch.tensor([0, 1], dtype=torch.int32, device="cuda")), num_tokens=1)
+    hd.rope_append_paged(ctx, 1, one, q[:1], kv[:1], kv[:1], q_rot[:1], cache)   # one row: in place
+    assert hd.hybrid_decode_device_errors(ctx) == 0
