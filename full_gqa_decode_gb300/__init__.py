@@ -167,9 +167,20 @@ def _check_gate(gate, batch: int, num_q_heads: int, like: torch.Tensor, tokens: 
         raise ValueError("gate must be contiguous")
 
 
+def _stream_lookup(torch_c):
+    """What gives the raw handle of a device's current stream: torch's own look-up where it has
+    one, as torch.cuda.current_stream() makes an object around it, 3 us on a Grace host, as much
+    as a launch; else that."""
+    return getattr(torch_c, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_raw_stream = _stream_lookup(torch._C)
+
+
 def _stream(stream) -> int | None:
-    if stream is None:   # the raw handle: torch.cuda.current_stream() costs 3 us on a Grace host, as much as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
