@@ -69,9 +69,11 @@ constexpr int kMaxPairs = 96;
 // tile's 1.5).  Shares are cut by tiles plus this; short items (the first rows of a causal prompt) would otherwise
 // pile up in a few shares.
 constexpr int kItemCost = 2;
-// Items of up to this many units are not cut: the merge of an item takes the time of seven tiles (5 prompts of up to 4099
-// tokens in 512-key windows: 119 us cut evenly, 104 us whole).
-constexpr int kSnap = 16;
+// Items of up to this many units are not cut: the pieces and their merge cost more than the imbalance.  Measured cut at up
+// to 12 against 16: a prompt of 1500 tokens 36.5 and 30.4 us; with 0, 5 prompts of up to 4099 in 512-key windows 119 and
+// 108 us.  The rows of few tokens are merged sooner: 8 sequences of 5 tokens behind 1700 24.6 and 33 us, 40 of them 50
+// and 63 us; at 64 rows of 8 sequences 27 and 33 us, at 128 rows about even.
+constexpr int kSnap = 16, kSnapFew = 12, kFewRows = 64;
 constexpr int kMinTiles = 2 + kItemCost;              // shortest share of a pair
 constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512, kOutCol = 256;
@@ -114,6 +116,11 @@ __device__ __forceinline__ ChunkTile make_chunk_tile(const PagedAttnArgs &a, con
 }
 __device__ __forceinline__ int num_chunk_tiles(const PagedAttnArgs &a, int n) {
     return ((n << a.group_shift) + kTileRows - 1) / kTileRows;
+}
+
+// Units of the longest item that is not cut, by the bound on a sequence's rows of a kv head.
+__device__ __forceinline__ int longest_whole(const PagedAttnArgs &a) {
+    return a.seqs.max_tokens <= kFewRows >> a.group_shift ? kSnapFew : kSnap;
 }
 
 // A walk over the segments of a pair's share.
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     long long x0, x1, T;
     int n, bad;
     const Start c0 = find_share(
-        sq, a.num_kv_heads, pair, pairs, kMinTiles, 0, kSnap, INT_MAX, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
+        sq, a.num_kv_heads, pair, pairs, kMinTiles, 0, longest_whole(a), INT_MAX, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_chunk_tiles(a, tokens); },
         [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units + kItemCost; });
     if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);

@@ -62,6 +62,7 @@ inline std::vector<Warp> warps;
 inline ucontext_t home;
 inline int at = 0, block = 0, arrived = 0;
 inline long epoch = 0;                 // block barriers passed
+inline int any[2];                     // __syncthreads_or, by the epoch's parity
 inline std::string races;
 inline std::function<void()> body;
 
@@ -77,7 +78,7 @@ inline void block_barrier() {
     const long seen = epoch;
     if (++arrived == (int)lanes.size()) {
         arrived = 0;
-        ++epoch;
+        any[++epoch & 1] = 0;
     } else {
         wait(&epoch, seen);
     }
@@ -106,7 +107,7 @@ inline bool run(int threads, int index, const std::vector<int> &warp_order, std:
     warps.assign(threads / 32, Warp());
     block = index;
     arrived = 0;
-    ++epoch;
+    any[++epoch & 1] = 0;
     body = f;
     for (int i = 0; i < threads; ++i) {
         Fiber &x = lanes[i];
@@ -203,7 +204,11 @@ inline unsigned __ballot_sync(unsigned, int p) {
 }
 inline int __any_sync(unsigned m, int p) { return __ballot_sync(m, p) != 0; }
 inline void __syncthreads() { emu::block_barrier(); }
-int __syncthreads_or(int p);   // of kernels that these tests do not run
+inline int __syncthreads_or(int p) {
+    emu::any[emu::epoch & 1] |= p != 0;
+    emu::block_barrier();
+    return emu::any[~emu::epoch & 1];
+}
 
 inline int __clz(unsigned x) { return x ? __builtin_clz(x) : 32; }
 inline int __ffs(unsigned x) { return __builtin_ffs((int)x); }
