@@ -23,10 +23,14 @@
 // codes convert exactly to f16, and a row's q is scaled by the power of two that
 // brings its largest value below 2, so that f16 holds it: values below 2^-14 of
 // that lose bits under 2^-25 of the largest, less than the fp32 sum of the
-// products does.  P is rounded to the cache's 16-bit type for the second product
-// (2^-9 or 2^-12 of each weight, below the output's own rounding once summed);
-// f16 weights are taken 2^15 times as large, which the division by their sum
-// undoes, so that small ones stay clear of f16's subnormals.  Sums and maxima
+// products does.  With bf16 pages P enters the second product in two bf16 parts,
+// the rounded weight and what the rounding left (2^-16 of the weight remain): in
+// one part alone its rounding adds as much to the error as the output's own
+// (2.2e-3 against 1.7e-3 of the output, root mean square), and the second
+// product of a fragment is nearly free (one sequence at 4096 12.7 and 12.9 us, 64
+// sequences 337 and 336 us).  With E4M3 pages one f16 part is enough (2^-11 of a
+// weight); f16 weights are taken 2^15 times as large, which the division by their
+// sum undoes, so that small ones stay clear of f16's subnormals.  Sums and maxima
 // stay in fp32.
 #include "paged_rows.cuh"
 
@@ -163,9 +167,9 @@ struct DecodeRowsState {
             for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
     }
     // Scores (times scale[e], log2 units) to weights; returns the two P^T operands: keys 2 t4 (+ 1) and 8 + 2 t4
-    // (+ 1) of row gid.
+    // (+ 1) of row gid; bf16: and those of the weights' low parts.
     __device__ __forceinline__ void weigh(const PagedAttnArgs &a, const float (&s)[4], const float (&scale)[2], int key0,
-                                          int first, bool full, int lane, uint32_t &pb0, uint32_t &pb1) {
+                                          int first, bool full, int lane, uint32_t (&pb)[F16 ? 2 : 4]) {
         float p[4], alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -198,8 +202,14 @@ struct DecodeRowsState {
                 o[mt][3] *= alpha[1];
             }
         }
-        pb0 = movmatrix_trans(F16 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
-        pb1 = movmatrix_trans(F16 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w = F16 ? pack_f16(p[2 * i], p[2 * i + 1]) : pack_bf16(p[2 * i], p[2 * i + 1]);
+            pb[i] = movmatrix_trans(w);
+            if constexpr (!F16)
+                pb[2 + i] = movmatrix_trans(pack_bf16(p[2 * i] - __uint_as_float(w << 16),
+                                                      p[2 * i + 1] - __uint_as_float(w & 0xFFFF0000u)));
+        }
     }
     // Masks of the V values of keys 2 t4 (+ 1) and 8 + 2 t4 (+ 1): slots outside [vlo, vhi) may hold anything, and
     // 0 * NaN would reach every row.
@@ -257,17 +267,17 @@ struct DecodeBf16 : DecodeRowsState<false> {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
-        uint32_t pb0, pb1, m01, m89;
-        weigh(a, s, scale, key0, first, full, lane, pb0, pb1);
+        uint32_t pb[4], m01, m89;
+        weigh(a, s, scale, key0, first, full, lane, pb);
         if (full) {   // the masks fold away
-            products(vst, base, col, lane, pb0, pb1, 0xFFFFFFFFu, 0xFFFFFFFFu);
+            products(vst, base, col, lane, pb, 0xFFFFFFFFu, 0xFFFFFFFFu);
         } else {
             value_masks(key0, vlo, vhi, lane, m01, m89);
-            products(vst, base, col, lane, pb0, pb1, m01, m89);
+            products(vst, base, col, lane, pb, m01, m89);
         }
     }
-    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane, uint32_t pb0,
-                                             uint32_t pb1, uint32_t m01, uint32_t m89) {
+    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane,
+                                             const uint32_t (&pb)[4], uint32_t m01, uint32_t m89) {
         const int lr = lane & 7;
         // V^T: matrices (dims 0-7, 8-15 of tile mt) x (keys 0-7, 8-15), transposed on the way.
         const uint32_t vb = smem_u32(vst) + base + (lr + ((lane & 16) >> 1)) * 128;
@@ -280,7 +290,8 @@ struct DecodeBf16 : DecodeRowsState<false> {
             x[1] &= m01;
             x[2] &= m89;
             x[3] &= m89;
-            mma_16816(o[mt], x, pb0, pb1);
+            mma_16816(o[mt], x, pb[0], pb[1]);
+            mma_16816(o[mt], x, pb[2], pb[3]);
         }
     }
     template <class F> __device__ void each(int lane, F f) {   // f(row, dim, value&)
@@ -355,17 +366,17 @@ struct DecodeE4m3 : DecodeRowsState<true> {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
-        uint32_t pb0, pb1, m01, m89;
-        weigh(a, s, scale, key0, first, full, lane, pb0, pb1);
+        uint32_t pb[2], m01, m89;
+        weigh(a, s, scale, key0, first, full, lane, pb);
         if (full) {   // the masks fold away
-            products(vst, base, col, lane, pb0, pb1, 0xFFFFFFFFu, 0xFFFFFFFFu);
+            products(vst, base, col, lane, pb, 0xFFFFFFFFu, 0xFFFFFFFFu);
         } else {
             value_masks(key0, vlo, vhi, lane, m01, m89);
-            products(vst, base, col, lane, pb0, pb1, m01, m89);
+            products(vst, base, col, lane, pb, m01, m89);
         }
     }
-    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane, uint32_t pb0,
-                                             uint32_t pb1, uint32_t m01, uint32_t m89) {
+    __device__ __forceinline__ void products(const uint8_t *vst, uint32_t base, uint32_t col, int lane,
+                                             const uint32_t (&pb)[2], uint32_t m01, uint32_t m89) {
         const int gid = lane >> 2, t4 = lane & 3;
         auto at = [&](int r, int c) { return base + (uint32_t)(c >> 3) * col + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
 #pragma unroll
@@ -385,7 +396,7 @@ struct DecodeE4m3 : DecodeRowsState<true> {
                     const uint32_t x01 = __byte_perm(w0[w], w1[w], sel), x89 = __byte_perm(w8[w], w9[w], sel);
                     const uint32_t x[4] = {e4m3x2_to_f16x2((uint16_t)(x01 & 0xFFFFu)) & m01, e4m3x2_to_f16x2((uint16_t)(x01 >> 16)) & m01,
                                            e4m3x2_to_f16x2((uint16_t)(x89 & 0xFFFFu)) & m89, e4m3x2_to_f16x2((uint16_t)(x89 >> 16)) & m89};
-                    mma_16816_f16(o[8 * half + 2 * w + q], x, pb0, pb1);
+                    mma_16816_f16(o[8 * half + 2 * w + q], x, pb[0], pb[1]);
                 }
         }
     }

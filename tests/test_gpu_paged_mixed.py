@@ -200,3 +200,28 @@ def test_queries_are_not_rotated_over_rows_of_others(hd):
     one = case.batch_of(hd, dict(d, offsets=torch.tensor([0, 1], dtype=torch.int32, device="cuda")), num_tokens=1)
     hd.rope_append_paged(ctx, 1, one, q[:1], kv[:1], kv[:1], q_rot[:1], cache)   # one row: in place
     assert hd.hybrid_decode_device_errors(ctx) == 0
+
+
+@pytest.mark.parametrize("window", [0, 512])
+@pytest.mark.parametrize("group", [1, 4, 8])
+def test_weights_of_few_rows_keep_their_bits(hd, window, group):
+    """Few rows over bf16 pages: beside the output's rounding (2^-8 of it) and the scores' error, only 2^-16 of each weight
+    is lost, two roundings of 2^-8 one after the other."""
+    case = PagedCase(160 + group, [(700, 1), (63, 1), (4095, 1), (0, 1), (9000, 1)], group=group, window=window, single=True)
+    out, _ = run_attn(hd, context(hd, group), case)
+    out = out.cpu().double().numpy()
+    for r in range(case.rows):
+        b, p = case.token(r)
+        lo = max(0, p - window + 1) if window else 0
+        for h in range(2):
+            k, v = (t[torch.from_numpy(case.table[b, lo // 64: p // 64 + 1].astype(np.int64)), h].reshape(-1, D).double().numpy()
+                    [lo % 64: lo % 64 + p - lo + 1] for t in (case.k, case.v))
+            q = case.q[r, h * group: (h + 1) * group].double().numpy()
+            s = q @ k.T / 16
+            w = np.exp(s - s.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            want, size = w @ v, w @ np.abs(v)
+            score = 256 * 2.0 ** -24 * (np.abs(q) @ np.abs(k).T / 16).max(1, keepdims=True) + 2.0 ** -20
+            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * score) * size + 1e-30
+            excess = np.abs(out[r, h * group: (h + 1) * group] - want) - bound
+            assert (excess <= 0).all(), (r, h, excess.max())
