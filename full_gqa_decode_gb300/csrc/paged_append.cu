@@ -170,6 +170,7 @@ __device__ __forceinline__ void rotate_bf16(uint2 &x, uint2 &y, const float (&c)
 
 // Grid: [0, runs) x kv heads: runs of keys and values; the CTAs behind them:
 // query rows, a warp each.
+// Five CTAs an SM leave 48 registers a thread, of which 60 bytes are spilled.
 __global__ void __launch_bounds__(kThreads, 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int runs) {
     const PagedSeqs &sq = a.seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -10,10 +10,11 @@
 // two SMs share a tile (a cluster of two CTAs, cta_group::2 MMAs): each holds
 // 128 of the query rows, the scores of its rows, and half of every operand tile
 // -- 64 of the 128 keys for S, 128 of the 256 dims for O -- and the pair reads
-// K and V once.  Measured: 4096 tokens behind 28672 at 8 heads 658 us (1.57
-// PFLOP/s, 1.5 us a tile); a prompt of 8192 at 16 heads over E4M3 pages 581 us
-// (2 us a tile, bound by shared memory: the MMAs' operands, the f16 stores and
-// the code loads all go through it).
+// K and V once.  Measured: 4096 tokens behind 28672 at 8 heads 687 us (1.50
+// PFLOP/s, 1.5 us a tile); a prompt of 8192 at 16 heads over E4M3 pages 575 us
+// (2 us a tile: the MMAs' operands, the f16 stores and the code loads all go
+// through shared memory, and at 96 registers a thread the kernel keeps about
+// 1.2 KB of them in local memory, which the bf16 one does not).
 //
 // Tensor memory (512 columns in each CTA): scores in two buffers of 128
 // columns, the output of 256.  P, in 16 bits, takes the place of the scores
@@ -32,9 +33,12 @@
 // Rows keep the reference m of their weights until a score passes it by 8 (in
 // log2 units), and only then is the output in tensor memory rescaled: weights
 // stay below 2^8, exact in range for bf16, and f16 weights (E4M3 pages) are
-// lifted by another 2^7 away from f16's subnormals.  Sums and maxima are fp32;
-// the rounding of P to 16 bits (2^-9, f16 2^-12 of each weight) is below the
-// output's own once summed.
+// lifted by another 2^7 away from f16's subnormals.  Sums and maxima are fp32.
+// P is rounded once, to the operands' type.  In f16 (2^-11 of each weight) that
+// hardly shows beside the output's rounding; in bf16 (2^-8) it adds as much as
+// that does (2.4e-3 against 1.7e-3 of the output, root mean square).  The low parts
+// of P through a second product, as the decode kernel takes them, would cost a
+// product in two again: 4096 tokens behind 28672 905 us against 657 in the same run.
 #include <climits>
 
 #include "paged_rows.cuh"

@@ -12,8 +12,8 @@
 // with E4M3) form a team and the teams take stages in turn, so a warp's chain of
 // dependent MMAs and shuffles overlaps the other teams' and not only its own
 // stage's copies.  The work is cut evenly over the CTAs (paged_sched.cuh).
-// Measured: 64 sequences of 512 to 32768 keys 331 us (7.05 TB/s of keys and values);
-// 256 of 512 to 8192 at group 8 over E4M3 pages 200 us (5.8 TB/s, bound by the warps'
+// Measured: 64 sequences of 512 to 32768 keys 336 us (6.9 TB/s of keys and values);
+// 256 of 512 to 8192 at group 8 over E4M3 pages 201 us (5.8 TB/s, bound by the warps'
 // conversions, MMAs and shuffles); one sequence at 4096 12 us, all latency.
 //
 // Per 16 keys, on mma.sync m16n8k16 with an online softmax in log2 units:

@@ -5,8 +5,9 @@
 //     sum_g sum_d max(q_gd lo_d, q_gd hi_d) = Q+ . hi + Q- . lo,
 // Q+ = sum_g max(q_g, 0), Q- = sum_g min(q_g, 0) -- one 512-term dot product
 // per block instead of one per head.  The score kernel reads each block's
-// bounds once (1 KiB); at long contexts that read bounds it (64 rows of up to
-// 1025 blocks at 2 kv heads: 18 us; the pick 8 us, mostly latency).
+// bounds once (1 KiB); at long contexts that read bounds it, at half of
+// DRAM's rate, as a warp has four blocks' bounds under way (64 rows of up to 1025
+// blocks at 2 kv heads: 19 us; the pick 10 us, mostly latency).
 //
 // Which block is chosen must not hang on the order of a sum.  Scores are taken
 // in binary32 first.  A score is sixteen terms a lane and five levels of a

@@ -330,7 +330,8 @@ hd_status hybrid_decode_set_consumer(hd_ctx *ctx, int32_t consumer);
 
 /* Test hook for failure detection (no counterpart in the pages).  With
  * stage >= 0, the copy producer of every attention CTA stops issuing copies at
- * that pipeline stage, as if the copy were lost; the consumers' waits, bounded
+ * that pipeline stage (chunks over E4M3 pages: the warps that convert an operand
+ * stop handing it on), as if the copy were lost; the consumers' waits, bounded
  * to one second, run out, the kernel records HD_DEVERR_WAIT_TIMEOUT and
  * returns (outputs of affected sequences are then meaningless), and the
  * context stays usable.  -1 (the default) turns it off. */
@@ -428,7 +429,11 @@ hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_head
  * chunk of a prompt, ragged.  rope_append_paged first puts their keys and
  * values into the pages; attn_paged (or select_pages and attn_selected_pages)
  * then attends.  Each query is rotated and rounded to bf16 once, by
- * rope_append_paged (the per-sequence calls keep fp32 queries).
+ * rope_append_paged (the per-sequence calls keep fp32 queries).  Softmax weights
+ * are rounded before they meet the values: over bf16 pages to 2^-16 of themselves
+ * in calls with up to eight rows a sequence (max_tokens x query heads per kv head)
+ * and over selected blocks, to 2^-8 in calls with more; over E4M3 pages to 2^-11.
+ * Sums and maxima are fp32.
  *
  * Entries at visible positions must be finite; slots no query may see (behind
  * a sequence's end, before its window) can hold anything, NaN included.  A
@@ -504,7 +509,9 @@ hd_status hd_validate_paged(const hd_config *cfg, const hd_paged_batch *batch, c
  * their pages: keys rotated exactly and rounded once (to bf16, or to E4M3 of
  * the quotient by the scale), values bit for bit (or as E4M3), like
  * rope_append_kv; and brings the touched pages' bounds up to date (a page whose
- * slot 0 is written starts anew) unless cache->bounds is NULL.
+ * slot 0 is written starts anew) unless cache->bounds is NULL.  Bounds only widen:
+ * where a position is written again, after drafted tokens that were not taken, they
+ * still cover its earlier key.
  *   q       bf16 [num_tokens][num_q_heads][head_dim], rows q_stride elements apart
  *   k, v    bf16 [num_tokens][num_kv_heads][head_dim], rows k_stride / v_stride apart
  *   q_rot   bf16 [num_tokens][num_q_heads][head_dim], contiguous; q itself, when
@@ -532,7 +539,9 @@ hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, co
  * token's own, then those of the largest score
  *     sum over the kv head's query heads and dims of max(q_d lo_d, q_d hi_d)
  * with lo / hi the block's bounds -- the sum of the largest scores that any of
- * its keys could reach.  Ties go to the lower block; scores that fp32
+ * its keys could reach.  The bounds of a token's own block hold the later tokens of
+ * the same call too: with keep_last 0 its place can depend on how a prompt is cut
+ * into calls (with keep_last 1 it is always chosen).  Ties go to the lower block; scores that fp32
  * cannot tell apart are summed to twice its precision, so the choice does not
  * depend on the order of summation.
  *   selected  int32 [num_tokens][num_kv_heads][num_selected]: block numbers,
