@@ -478,7 +478,7 @@ def paged_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None =
     bf16, or E4M3 codes (uint8 or float8_e4m3fn) with fp32 ``k_scale``/``v_scale`` of shape
     [num_kv_heads].  Pages may lie apart (stride 0) but each is contiguous.  ``bounds``: bf16
     [num_pages, num_kv_heads, 2, head_dim] for select_pages.  Keep it while the tensors stay."""
-    if k.shape != v.shape or k.dim() != 4 or k.stride() != v.stride():
+    if k.shape != v.shape or k.dim() != 4 or any(a != b for n, a, b in zip(k.shape, k.stride(), v.stride()) if n > 1):
         raise ValueError("k and v pages must share a [num_pages, kv_heads, page_size, head_dim] layout")
     if not k.is_cuda or v.device != k.device:
         raise ValueError("pages must be CUDA tensors on one device")
@@ -486,7 +486,8 @@ def paged_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None =
     fp8 = k.dtype in _FP8_CACHE_TYPES
     if v.dtype != k.dtype or not (fp8 or k.dtype == torch.bfloat16):
         raise ValueError("pages must be bf16, or E4M3 codes with scales, K and V alike")
-    if D != 256 or k.stride()[1:] != (S * D, D, 1) or (P > 1 and k.stride(0) < H * S * D):
+    if (D != 256 or (H > 1 and k.stride(1) != S * D) or (S > 1 and k.stride(2) != D) or k.stride(3) != 1 or
+            (P > 1 and k.stride(0) < H * S * D)):
         raise ValueError("each page must be contiguous [kv_heads, page_size, 256] and pages may not overlap")
     for name, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
         if not fp8:
@@ -516,7 +517,7 @@ def paged_batch(block_table: torch.Tensor, context: torch.Tensor, token_offsets:
         raise ValueError("block_table must be [batch, max_blocks] and context [batch]")
     for name, t in (("block_table", block_table), ("context", context), ("token_offsets", token_offsets)):
         if t is not None and (t.dtype != torch.int32 or t.device != context.device or not t.is_cuda or
-                              (t.numel() > 0 and t.stride(-1) != 1)):
+                              (t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1)):
             raise ValueError(f"{name} must be an int32 CUDA tensor with unit stride, on one device with the others")
     if token_offsets is not None and (token_offsets.dim() != 1 or token_offsets.shape[0] != batch + 1):
         raise ValueError(f"token_offsets must have shape ({batch + 1},)")

@@ -225,3 +225,19 @@ def test_weights_of_few_rows_keep_their_bits(hd, window, group):
             bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * score) * size + 1e-30
             excess = np.abs(out[r, h * group: (h + 1) * group] - want) - bound
             assert (excess <= 0).all(), (r, h, excess.max())
+
+
+def test_strides_of_dimensions_of_one_do_not_matter(hd, orc):
+    """One kv head in pages of [slots][heads][dims], one sequence out of a table of many."""
+    case = PagedCase(170, [(130, 1)], kv_heads=1, single=True)
+    ctx, d = context(hd, kv_heads=1), case.device()
+    for name in ("k", "v"):
+        d[name] = d[name].as_strided(d[name].shape, (64 * D, D, D, 1))
+    d["context"] = torch.tensor([130, 7, 7], dtype=torch.int32, device="cuda")[::3]
+    assert d["context"].stride(0) == 3
+    out, lse = run_attn(hd, ctx, case, d)
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    assert_rows(reference_rows(orc, case), out, lse)
+    with pytest.raises(ValueError):   # two heads that way are no pages
+        two = torch.zeros(4, 64, 2, D, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+        hd.paged_cache(two, two)
