@@ -9,7 +9,9 @@ Names follow the C entry points: ``hybrid_decode_init``, ``rope_append_kv``,
 ``decode_attn_sliding``, ``decode_attn_full``, ``decode_step`` (plus
 ``hybrid_decode_destroy`` and the helpers); over paged caches ``paged_cache``,
 ``paged_batch``, ``rope_append_paged``, ``attn_paged``, ``select_pages`` and
-``attn_selected_pages``.  Each call raises ``HDError``
+``attn_selected_pages``; for normed heads, other angles and other scores
+``rope_table``, ``norm_rope_append_paged``, ``scoring``, ``attn_paged_scored``
+and ``read_paged``.  Each call raises ``HDError``
 carrying the hd_status when the library rejects it.
 """
 from __future__ import annotations
@@ -34,7 +36,9 @@ STATUS = {0: "HD_OK", 1: "HD_ERR_INVALID_ARG", 2: "HD_ERR_UNSUPPORTED", 3: "HD_E
           4: "HD_ERR_CUDA", 5: "HD_ERR_STATE"}
 DEVERR = {1: "HD_DEVERR_CONTEXT_NEGATIVE", 2: "HD_DEVERR_CONTEXT_CAPACITY",
           4: "HD_DEVERR_CONTEXT_PLAN", 8: "HD_DEVERR_WAIT_TIMEOUT", 16: "HD_DEVERR_TOKEN_OFFSETS",
-          32: "HD_DEVERR_PAGE"}
+          32: "HD_DEVERR_PAGE", 64: "HD_DEVERR_SPAN"}
+HD_ROPE_HALVES, HD_ROPE_NEIGHBOURS = 0, 1
+HD_ROPE_PLAIN, HD_ROPE_LINEAR, HD_ROPE_RAMP, HD_ROPE_BANDS = 0, 1, 2, 3
 
 if not os.path.exists(LIBRARY):
     raise ImportError(f"{LIBRARY} is missing: build it with full_gqa_decode_gb300.build.build() "
@@ -81,6 +85,27 @@ class hd_paged_batch(ctypes.Structure):
                 ("num_tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("max_context", ctypes.c_int32)]
 
 
+class hd_rope_params(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_context", ctypes.c_double), ("slow", ctypes.c_double),
+                ("fast", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class hd_rope_table(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32)]
+
+
+class hd_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("f32_weights", ctypes.c_int32),
+                ("per_head", ctypes.c_int32), ("offset", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class hd_scoring(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("last", ctypes.c_void_p)]
+
+
 _c = ctypes
 _P = _c.c_void_p
 _i32, _i64 = _c.c_int32, _c.c_int64
@@ -116,6 +141,13 @@ _SIGS = {
     "select_pages": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _c.POINTER(hd_paged_cache), _i32, _i32, _i32, _P, _P],
     "attn_selected_pages": [_P, _i32, _c.POINTER(hd_paged_batch), _P, _c.POINTER(hd_paged_cache), _P, _i32, _P, _P, _P,
                             _P, _P],
+    "hd_rope_frequencies": [_c.POINTER(hd_rope_params), _c.POINTER(_c.c_double), _c.POINTER(_c.c_double)],
+    "hd_rope_fill": [_c.POINTER(hd_rope_params), _i32, _P, _P],
+    "norm_rope_append_paged": [_P, _i32, _c.POINTER(hd_paged_batch), _c.POINTER(hd_head_norm), _c.POINTER(hd_rope_table), _P,
+                               _P, _i64, _P, _i64, _P, _i64, _P, _c.POINTER(hd_paged_cache), _P],
+    "attn_paged_scored": [_P, _i32, _c.POINTER(hd_paged_batch), _c.POINTER(hd_scoring), _P, _c.POINTER(hd_paged_cache), _P,
+                          _P, _P, _P, _P],
+    "read_paged": [_P, _c.POINTER(hd_paged_batch), _c.POINTER(hd_paged_cache), _P, _i64, _P, _i64, _P],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -548,11 +580,7 @@ def _row_stride(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
-def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
-                      stream=None) -> None:
-    """Rotate the new q [num_tokens, Hq, 256] into q_rot (bf16; may be q) and the new k, and store
-    k / v [num_tokens, Hkv, 256] in their pages, with the pages' bounds when the cache has them.
-    q, k and v may be parts of wider rows; q and q_rot may both be None."""
+def _check_append(ctx: Context, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache) -> int:
     _check_paged(ctx, batch, cache)
     n, D, dev = batch.num_tokens, 256, cache.device
     kv = (n, ctx.cfg.num_kv_heads, D)
@@ -565,6 +593,15 @@ def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_ro
         _check_rows("q", q, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev, True)
         _check_rows("q_rot", q_rot, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev)
         qs = _row_stride(q)
+    return qs
+
+
+def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
+                      stream=None) -> None:
+    """Rotate the new q [num_tokens, Hq, 256] into q_rot (bf16; may be q) and the new k, and store
+    k / v [num_tokens, Hkv, 256] in their pages, with the pages' bounds when the cache has them.
+    q, k and v may be parts of wider rows; q and q_rot may both be None."""
+    qs = _check_append(ctx, batch, q, k, v, q_rot, cache)
     _check(_lib.rope_append_paged(ctx.handle, layer, batch.ref, _ptr(q), qs, k.data_ptr(), _row_stride(k), v.data_ptr(),
                                   _row_stride(v), _ptr(q_rot), cache.ref, _stream(stream)), "rope_append_paged")
 
@@ -610,6 +647,129 @@ def attn_selected_pages(ctx: Context, layer: int, batch: PagedBatch, q_rot, cach
     _check(_lib.attn_selected_pages(ctx.handle, layer, batch.ref, q_rot.data_ptr(), cache.ref, selected.data_ptr(),
                                     selected.shape[-1], _ptr(sink), _ptr(gate), out.data_ptr(), lse.data_ptr(),
                                     _stream(stream)), "attn_selected_pages")
+
+
+def _rope_params(rotary_dim, theta, scaling, factor, original_context, slow, fast, amplitude) -> hd_rope_params:
+    return hd_rope_params(rotary_dim, scaling, theta, factor, original_context, slow, fast, amplitude)
+
+
+def hd_rope_frequencies(rotary_dim: int, theta: float = 1.0e4, scaling: int = HD_ROPE_PLAIN, factor: float = 1.0,
+                        original_context: float = 0.0, slow: float = 1.0, fast: float = 32.0,
+                        amplitude: float = 0.0) -> tuple[list, float]:
+    """(frequencies of the rotary_dim / 2 pairs in radians a position, amplitude) of a table of
+    angles (pure host function); the arguments are hd_rope_params' in include/hybrid_decode.h."""
+    p = _rope_params(rotary_dim, theta, scaling, factor, original_context, slow, fast, amplitude)
+    f, m = (ctypes.c_double * 128)(), ctypes.c_double()
+    _check(_lib.hd_rope_frequencies(ctypes.byref(p), f, ctypes.byref(m)), "hd_rope_frequencies")
+    return list(f[: rotary_dim // 2]), m.value
+
+
+class RopeTable:
+    """A table of angles (see ``rope_table``): the C descriptor and its tensor."""
+
+    def __init__(self, c, table):
+        self.c, self.ref, self.table = c, ctypes.byref(c), table
+
+
+def rope_table(rotary_dim: int, positions: int, theta: float = 1.0e4, layout: int = HD_ROPE_HALVES,
+               scaling: int = HD_ROPE_PLAIN, factor: float = 1.0, original_context: float = 0.0, slow: float = 1.0,
+               fast: float = 32.0, amplitude: float = 0.0, table: torch.Tensor | None = None, stream=None) -> RopeTable:
+    """A table of ``positions`` rows of angles for norm_rope_append_paged, made once for a model:
+    HD_ROPE_PLAIN, or scaled for long contexts (LINEAR, RAMP, BANDS; include/hybrid_decode.h has the
+    formulas), turning dims in HD_ROPE_HALVES or as HD_ROPE_NEIGHBOURS.  ``table``: float32
+    [positions, rotary_dim / 2, 2] on the current device to fill (default: a new one)."""
+    p = _rope_params(rotary_dim, theta, scaling, factor, original_context, slow, fast, amplitude)
+    f, m = (ctypes.c_double * 128)(), ctypes.c_double()
+    _check(_lib.hd_rope_frequencies(ctypes.byref(p), f, ctypes.byref(m)), "rope_table")
+    if layout not in (HD_ROPE_HALVES, HD_ROPE_NEIGHBOURS) or positions < 1:
+        raise ValueError("layout must be HD_ROPE_HALVES or HD_ROPE_NEIGHBOURS, positions at least 1")
+    shape = (positions, rotary_dim // 2, 2)
+    if table is None:
+        table = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()))
+    elif (tuple(table.shape) != shape or table.dtype != torch.float32 or not table.is_contiguous() or not table.is_cuda or
+          table.device.index != torch.cuda.current_device()):
+        raise ValueError(f"table must be contiguous float32 of shape {shape} on the current device")
+    _check(_lib.hd_rope_fill(ctypes.byref(p), positions, table.data_ptr(), _stream(stream)), "rope_table")
+    return RopeTable(hd_rope_table(table.data_ptr(), positions, rotary_dim, layout), table)
+
+
+def _check_ints(name: str, t, n: int, device) -> None:
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 of shape ({n},) on {device}")
+
+
+def norm_rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
+                           rope: RopeTable | None = None, q_weight: torch.Tensor | None = None,
+                           k_weight: torch.Tensor | None = None, eps: float = 1.0e-6, weight_offset: float = 0.0,
+                           positions: torch.Tensor | None = None, norm: bool = True, stream=None) -> None:
+    """rope_append_paged for models that norm the heads of their queries and keys or turn them by other
+    angles: y = x / rms(x) * (weight_offset + weight), rotated by ``rope`` (None: the context's own
+    angles) at the rows' positions in their sequences, or at ``positions`` (int32 [num_tokens]).
+    ``q_weight`` / ``k_weight``: bf16 or float32 [256], or one row a head ([Hq, 256] and [Hkv, 256]);
+    None: ones.  ``norm=False``: the rotation alone."""
+    qs = _check_append(ctx, batch, q, k, v, q_rot, cache)
+    _check_ints("positions", positions, batch.num_tokens, cache.device)
+    if rope is not None and rope.table.device != cache.device:
+        raise ValueError("the table of angles must be on the pages' device")
+    ref = None
+    if norm:
+        have = [(n, w, h) for n, w, h in (("q_weight", q_weight, ctx.cfg.num_q_heads), ("k_weight", k_weight, ctx.cfg.num_kv_heads))
+                if w is not None]
+        for n, w, h in have:
+            if (tuple(w.shape) not in ((256,), (h, 256)) or w.dtype not in (torch.bfloat16, torch.float32) or
+                    w.device != cache.device or not w.is_contiguous()):
+                raise ValueError(f"{n} must be contiguous bf16 or float32 of shape (256,) or ({h}, 256) on {cache.device}")
+        if len({(w.dtype, w.dim()) for _, w, _ in have}) > 1:
+            raise ValueError("q_weight and k_weight must share a type and be both per head or both shared")
+        ref = ctypes.byref(hd_head_norm(_ptr(q_weight), _ptr(k_weight), int(any(w.dtype == torch.float32 for _, w, _ in have)),
+                                        int(any(w.dim() == 2 for _, w, _ in have)), weight_offset, eps))
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights belong to a norm")
+    _check(_lib.norm_rope_append_paged(ctx.handle, layer, batch.ref, ref, None if rope is None else rope.ref, _ptr(positions),
+                                       _ptr(q), qs, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), _ptr(q_rot),
+                                       cache.ref, _stream(stream)), "norm_rope_append_paged")
+
+
+class Scoring:
+    """A rule of scores and visible positions (see ``scoring``): the C descriptor and its tensors."""
+
+    def __init__(self, c, slopes, first, last):
+        self.c, self.ref, self.slopes, self.first, self.last = c, ctypes.byref(c), slopes, first, last
+
+
+def scoring(softcap: float = 0.0, scale: float = 0.0, slopes: torch.Tensor | None = None, first: torch.Tensor | None = None,
+            last: torch.Tensor | None = None) -> Scoring:
+    """How attn_paged_scored scores and masks: scores scale * q.k (0: 1/16), capped at ``softcap`` by a
+    tanh (0: not), less ``slopes[head]`` (float32 [Hq]) times the distance of query and key; row r sees
+    the positions ``first[r]`` .. ``last[r]`` (int32 [num_tokens], both ascending along a sequence's rows;
+    None: 0 and its own position), within a sliding layer's window and the sequence."""
+    return Scoring(hd_scoring(scale, softcap, _ptr(slopes), _ptr(first), _ptr(last)), slopes, first, last)
+
+
+def attn_paged_scored(ctx: Context, layer: int, batch: PagedBatch, rule: Scoring, q_rot, cache: PagedCache, sink, out, lse,
+                      gate=None, stream=None) -> None:
+    """attn_paged with capped or biased scores and masks of documents and prefixes (``scoring``)."""
+    _check_attn_paged(ctx, batch, q_rot, cache, sink, gate, out, lse)
+    if rule.slopes is not None and (rule.slopes.dtype != torch.float32 or tuple(rule.slopes.shape) != (ctx.cfg.num_q_heads,) or
+                                    rule.slopes.device != cache.device or not rule.slopes.is_contiguous()):
+        raise ValueError(f"slopes must be contiguous float32 of shape ({ctx.cfg.num_q_heads},) on {cache.device}")
+    _check_ints("first", rule.first, batch.num_tokens, cache.device)
+    _check_ints("last", rule.last, batch.num_tokens, cache.device)
+    _check(_lib.attn_paged_scored(ctx.handle, layer, batch.ref, rule.ref, q_rot.data_ptr(), cache.ref, _ptr(sink), _ptr(gate),
+                                  out.data_ptr(), lse.data_ptr(), _stream(stream)), "attn_paged_scored")
+
+
+def read_paged(ctx: Context, batch: PagedBatch, cache: PagedCache, k=None, v=None, stream=None) -> None:
+    """Read entries back: k / v [num_tokens, Hkv, 256] bf16 (either may be None, rows may be parts of wider
+    ones) get the entries at the batch's "new" positions, context[b] onwards; E4M3 codes times their
+    scale, rounded once.  Keys come as stored, rotated."""
+    _check_paged(ctx, batch, cache)
+    shape = (batch.num_tokens, ctx.cfg.num_kv_heads, 256)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _check_rows(name, t, shape, torch.bfloat16, cache.device, True)
+    _check(_lib.read_paged(ctx.handle, batch.ref, cache.ref, _ptr(k), 0 if k is None else _row_stride(k), _ptr(v),
+                           0 if v is None else _row_stride(v), _stream(stream)), "read_paged")
 
 
 def hybrid_decode_read_probe(buffer: torch.Tensor, stream=None) -> int:

@@ -19,9 +19,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libhybriddecode.so")
 SOURCES = ["api.cpp", "rope_append.cu", "attn_decode.cu", "attn_decode_fp8.cu", "attn_step.cu",
            "attn_step_fp8.cu", "noalloc.cu", "read_probe.cu", "paged_api.cpp", "paged_append.cu",
-           "paged_decode.cu", "paged_chunk.cu", "paged_select.cu"]
+           "paged_decode.cu", "paged_chunk.cu", "paged_select.cu", "paged_norm_append.cu", "paged_read.cu", "rope_table.cu"]
 HEADERS = ["hd_internal.h", "hd_context.h", "ptx.cuh", "attn_kernel.cuh", "e4m3.cuh", "rope_round.cuh", "paged.h",
-           "paged_sched.cuh", "paged_rows.cuh"]
+           "paged_sched.cuh", "paged_rows.cuh", "paged_entry.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -43,6 +43,26 @@ struct PagedAppendArgs {
     int32_t rotary_dim, num_q_heads, num_kv_heads, kv_type;
 };
 
+// The same with the heads' norms and a given table of angles (entry.rope, entry.rotary_dim).
+struct PagedNormArgs {
+    PagedAppendArgs entry;
+    const int32_t *positions;               // [num_tokens] rows of the table, or null: the positions in the sequences
+    const void *q_weight, *k_weight;        // [256], or [heads][256] with per_head; null: ones
+    float offset, eps;
+    int32_t table_rows;
+    int32_t norm, f32_weights, per_head, neighbours;
+};
+
+struct PagedReadArgs {
+    PagedSeqs seqs;
+    const void *cache_k, *cache_v;
+    int64_t page_stride;                    // elements
+    const float *k_scale, *v_scale;         // E4M3 or null
+    __nv_bfloat16 *k, *v;                   // rows, either may be null
+    int64_t k_stride, v_stride;
+    int32_t num_kv_heads, kv_type;
+};
+
 // Attention over pages: dense (every visible position) or over selected
 // blocks (`selected`: [num_tokens][Hkv][num_selected] ascending block numbers,
 // -1 past the end).
@@ -64,6 +84,12 @@ struct PagedAttnArgs {
     int32_t window;            // sliding layers; 0: all positions
     int32_t kv_type;
     int32_t drop_stage;        // test hook: the producers stop issuing at this stage (-1: off)
+    // attn_paged_scored: its rule, in log2 units (scores times log2(e)).
+    int32_t scored;            // 0: none of what follows counts
+    float qscale;              // of q . k
+    float cap, two_over_cap;   // cap log2(e) and 2 / cap; 0: no cap
+    const float *slopes;       // [Hq] or null
+    const int32_t *first, *last;   // [num_tokens] or null: visible positions of a row
 };
 
 struct PagedSelectArgs {
@@ -112,6 +138,13 @@ cudaError_t launch_overlapping(void (*kernel)(P...), dim3 grid, int threads, siz
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s);
+cudaError_t launch_paged_norm_append(const PagedNormArgs &a, cudaStream_t s);
+cudaError_t launch_paged_read(const PagedReadArgs &a, cudaStream_t s);
+// Angles of `pairs` frequencies for positions 0 .. positions - 1.
+struct RopeFrequencies {
+    double f[kHeadDim / 2];
+};
+cudaError_t launch_rope_fill(const RopeFrequencies &f, double amplitude, int pairs, int positions, float2 *table, cudaStream_t s);
 // kmap / vmap: 5-D views of the pages with boxes of min(page, stage) rows (paged_map_rows).
 cudaError_t launch_paged_decode(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms,
                                 cudaStream_t s);

@@ -4,12 +4,15 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "hd_context.h"
 
 using namespace hd;
 
 namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 bool page_shift_of(int page_size, int *shift) {
     for (int s = kMinPageShift; s <= kMaxPageShift; ++s)
@@ -79,8 +82,8 @@ bool encode_queries(CUtensorMap *map, const void *q, int num_q_heads, int num_to
 }
 
 hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_rot, const hd_paged_cache &c,
-                 const int32_t *selected, int num_selected, const float *sink, const float *gate, void *out, float *lse,
-                 void *stream) {
+                 const int32_t *selected, int num_selected, const hd_scoring *rule, const float *sink, const float *gate,
+                 void *out, float *lse, void *stream) {
     if (seqs.num_tokens == 0) return HD_OK;   // no rows: their tensors may be null
     if (!q_rot || !aligned16(q_rot) || !out || !aligned16(out) || !lse) return HD_ERR_INVALID_ARG;
     PagedAttnArgs a{};
@@ -105,6 +108,17 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     a.window = ctx->layer_types[layer] == HD_SLIDING ? ctx->cfg.sliding_window : 0;
     a.kv_type = ctx->kv_type;
     a.drop_stage = ctx->drop_stage;
+    if (rule) {
+        a.scored = 1;
+        a.qscale = (rule->scale != 0.f ? rule->scale : 1.f / 16.f) * kLog2e;
+        if (rule->softcap != 0.f) {
+            a.cap = rule->softcap * kLog2e;
+            a.two_over_cap = 2.f / rule->softcap;
+        }
+        a.slopes = rule->slopes;
+        a.first = rule->first;
+        a.last = rule->last;
+    }
     // More than eight rows per kv head in some sequence: the tensor-memory kernel, which also serves the call's
     // single tokens; lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
     const bool chunk = !selected && (int64_t)seqs.max_tokens * ctx->group > kDecodeRows;
@@ -133,6 +147,45 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     }
     if (st == HD_OK) ++ctx->launches;
     return st;
+}
+
+// Checks of an append's tensors; fills everything of its kernel arguments but the angles.
+hd_status check_append(const hd_ctx *ctx, int layer, const hd_paged_batch *batch, const void *q, int64_t q_stride, const void *k,
+                       int64_t k_stride, const void *v, int64_t v_stride, void *q_rot, const hd_paged_cache *cache,
+                       PagedAppendArgs *out) {
+    PagedAppendArgs &a = *out;
+    const hd_status st = check_paged(ctx, layer, batch, cache, &a.seqs);
+    if (st != HD_OK || batch->num_tokens == 0) return st;
+    const int64_t Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || (q == nullptr) != (q_rot == nullptr) || !aligned16(q) ||
+        !aligned16(q_rot))
+        return HD_ERR_INVALID_ARG;
+    if (k_stride % 8 || v_stride % 8 || k_stride < Hkv * kHeadDim || v_stride < Hkv * kHeadDim ||
+        (q && (q_stride % 8 || q_stride < Hq * kHeadDim)))
+        return HD_ERR_INVALID_ARG;
+    // q_rot in place of q, row by row, or apart from it: elsewhere its rows would lie over rows not yet rotated.
+    const auto *src = static_cast<const uint8_t *>(q), *dst = static_cast<const uint8_t *>(q_rot);
+    const int64_t row = Hq * kHeadDim * 2, rows = batch->num_tokens;
+    if (q && src < dst + rows * row && dst < src + (rows - 1) * q_stride * 2 + row &&
+        !(src == dst && (rows == 1 || q_stride == Hq * kHeadDim)))
+        return HD_ERR_INVALID_ARG;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_rot = static_cast<__nv_bfloat16 *>(q_rot);
+    a.cache_k = cache->k;
+    a.cache_v = cache->v;
+    a.page_stride = cache->page_stride;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.bounds = static_cast<__nv_bfloat16 *>(cache->bounds);
+    a.num_q_heads = (int32_t)Hq;
+    a.num_kv_heads = (int32_t)Hkv;
+    a.kv_type = ctx->kv_type;
+    return HD_OK;
 }
 
 }  // namespace
@@ -164,45 +217,96 @@ hd_status rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *ba
                             const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_rot,
                             const hd_paged_cache *cache, void *stream) {
     PagedAppendArgs a{};
-    hd_status st = check_paged(ctx, layer, batch, cache, &a.seqs);
+    hd_status st = check_append(ctx, layer, batch, q, q_stride, k, k_stride, v, v_stride, q_rot, cache, &a);
     if (st != HD_OK || batch->num_tokens == 0) return st;
-    const int64_t Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads;
-    if (!k || !v || !aligned16(k) || !aligned16(v) || (q == nullptr) != (q_rot == nullptr) || !aligned16(q) ||
-        !aligned16(q_rot))
-        return HD_ERR_INVALID_ARG;
-    if (k_stride % 8 || v_stride % 8 || k_stride < Hkv * kHeadDim || v_stride < Hkv * kHeadDim ||
-        (q && (q_stride % 8 || q_stride < Hq * kHeadDim)))
-        return HD_ERR_INVALID_ARG;
-    // q_rot in place of q, row by row, or apart from it: elsewhere its rows would lie over rows not yet rotated.
-    const auto *src = static_cast<const uint8_t *>(q), *dst = static_cast<const uint8_t *>(q_rot);
-    const int64_t row = Hq * kHeadDim * 2, rows = batch->num_tokens;
-    if (q && src < dst + rows * row && dst < src + (rows - 1) * q_stride * 2 + row &&
-        !(src == dst && (rows == 1 || q_stride == Hq * kHeadDim)))
-        return HD_ERR_INVALID_ARG;
-    const bool sliding = ctx->layer_types[layer] == HD_SLIDING;
-    const DeviceTable &tab = sliding ? ctx->table_sliding : ctx->table_full;
+    const DeviceTable &tab = ctx->layer_types[layer] == HD_SLIDING ? ctx->table_sliding : ctx->table_full;
     if (tab.rotary_dim % 8) return HD_ERR_UNSUPPORTED;
-    a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.k = static_cast<const __nv_bfloat16 *>(k);
-    a.v = static_cast<const __nv_bfloat16 *>(v);
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.q_rot = static_cast<__nv_bfloat16 *>(q_rot);
+    a.rope = tab.data;
+    a.rotary_dim = tab.rotary_dim;
+    st = cuda_status(launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+    if (st == HD_OK) ++ctx->launches;
+    return st;
+}
+
+hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const hd_head_norm *norm,
+                                 const hd_rope_table *rope, const int32_t *positions, const void *q, int64_t q_stride,
+                                 const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_rot,
+                                 const hd_paged_cache *cache, void *stream) {
+    PagedNormArgs a{};
+    hd_status st = check_append(ctx, layer, batch, q, q_stride, k, k_stride, v, v_stride, q_rot, cache, &a.entry);
+    if (st != HD_OK) return st;
+    if (norm && (!aligned16(norm->q_weight) || !aligned16(norm->k_weight) || !std::isfinite(norm->offset) || !(norm->eps > 0.f) ||
+                 !std::isfinite(norm->eps)))
+        return HD_ERR_INVALID_ARG;
+    if (rope && (!rope->table || !aligned16(rope->table) || rope->positions < 1 || rope->rotary_dim < 8 ||
+                 rope->rotary_dim > kHeadDim || rope->rotary_dim % 8 || rope->layout < HD_ROPE_HALVES ||
+                 rope->layout > HD_ROPE_NEIGHBOURS))
+        return HD_ERR_INVALID_ARG;
+    if (batch->num_tokens == 0) return HD_OK;
+    if (rope) {
+        a.entry.rope = reinterpret_cast<const float2 *>(rope->table);
+        a.entry.rotary_dim = rope->rotary_dim;
+        a.table_rows = rope->positions;
+        a.neighbours = rope->layout == HD_ROPE_NEIGHBOURS;
+    } else {
+        const DeviceTable &tab = ctx->layer_types[layer] == HD_SLIDING ? ctx->table_sliding : ctx->table_full;
+        if (tab.rotary_dim % 8) return HD_ERR_UNSUPPORTED;
+        a.entry.rope = tab.data;
+        a.entry.rotary_dim = tab.rotary_dim;
+        a.table_rows = ctx->cfg.max_context + 1;
+    }
+    a.positions = positions;
+    if (!positions) a.entry.seqs.max_position = std::min(a.entry.seqs.max_position, a.table_rows - 1);
+    if (norm) {
+        a.norm = 1;
+        a.q_weight = norm->q_weight;
+        a.k_weight = norm->k_weight;
+        a.f32_weights = norm->f32_weights != 0;
+        a.per_head = norm->per_head != 0;
+        a.offset = norm->offset;
+        a.eps = norm->eps;
+    }
+    st = cuda_status(launch_paged_norm_append(a, static_cast<cudaStream_t>(stream)));
+    if (st == HD_OK) ++ctx->launches;
+    return st;
+}
+
+hd_status read_paged(hd_ctx *ctx, const hd_paged_batch *batch, const hd_paged_cache *cache, void *k, int64_t k_stride, void *v,
+                     int64_t v_stride, void *stream) {
+    PagedReadArgs a{};
+    hd_status st = check_paged(ctx, 0, batch, cache, &a.seqs);
+    if (st != HD_OK || batch->num_tokens == 0 || (!k && !v)) return st;
+    const int64_t row = (int64_t)ctx->cfg.num_kv_heads * kHeadDim;
+    if (!aligned16(k) || !aligned16(v) || (k && (k_stride % 8 || k_stride < row)) || (v && (v_stride % 8 || v_stride < row)))
+        return HD_ERR_INVALID_ARG;
     a.cache_k = cache->k;
     a.cache_v = cache->v;
     a.page_stride = cache->page_stride;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
-    a.bounds = static_cast<__nv_bfloat16 *>(cache->bounds);
-    a.rope = tab.data;
-    a.rotary_dim = tab.rotary_dim;
-    a.num_q_heads = (int32_t)Hq;
-    a.num_kv_heads = (int32_t)Hkv;
+    a.k = static_cast<__nv_bfloat16 *>(k);
+    a.v = static_cast<__nv_bfloat16 *>(v);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.num_kv_heads = ctx->cfg.num_kv_heads;
     a.kv_type = ctx->kv_type;
-    st = cuda_status(launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+    st = cuda_status(launch_paged_read(a, static_cast<cudaStream_t>(stream)));
     if (st == HD_OK) ++ctx->launches;
     return st;
+}
+
+hd_status attn_paged_scored(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const hd_scoring *scoring,
+                            const void *q_rot, const hd_paged_cache *cache, const float *sink, const float *gate, void *out,
+                            float *lse, void *stream) {
+    PagedSeqs s;
+    const hd_status st = check_paged(ctx, layer, batch, cache, &s);
+    if (st != HD_OK) return st;
+    if (scoring) {
+        const float scale = scoring->scale, cap = scoring->softcap;
+        if (!std::isfinite(scale) || scale < 0.f || !std::isfinite(cap) || cap < 0.f) return HD_ERR_INVALID_ARG;
+        if (cap != 0.f && (cap < 1.f / 1024.f || cap > 1024.f)) return HD_ERR_UNSUPPORTED;
+    }
+    return attend(ctx, layer, s, q_rot, *cache, nullptr, 0, scoring, sink, gate, out, lse, stream);
 }
 
 hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
@@ -211,7 +315,7 @@ hd_status attn_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, co
     PagedSeqs s;
     const hd_status st = check_paged(ctx, layer, batch, cache, &s);
     if (st != HD_OK) return st;
-    return attend(ctx, layer, s, q_rot, *cache, nullptr, 0, sink, gate, out, lse, stream);
+    return attend(ctx, layer, s, q_rot, *cache, nullptr, 0, nullptr, sink, gate, out, lse, stream);
 }
 
 hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
@@ -256,7 +360,7 @@ hd_status attn_selected_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *
     if (st != HD_OK) return st;
     if (ctx->layer_types[layer] != HD_FULL) return HD_ERR_STATE;
     if ((!selected && batch->num_tokens) || num_selected < 1) return HD_ERR_INVALID_ARG;
-    return attend(ctx, layer, s, q_rot, *cache, selected, num_selected, sink, gate, out, lse, stream);
+    return attend(ctx, layer, s, q_rot, *cache, selected, num_selected, nullptr, sink, gate, out, lse, stream);
 }
 
 }  // extern "C"

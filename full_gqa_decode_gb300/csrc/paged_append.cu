@@ -21,24 +21,15 @@
 // of this, not by its bytes: testing each value's distance from the rounding's
 // midpoint instead took twice as many (9026 tokens at 16 heads, E4M3: 71 us,
 // so 37 us).
-#include <cuda_fp8.h>
-
-#include "e4m3.cuh"
-#include "paged_sched.cuh"
-#include "rope_round.cuh"
+#include "paged_entry.cuh"
 
 namespace hd {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = kEntryThreads, kWarps = kEntryWarps;
 constexpr int kQueryHeads = 4;   // heads of a row that one warp rotates (9026 tokens at 16 heads: 2 44 us, 4 37 us)
 
-// The binary64 paths are calls: inlined at every use they make the kernel wait for its instructions.
-__device__ __noinline__ uint32_t e4m3_rotated_f64(float a, float c, float b, float sn, float s) {
-    const double y = __dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)sn));
-    return e4m3_from_f64(__ddiv_rn(y, (double)s));
-}
+// The binary64 paths are calls, see e4m3_rotated_f64.
 __device__ __noinline__ uint32_t rotated_f64(float a, float c, float b, float s) {
     return __float_as_uint(f64_to_bf16_value(__dsub_rn(__dmul_rn((double)a, (double)c), __dmul_rn((double)b, (double)s)))) >> 16;
 }
@@ -55,28 +46,6 @@ __device__ __forceinline__ uint32_t rotated_bf16x2(float a0, float b0, float a1,
     if (differ & 0xFFFFu) lo = (lo & 0xFFFF0000u) | rotated_f64(a0, c0, b0, s0);
     if (differ >> 16) lo = (lo & 0xFFFFu) | rotated_f64(a1, c1, b1, s1) << 16;
     return lo;
-}
-
-// A scale's reciprocal, and the bounds that go with it.
-struct Recip {
-    float s, inv;   // inv = RN(1 / s)
-    float rel, abs;
-    uint32_t odd;   // all ones: the reciprocal is no normal number
-};
-__device__ __forceinline__ Recip recip_of(float s) {
-    Recip r;
-    r.s = s;
-    r.inv = 1.f / s;
-    const float m = fabsf(r.inv);
-    r.odd = m > 1.2e-38f && m < 3e38f ? 0u : 0xFFFFFFFFu;
-    r.rel = 2.4e-7f * m;   // over 2^-22 |1 / s|
-    r.abs = fmaf(m, 7.2e-43f, 7.2e-43f);
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
-    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, __NV_E4M3);
-    return l | h << 16;
 }
 
 // Four codes e4m3(fl64(y / s)) for y = a c - b sn rounded to binary64.  With y and q as above, y inv is off by
@@ -100,63 +69,6 @@ __device__ __forceinline__ uint32_t e4m3_rotated(const float (&a)[4], const floa
     }
     return code;
 }
-// Four codes e4m3(fl64(a / s)).  a inv carries a's sign to the last.
-__device__ __forceinline__ uint32_t e4m3_plain(const float (&a)[4], const Recip &r) {
-    float lo[4], hi[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float e = fabsf(a[j]) * r.rel;
-        lo[j] = fmaf(a[j], r.inv, -e);
-        hi[j] = fmaf(a[j], r.inv, e);
-    }
-    uint32_t code = e4m3x4(lo[0], lo[1], lo[2], lo[3]);
-    if ((code ^ e4m3x4(hi[0], hi[1], hi[2], hi[3])) | r.odd) {
-        code = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code |= e4m3_rotated_f64(a[j], 1.f, 0.f, 0.f, r.s) << (8 * j);
-    }
-    return code;
-}
-
-// Elementwise minimum and maximum of two bf16 or two f16, numbers before NaN.
-template <bool BF16>
-__device__ __forceinline__ void widen2(uint32_t &lo, uint32_t &hi, uint32_t x) {
-    if (BF16) {
-        asm("min.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(x));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(x));
-    } else {
-        asm("min.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(x));
-        asm("max.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(x));
-    }
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t x;
-    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(x) : "r"(codes));
-    return x;
-}
-
-// A lane's eight dims of a row: two runs of four, at d0 and d1.
-struct LaneDims {
-    int d0, d1, i;   // i: first rotary pair (-1: past the rotation)
-};
-__device__ __forceinline__ LaneDims lane_dims(int lane, int rot) {
-    const int half = rot >> 1;
-    if (4 * lane < half) return {4 * lane, 4 * lane + half, 4 * lane};
-    const int d = rot + 8 * (lane - half / 4);
-    return {d, d + 4, -1};
-}
-__device__ __forceinline__ void unpack4(uint2 w, float (&x)[4]) {
-    x[0] = __uint_as_float(w.x << 16);
-    x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(w.y << 16);
-    x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load_angles(const float2 *cs, int i, float (&c)[4], float (&s)[4]) {
-    const float4 u = __ldg(reinterpret_cast<const float4 *>(cs + i)), v = __ldg(reinterpret_cast<const float4 *>(cs + i + 2));
-    c[0] = u.x; s[0] = u.y; c[1] = u.z; s[1] = u.w;
-    c[2] = v.x; s[2] = v.y; c[3] = v.z; s[3] = v.w;
-}
-
 // Rotates a lane's dims in place, each value rounded once to bf16.
 __device__ __forceinline__ void rotate_bf16(uint2 &x, uint2 &y, const float (&c)[4], const float (&s)[4]) {
     float a[4], b[4];
@@ -215,45 +127,9 @@ __global__ void __launch_bounds__(kThreads, 5) paged_append_kernel(const __grid_
 
     // ---- keys and values of one run ----
     const int run = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
-    int b = run, block = 0, bit = 0;
-    if (sq.offsets) {
-        const int per = (sq.batch + kThreads - 1) / kThreads;
-        const int b_lo = min(tid * per, sq.batch), b_hi = min(b_lo + per, sq.batch);
-        long long mine = 0, total;
-        int bad = 0;
-        for (int i = b_lo; i < b_hi; ++i) {
-            const SeqSpan q = seq_span(sq, i, &bit);
-            bad |= bit;
-            if (q.n) mine += ((q.ctx + q.n - 1) >> sq.page_shift) - (q.ctx >> sq.page_shift) + 1;
-        }
-        if (bad && run == 0 && h == 0) atomicOr(sq.err, bad);
-        if (tid == 0) found[0] = -1;
-        const long long before = block_prefix(mine, scan, &total);
-        if (before <= run && run < before + mine) {
-            long long rem = run - before;
-            for (int i = b_lo; i < b_hi; ++i) {
-                const SeqSpan q = seq_span(sq, i, &bit);
-                if (!q.n) continue;
-                const int nb = ((q.ctx + q.n - 1) >> sq.page_shift) - (q.ctx >> sq.page_shift) + 1;
-                if (rem < nb) {
-                    found[0] = i;
-                    found[1] = (q.ctx >> sq.page_shift) + (int)rem;
-                    break;
-                }
-                rem -= nb;
-            }
-        }
-        __syncthreads();
-        b = found[0];
-        if (b < 0) return;
-        block = found[1];
-    }
-    const SeqSpan q = seq_span(sq, b, &bit);
-    if (q.n == 0) {
-        if (bit && !sq.offsets && h == 0 && tid == 0) atomicOr(sq.err, bit);
-        return;
-    }
-    if (!sq.offsets) block = q.ctx >> sq.page_shift;
+    int b, block;
+    SeqSpan q;
+    if (!find_run(sq, run, h == 0, scan, found, &b, &block, &q)) return;
     const int page = sq.table[(size_t)b * sq.table_stride + block];
     if (page < 0 || page >= sq.num_pages) {
         if (tid == 0) atomicOr(sq.err, HD_DEVERR_PAGE);
@@ -313,42 +189,14 @@ __global__ void __launch_bounds__(kThreads, 5) paged_append_kernel(const __grid_
             widen2<true>(lo[3], hi[3], y.y);
         }
     }
-    if (!a.bounds) return;
-    auto pair = [&](uint32_t w) {
-        return fp8 ? __half22float2(*reinterpret_cast<const __half2 *>(&w))
-                   : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    };
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int d = (j < 2 ? ld.d0 : ld.d1) + 2 * (j & 1);
-        *reinterpret_cast<float2 *>(&edge[0][warp][d]) = pair(lo[j]);
-        *reinterpret_cast<float2 *>(&edge[1][warp][d]) = pair(hi[j]);
-    }
-    __syncthreads();
-    __nv_bfloat16 *bd = a.bounds + ((size_t)page * a.num_kv_heads + h) * 2 * kHeadDim;
-    const bool fresh = (p0 & (ps - 1)) == 0;
-    for (int d = tid; d < kHeadDim; d += kThreads) {
-        float l = edge[0][0][d], m = edge[1][0][d];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            l = fminf(l, edge[0][w][d]);
-            m = fmaxf(m, edge[1][w][d]);
-        }
-        if (!fresh) {
-            l = fminf(l, __bfloat162float(bd[d]));
-            m = fmaxf(m, __bfloat162float(bd[kHeadDim + d]));
-        }
-        bd[d] = __float2bfloat16_rn(l);             // exact: bf16 keys or E4M3 code values
-        bd[kHeadDim + d] = __float2bfloat16_rn(m);
-    }
+    if (a.bounds) store_bounds(a, page, h, fp8, (p0 & (ps - 1)) == 0, ld, lo, hi, edge);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s) {
     const PagedSeqs &q = a.seqs;
-    // A sequence of n tokens touches at most (n - 1) / page + 2 pages, one of one token exactly one.
-    const long long runs = q.offsets ? ((long long)q.num_tokens >> q.page_shift) + 2LL * q.batch : q.batch;
+    const long long runs = max_runs(q);
     const long long parts = (a.num_q_heads + kQueryHeads - 1) / kQueryHeads;
     const long long qctas = a.q ? ((long long)q.num_tokens * parts + kWarps - 1) / kWarps : 0;
     const long long grid = runs * a.num_kv_heads + qctas;

@@ -118,6 +118,12 @@ __device__ __forceinline__ ChunkTile make_chunk_tile(const PagedAttnArgs &a, con
     t.units = ((t.hi + kTileKeys - 1) >> kKeyShift) - t.u0;
     return t;
 }
+template <bool SCORED>
+__device__ __forceinline__ ChunkTile make_item(const PagedAttnArgs &a, const SeqSpan &q, int tile) {
+    if constexpr (!SCORED) return make_chunk_tile(a, q, tile);
+    const int tt = kTileRows >> a.group_shift;
+    return scored_tile<ChunkTile>(a, q, tile * tt, min(tt, q.n - tile * tt), kKeyShift);
+}
 __device__ __forceinline__ int num_chunk_tiles(const PagedAttnArgs &a, int n) {
     return ((n << a.group_shift) + kTileRows - 1) / kTileRows;
 }
@@ -128,6 +134,7 @@ __device__ __forceinline__ int longest_whole(const PagedAttnArgs &a) {
 }
 
 // A walk over the segments of a pair's share.
+template <bool SCORED>
 struct Segment {
     int b, tile, h;      // the item
     SeqSpan q;
@@ -159,7 +166,7 @@ struct Segment {
                     q = seq_span(a.seqs, ++b, &bit);
                 } while (q.n == 0 && b + 1 < a.seqs.batch);
             }
-            t = make_chunk_tile(a, q, tile);
+            t = make_item<SCORED>(a, q, tile);
         }
         return true;
     }
@@ -172,7 +179,7 @@ struct Segment {
         done = 0;
         int bit;
         q = seq_span(a.seqs, b, &bit);
-        t = make_chunk_tile(a, q, tile);
+        t = make_item<SCORED>(a, q, tile);
         return settle(a);
     }
     __device__ bool next(const PagedAttnArgs &a) { return advance(a) && settle(a); }
@@ -312,7 +319,7 @@ __device__ __forceinline__ void transpose4(uint4 (&e)[4], int lane) {
         }
 }
 
-template <int KV>
+template <int KV, bool SCORED>
 __global__ void __launch_bounds__(chunk_threads(KV), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     const Start c0 = find_share(
         sq, a.num_kv_heads, pair, pairs, kMinTiles, 0, longest_whole(a), INT_MAX, reinterpret_cast<long long *>(xm), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_chunk_tiles(a, tokens); },
-        [&](const SeqSpan &q, int i) { return make_chunk_tile(a, q, i).units + kItemCost; });
+        [&](const SeqSpan &q, int i) { return make_item<SCORED>(a, q, i).units + kItemCost; });
     if (bad) fill_bad_rows(a, blockIdx.x, gridDim.x);
     if (x0 >= x1) return;   // both CTAs of the pair
     long long *call = reinterpret_cast<long long *>(misc + 6);   // T and x0, which only cut items need again
@@ -369,14 +376,14 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     tc_fence_after();
     const uint32_t tmem = *taddr_s;
     const int share = (int)(x1 - x0);
-    Segment w;
+    Segment<SCORED> w;
     bool more = w.start(a, c0, share);   // no role has work when the share holds item costs alone
     bool dead = false;
     const int ps = 1 << sq.page_shift;
     // Whole-warp wait for the end of block i.
     auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 3)], (uint32_t)(i >> 2) & 1, dead, err); };
     // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
-    auto pages_of = [&](const Segment &x, int k) {
+    auto pages_of = [&](const Segment<SCORED> &x, int k) {
         const int pos = x.key0(k) + 16 * (lane & 7), first = pos & ~(ps - 1);
         int page = sq.num_pages;
         if (first < x.t.hi && first + ps > x.t.lo) {
@@ -698,11 +705,24 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         const float lift = kFp8 ? 7.f : 0.f;
         int blocks = 0, tiles = 0;   // before this segment
         for (uint32_t seg = 0; more; ++seg) {
-        float m = -INFINITY, l = 0.f, scale = kQScale;
+        float m = -INFINITY, l = 0.f, scale = SCORED ? a.qscale : kQScale;
         const int r = rank * kCtaRows + row;
-        const int hi_pos = w.q.ctx + w.t.t0 + (r >> a.group_shift), lo_pos = a.window ? hi_pos - a.window + 1 : 0;
-        const int all_hi = w.q.ctx + w.t.t0;                                            // every row sees up to here ..
-        const int all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;        // .. from here
+        const int pos = w.q.ctx + w.t.t0 + (r >> a.group_shift);
+        int hi_pos = pos, lo_pos = a.window ? hi_pos - a.window + 1 : 0;
+        int all_hi = w.q.ctx + w.t.t0;                                            // every row sees up to here ..
+        int all_lo = a.window ? w.q.ctx + w.t.t0 + w.t.nt - a.window : 0;        // .. from here
+        bool bad_span = false;
+        float slope = 0.f;
+        if constexpr (SCORED) {
+            const RowSpan f = row_span(a, w.q, w.t.t0), z = row_span(a, w.q, w.t.t0 + w.t.nt - 1);
+            const RowSpan mine = row_span(a, w.q, w.t.t0 + min(r >> a.group_shift, w.t.nt - 1));
+            all_hi = f.hi;
+            all_lo = z.lo;
+            lo_pos = mine.lo;
+            hi_pos = mine.hi;
+            bad_span = span_is_bad(mine, f, z);
+            if (a.slopes) slope = a.slopes[(w.h << a.group_shift) + (r & (a.group - 1))] * kLog2e;
+        }
         const int rows_here = (w.t.nt << a.group_shift) - rank * kCtaRows;              // valid rows of this CTA
         const bool idle = (warp & 3) * 32 >= rows_here;                                  // none of this warp's rows exists
         for (int k = 0; k < w.L; ++k) {
@@ -711,7 +731,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             wait_block(blocks + k);
             if (kFp8 && k == 0) {
                 const uint32_t ex = smem[kQexpOff + (seg & 3) * kCtaRows + row];
-                scale = fmaxf(__uint_as_float(ex << 23) * fabsf(a.k_scale[w.h] * kQScale), 1e-37f);
+                scale = fmaxf(__uint_as_float(ex << 23) * fabsf(a.k_scale[w.h] * (SCORED ? a.qscale : kQScale)), 1e-37f);
             }
             if (!idle) {
                 tc_fence_after();
@@ -719,6 +739,21 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 tmem_ld32(buf + half * 64, *reinterpret_cast<float(*)[32]>(s));
                 tmem_ld32(buf + half * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
                 const int key0 = w.key0(k) + half * 64;
+                float unit = scale;   // of s in log2 units
+                if constexpr (SCORED) {
+                    if (a.cap != 0.f) {
+                        const float z = scale * a.two_over_cap;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) s[i] = capped(a, s[i] * z);
+                        unit = 1.f;
+                    }
+                    if (a.slopes) {
+                        const float far = (float)(key0 - pos);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) s[i] = fmaf(-slope, fabsf(far + (float)i), s[i] * unit);
+                        unit = 1.f;
+                    }
+                }
                 if (key0 < all_lo || key0 + 63 > all_hi) {
                     const int from = lo_pos - key0, to = hi_pos - key0;
 #pragma unroll
@@ -732,7 +767,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 x[half * kCtaRows + row] = top;
                 pair_sync();
                 top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
-                top *= scale;
+                top *= unit;
                 float alpha = 1.f;
                 if (top > m + kRescale) {   // also a row's first key: m = -inf
                     alpha = fast_exp2(m - top);   // m = -inf: 0
@@ -757,7 +792,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float p0 = fast_exp2(fmaf(s[2 * i], scale, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], scale, -ref));
+                    const float p0 = fast_exp2(fmaf(s[2 * i], unit, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], unit, -ref));
                     sum[i & 1] += p0;
                     sum[2 + (i & 1)] += p1;
                     pw[i] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
@@ -792,6 +827,10 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     if (whole) {
                         float lse;
                         f = row_factor(a, orow, head, ml_m, l, vscale, &lse);
+                        if (SCORED && bad_span) {
+                            f = lse = __int_as_float(0x7FC00000);
+                            atomicOr(err, HD_DEVERR_SPAN);
+                        }
                         if (half == 0) a.lse[orow] = lse;
                     } else if (half == 0) {
                         a.part_ml[prow] = make_float2(ml_m, l);
@@ -877,7 +916,12 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                                 mm = top;
                             }
                             float lse;
-                            xm[kCtaRows + row] = row_factor(a, orow, head, mm, ll, vscale, &lse);
+                            float ff = row_factor(a, orow, head, mm, ll, vscale, &lse);
+                            if (SCORED && bad_span) {
+                                ff = lse = __int_as_float(0x7FC00000);
+                                atomicOr(err, HD_DEVERR_SPAN);
+                            }
+                            xm[kCtaRows + row] = ff;
                             xm[row] = mm;
                             a.lse[orow] = lse;
                         }
@@ -943,13 +987,13 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     }
 }
 
-template <int KV>
+template <int KV, bool SCORED>
 cudaError_t chunk_setup(int *pairs) {
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> limit[64];
     int dev = 0;
     if (!done_on_device(done, &dev)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
+        cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<KV, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute at[1];
@@ -961,7 +1005,7 @@ cudaError_t chunk_setup(int *pairs) {
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, paged_chunk_kernel<KV>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, paged_chunk_kernel<KV, SCORED>, &cfg);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) limit[dev].store(n, std::memory_order_relaxed);
         *pairs = n;
@@ -972,14 +1016,14 @@ cudaError_t chunk_setup(int *pairs) {
     return cudaSuccess;
 }
 
-template <int KV>
+template <int KV, bool SCORED>
 cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStream_t s) {
     int pairs = 0;
-    cudaError_t e = chunk_setup<KV>(&pairs);
+    cudaError_t e = chunk_setup<KV, SCORED>(&pairs);
     if (e != cudaSuccess) return e;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    return launch_overlapping(paged_chunk_kernel<KV>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
+    return launch_overlapping(paged_chunk_kernel<KV, SCORED>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
 }
 
 }  // namespace
@@ -987,7 +1031,8 @@ cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStre
 cudaError_t launch_paged_chunk(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
                                const PagedAttnArgs &a, cudaStream_t s) {
     ChunkMaps maps{*qmap, *kmap, *vmap};
-    return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8>(maps, a, s) : launch_chunk<KV_BF16>(maps, a, s);
+    if (a.scored) return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8, true>(maps, a, s) : launch_chunk<KV_BF16, true>(maps, a, s);
+    return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8, false>(maps, a, s) : launch_chunk<KV_BF16, false>(maps, a, s);
 }
 
 }  // namespace hd

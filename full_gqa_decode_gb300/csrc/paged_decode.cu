@@ -78,11 +78,12 @@ __device__ __forceinline__ int tile_tokens(const PagedAttnArgs &a) {
     return SPARSE ? 1 : kDecodeRows >> a.group_shift;
 }
 
-template <int KV, bool SPARSE>
+template <int KV, bool SPARSE, bool SCORED>
 __device__ __forceinline__ Tile make_tile(const PagedAttnArgs &a, const SeqSpan &q, int tile) {
     constexpr int kShift = stage_shift(KV), kKeys = 1 << kShift;
-    Tile t;
     const int tt = tile_tokens<KV, SPARSE>(a);
+    if constexpr (SCORED) return scored_tile<Tile>(a, q, tile * tt, min(tt, q.n - tile * tt), kShift);
+    Tile t;
     t.t0 = tile * tt;
     t.nt = min(tt, q.n - t.t0);
     t.hi = q.ctx + t.t0 + t.nt;
@@ -149,11 +150,13 @@ __device__ __forceinline__ size_t query_row(const PagedAttnArgs &a, const SeqSpa
 
 // What both cache types share: the softmax on S^T fragments (register r of
 // lane (gid, t4): key gid + 8 (r / 2), row 2 t4 + r % 2), and the rows' state.
-template <bool F16>
+template <bool F16, bool SCORED>
 struct DecodeRowsState {
     static constexpr float kLift = F16 ? 15.f : 0.f;
     float o[16][4];            // O^T: dims (two of tile mt) x rows 2 t4 (+ 1)
     float m_run[2], l_run[2];  // rows 2 t4 + e; l_run: this lane's keys
+    RowSpan span[SCORED ? 2 : 1];     // their visible positions ..
+    float slope[SCORED ? 2 : 1];      // .. and biases of a position's distance, log2 units
 
     __device__ void init_rows() {
 #pragma unroll
@@ -166,6 +169,16 @@ struct DecodeRowsState {
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[mt][j] = 0.f;
     }
+    __device__ __forceinline__ void init_rule(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int lane) {
+        if constexpr (SCORED) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * (lane & 3) + e;
+                span[e] = row_span(a, q, t.t0 + min(r >> a.group_shift, t.nt - 1));
+                slope[e] = a.slopes ? a.slopes[(h << a.group_shift) + (r & (a.group - 1))] * kLog2e : 0.f;
+            }
+        }
+    }
     // Scores (times scale[e], log2 units) to weights; returns the two P^T operands: keys 2 t4 (+ 1) and 8 + 2 t4
     // (+ 1) of row gid; bf16: and those of the weights' low parts.
     __device__ __forceinline__ void weigh(const PagedAttnArgs &a, const float (&s)[4], const float (&scale)[2], int key0,
@@ -174,14 +187,25 @@ struct DecodeRowsState {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             bool v0 = true, v1 = true;
+            const int k0 = key0 + (lane >> 2), pos = first + ((2 * (lane & 3) + e) >> a.group_shift);
             if (!full) {   // first: position of the tile's first row
-                const int k0 = key0 + (lane >> 2), hi = first + ((2 * (lane & 3) + e) >> a.group_shift);
-                const int lo = a.window ? hi - a.window + 1 : 0;
+                const int hi = SCORED ? span[e].hi : pos;
+                const int lo = SCORED ? span[e].lo : a.window ? hi - a.window + 1 : 0;
                 v0 = k0 >= lo && k0 <= hi;
                 v1 = k0 + 8 >= lo && k0 + 8 <= hi;
             }
-            const float x0 = v0 ? s[e] * scale[e] : -INFINITY;
-            const float x1 = v1 ? s[2 + e] * scale[e] : -INFINITY;
+            float x0 = s[e] * scale[e], x1 = s[2 + e] * scale[e];
+            if constexpr (SCORED) {
+                if (a.cap != 0.f) {
+                    x0 = capped(a, x0 * a.two_over_cap);
+                    x1 = capped(a, x1 * a.two_over_cap);
+                }
+                const float far = (float)(k0 - pos);
+                x0 = fmaf(-slope[e], fabsf(far), x0);
+                x1 = fmaf(-slope[e], fabsf(far + 8.f), x1);
+            }
+            x0 = v0 ? x0 : -INFINITY;
+            x1 = v1 ? x1 : -INFINITY;
             float mx = fmaxf(x0, x1);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -235,7 +259,10 @@ struct DecodeRowsState {
 };
 
 // bf16 pages.  O^T tile mt: dims 16 mt + gid (+ 8).
-struct DecodeBf16 : DecodeRowsState<false> {
+template <bool SCORED>
+struct DecodeBf16 : DecodeRowsState<false, SCORED> {
+    using Rows = DecodeRowsState<false, SCORED>;
+    using Rows::o;
     uint32_t qb[16][2];
     float scale[2];
 
@@ -248,8 +275,9 @@ struct DecodeBf16 : DecodeRowsState<false> {
             qb[ks][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks)) : 0u;
             qb[ks][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 8)) : 0u;
         }
-        scale[0] = scale[1] = kQScale;
-        init_rows();
+        scale[0] = scale[1] = SCORED ? a.qscale : kQScale;
+        Rows::init_rows();
+        Rows::init_rule(a, q, t, h, lane);
     }
 
     __device__ void consume(const PagedAttnArgs &a, const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col,
@@ -268,11 +296,11 @@ struct DecodeBf16 : DecodeRowsState<false> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
         uint32_t pb[4], m01, m89;
-        weigh(a, s, scale, key0, first, full, lane, pb);
+        Rows::weigh(a, s, scale, key0, first, full, lane, pb);
         if (full) {   // the masks fold away
             products(vst, base, col, lane, pb, 0xFFFFFFFFu, 0xFFFFFFFFu);
         } else {
-            value_masks(key0, vlo, vhi, lane, m01, m89);
+            Rows::value_masks(key0, vlo, vhi, lane, m01, m89);
             products(vst, base, col, lane, pb, m01, m89);
         }
     }
@@ -311,7 +339,10 @@ struct DecodeBf16 : DecodeRowsState<false> {
 // different chunks); q's columns are held in the same order of dims, which
 // leaves every dot product as it is.  O^T tile mt: dims 128 (mt / 8) + 16 gid +
 // 2 (mt % 8) (+ 1).
-struct DecodeE4m3 : DecodeRowsState<true> {
+template <bool SCORED>
+struct DecodeE4m3 : DecodeRowsState<true, SCORED> {
+    using Rows = DecodeRowsState<true, SCORED>;
+    using Rows::o;
     uint32_t qb[16][2];
     float scale[2];
 
@@ -342,8 +373,9 @@ struct DecodeE4m3 : DecodeRowsState<true> {
             for (int j = 0; j < 2; ++j)
                 qb[i][j] = pack_f16(__uint_as_float(qb[i][j] << 16) * down, __uint_as_float(qb[i][j] & 0xFFFF0000u) * down);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) scale[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * kQScale);
-        init_rows();
+        for (int e = 0; e < 2; ++e) scale[e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e)) * (a.k_scale[h] * (SCORED ? a.qscale : kQScale));
+        Rows::init_rows();
+        Rows::init_rule(a, q, t, h, lane);
     }
 
     __device__ void consume(const PagedAttnArgs &a, const uint8_t *kst, const uint8_t *vst, uint32_t base, uint32_t col,
@@ -367,11 +399,11 @@ struct DecodeE4m3 : DecodeRowsState<true> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
         uint32_t pb[2], m01, m89;
-        weigh(a, s, scale, key0, first, full, lane, pb);
+        Rows::weigh(a, s, scale, key0, first, full, lane, pb);
         if (full) {   // the masks fold away
             products(vst, base, col, lane, pb, 0xFFFFFFFFu, 0xFFFFFFFFu);
         } else {
-            value_masks(key0, vlo, vhi, lane, m01, m89);
+            Rows::value_masks(key0, vlo, vhi, lane, m01, m89);
             products(vst, base, col, lane, pb, m01, m89);
         }
     }
@@ -413,18 +445,26 @@ struct DecodeE4m3 : DecodeRowsState<true> {
     }
 };
 
-template <int KV> struct DecodeConsumer;
-template <> struct DecodeConsumer<KV_BF16> { using T = DecodeBf16; };
-template <> struct DecodeConsumer<KV_FP8> { using T = DecodeE4m3; };
+template <int KV, bool SCORED> struct DecodeConsumer;
+template <bool SCORED> struct DecodeConsumer<KV_BF16, SCORED> { using T = DecodeBf16<SCORED>; };
+template <bool SCORED> struct DecodeConsumer<KV_FP8, SCORED> { using T = DecodeE4m3<SCORED>; };
 
 // Writes row r of a finished tile (thread's four dims d..d+3 of its
 // unnormalised output, log2-unit maximum m and sum l).
+template <bool SCORED>
 __device__ __forceinline__ void finish_row(const PagedAttnArgs &a, const SeqSpan &q, const Tile &t, int h, int r, int d,
                                            float4 v, float m, float l, float vscale) {
     const int head = (h << a.group_shift) + (r & (a.group - 1));
     const size_t row = query_row(a, q, t, h, r);
     float lse;
-    const float f = row_factor(a, row, head, m, l, vscale, &lse);
+    float f = row_factor(a, row, head, m, l, vscale, &lse);
+    if constexpr (SCORED) {
+        if ((a.first || a.last) && span_is_bad(row_span(a, q, t.t0 + (r >> a.group_shift)), row_span(a, q, t.t0),
+                                               row_span(a, q, t.t0 + t.nt - 1))) {
+            f = lse = __int_as_float(0x7FC00000);
+            if (d == 0) atomicOr(a.seqs.err, HD_DEVERR_SPAN);
+        }
+    }
     uint2 w;
     w.x = pack_bf16(v.x * f, v.y * f);
     w.y = pack_bf16(v.z * f, v.w * f);
@@ -432,7 +472,7 @@ __device__ __forceinline__ void finish_row(const PagedAttnArgs &a, const SeqSpan
     if (d == 0) a.lse[row] = lse;
 }
 
-template <int KV, bool SPARSE>
+template <int KV, bool SPARSE, bool SCORED>
 __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ PagedAttnArgs a) {
@@ -463,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         sq, a.num_kv_heads, cta, gridDim.x, min_units(KV),
         (SPARSE ? sq.num_tokens : sq.batch) * a.num_kv_heads, kSnap, kSnap, reinterpret_cast<long long *>(buf), misc, &x0, &x1, &T, &n, &bad,
         [&](int tokens) { return num_tiles<KV, SPARSE>(a, tokens); },
-        [&](const SeqSpan &q, int i) { return make_tile<KV, SPARSE>(a, q, i).units; });
+        [&](const SeqSpan &q, int i) { return make_tile<KV, SPARSE, SCORED>(a, q, i).units; });
     if (bad) fill_bad_rows(a, cta, gridDim.x);
     if (x0 >= x1) return;
     // Behind the barrier a share is counted in stages done; what only cut items need waits in shared memory.
@@ -478,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     Cursor c{c0.b, c0.tile, c0.h, c0.off};
     int bit;
     SeqSpan q = seq_span(sq, c.b, &bit);
-    if (c.off == make_tile<KV, SPARSE>(a, q, c.tile).units) next_item<KV, SPARSE>(a, c, q);   // a border moved to its item's end
+    if (c.off == make_tile<KV, SPARSE, SCORED>(a, q, c.tile).units) next_item<KV, SPARSE>(a, c, q);   // a border moved to its item's end
     const int ps = 1 << sq.page_shift;
     const int box_shift = min(sq.page_shift, kShift), box_rows = 1 << box_shift;
     constexpr int kRowBytes = kHeadDim * kv_elem_bytes(KV);
@@ -492,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
         bool dead = false;
         int issued = 0, copied = 0;   // stages; those whose copies were issued, the first so many
         while (x < share) {
-            const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
+            const Tile t = make_tile<KV, SPARSE, SCORED>(a, q, c.tile);
             const int seg = min(t.units - c.off, share - x);
             const int32_t *row = sq.table + (size_t)c.b * sq.table_stride;
             const int32_t *sel = SPARSE ? a.selected + ((size_t)(q.row0 + t.t0) * a.num_kv_heads + c.h) * a.num_selected : nullptr;
@@ -553,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     // ---- consumers ----
     constexpr int kTeam = team_warps(KV), kTeams = kWarps / kTeam;
     static_assert(kFulls % kTeams == 0, "a barrier serves one team");
-    typename DecodeConsumer<KV>::T cons;
+    typename DecodeConsumer<KV, SCORED>::T cons;
     const int team = warp / kTeam;
     const int r0 = (warp % kTeam) * kWarpKeys;   // this warp's key rows of a stage
     const uint32_t base = (uint32_t)(r0 >> box_shift) * (box_rows * kRowBytes) + (r0 & (box_rows - 1)) * 128;
@@ -564,19 +604,24 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     int u = team;              // .. and its number from the segment's first stage
     bool dead = false;
     while (x < share) {
-        const Tile t = make_tile<KV, SPARSE>(a, q, c.tile);
+        const Tile t = make_tile<KV, SPARSE, SCORED>(a, q, c.tile);
         const int seg = min(t.units - c.off, share - x);
         cons.init(a, q, t, c.h, lane);
         if (warp == 0 && x + seg < share) {   // the next item's query rows into L2
             Cursor nc = c;
             SeqSpan nq = q;
             next_item<KV, SPARSE>(a, nc, nq);
-            const Tile nt = make_tile<KV, SPARSE>(a, nq, nc.tile);
+            const Tile nt = make_tile<KV, SPARSE, SCORED>(a, nq, nc.tile);
             for (int i = lane; i < (nt.nt << a.group_shift) * 4; i += 32)   // 128-byte lines
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + query_row(a, nq, nt, nc.h, i >> 2) * kHeadDim + (i & 3) * 64));
         }
-        const int all_hi = q.ctx + t.t0;                                        // every row sees up to here ..
-        const int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;      // .. from here
+        const int pos0 = q.ctx + t.t0;
+        int all_hi = pos0;                                              // every row sees up to here ..
+        int all_lo = a.window ? q.ctx + t.t0 + t.nt - a.window : 0;    // .. from here
+        if constexpr (SCORED) {
+            all_hi = row_span(a, q, t.t0).hi;
+            all_lo = row_span(a, q, t.t0 + t.nt - 1).lo;
+        }
         for (; u < seg; u += kTeams) {
             const int st = fb < kRing ? fb : fb - kRing;
             if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[fb], ph))) {
@@ -588,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
             if (!dead && key0 < t.hi && key0 + kWarpKeys > t.lo) {
                 const uint8_t *stage = smem + st * kStageBytes;
                 const bool whole = key0 >= all_lo && key0 + kWarpKeys - 1 <= all_hi;
-                cons.consume(a, stage, stage + kHalf, base, col, key0, t.lo, t.hi, all_hi, whole, lane);
+                cons.consume(a, stage, stage + kHalf, base, col, key0, t.lo, t.hi, pos0, whole, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -644,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                 v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
             }
             if (whole_item) {
-                finish_row(a, q, t, c.h, r, d, v, mfin[r], mfin[kDecodeRows + r], vscale);
+                finish_row<SCORED>(a, q, t, c.h, r, d, v, mfin[r], mfin[kDecodeRows + r], vscale);
             } else {
                 *reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kDecodeRows + r) * kHeadDim + d) = v;
                 if (d == 0) a.part_ml[(size_t)slot * kDecodeRows + r] = make_float2(mfin[r], mfin[kDecodeRows + r]);
@@ -695,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
                             v.w = fmaf(w, p[k].w, v.w);
                         }
                     }
-                    finish_row(a, q, t, c.h, r, d, v, m, l, vscale);
+                    finish_row<SCORED>(a, q, t, c.h, r, d, v, m, l, vscale);
                 }
                 if (tid == 0) a.tickets[i0] = 0;
             }
@@ -706,17 +751,17 @@ __global__ void __launch_bounds__(kThreads, kDecodeCtasPerSm)
     }
 }
 
-template <int KV, bool SPARSE>
+template <int KV, bool SPARSE, bool SCORED>
 cudaError_t launch(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (!done_on_device(done, &dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<KV, SPARSE>,
+        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<KV, SPARSE, SCORED>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
         mark_done_on_device(done, dev);
     }
-    return launch_overlapping(paged_decode_kernel<KV, SPARSE>, dim3(kDecodeCtasPerSm * num_sms), kThreads, kSmemBytes, 1, s,
+    return launch_overlapping(paged_decode_kernel<KV, SPARSE, SCORED>, dim3(kDecodeCtasPerSm * num_sms), kThreads, kSmemBytes, 1, s,
                               *kmap, *vmap, a);
 }
 
@@ -724,10 +769,14 @@ cudaError_t launch(const CUtensorMap *kmap, const CUtensorMap *vmap, const Paged
 
 cudaError_t launch_paged_decode(const CUtensorMap *kmap, const CUtensorMap *vmap, const PagedAttnArgs &a, int num_sms,
                                 cudaStream_t s) {
-    const bool sparse = a.selected != nullptr;
+    const bool sparse = a.selected != nullptr, scored = a.scored != 0;   // a rule and a choice of blocks do not meet
     if (a.kv_type == KV_FP8)
-        return sparse ? launch<KV_FP8, true>(kmap, vmap, a, num_sms, s) : launch<KV_FP8, false>(kmap, vmap, a, num_sms, s);
-    return sparse ? launch<KV_BF16, true>(kmap, vmap, a, num_sms, s) : launch<KV_BF16, false>(kmap, vmap, a, num_sms, s);
+        return sparse   ? launch<KV_FP8, true, false>(kmap, vmap, a, num_sms, s)
+               : scored ? launch<KV_FP8, false, true>(kmap, vmap, a, num_sms, s)
+                        : launch<KV_FP8, false, false>(kmap, vmap, a, num_sms, s);
+    return sparse   ? launch<KV_BF16, true, false>(kmap, vmap, a, num_sms, s)
+           : scored ? launch<KV_BF16, false, true>(kmap, vmap, a, num_sms, s)
+                    : launch<KV_BF16, false, false>(kmap, vmap, a, num_sms, s);
 }
 
 }  // namespace hd

@@ -21,6 +21,54 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
 __device__ __forceinline__ float part_weight(float x, float m) { return x == -INFINITY ? 0.f : fast_exp2(x - m); }
 
 
+// ---- attn_paged_scored ----
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// cap tanh(x / cap) of a score: with e = exp(2 x / cap) it is cap - 2 cap / (1 + e), which keeps an absolute error below
+// 2^-21 cap (the roundings of 2^x, of 1 + e, of its reciprocal and of the last step; the first counts at most half, as
+// the slope 2 e / (1 + e)^2 is).  e overflows to infinity and underflows to 0 where tanh is 1 and -1.
+// `z`: x times 2 log2(e) / cap; all else in log2 units.
+__device__ __forceinline__ float capped(const PagedAttnArgs &a, float z) {
+    return fmaf(-2.f * a.cap, fast_rcp(1.f + fast_exp2(z)), a.cap);
+}
+
+// Visible positions [lo, hi] of token i of a sequence; none when hi < lo.
+struct RowSpan {
+    int lo, hi;
+};
+__device__ __forceinline__ RowSpan row_span(const PagedAttnArgs &a, const SeqSpan &q, int i) {
+    const int p = q.ctx + i, r = q.row0 + i;
+    RowSpan s{a.window ? max(0, p - a.window + 1) : 0, p};
+    if (a.first) s.lo = max(s.lo, a.first[r]);
+    if (a.last) s.hi = max(min(a.last[r], q.ctx + q.n - 1), -1);
+    return s;
+}
+// A tile of tokens t0 .. t0 + nt - 1: as both ends of the rows' spans ascend, its first row's lo and its last row's hi hold
+// what any of its rows sees.  A tile that sees nothing has one unit outside every page's range, for its rows' zeros.
+template <class T>
+__device__ __forceinline__ T scored_tile(const PagedAttnArgs &a, const SeqSpan &q, int t0, int nt, int shift) {
+    T t;
+    t.t0 = t0;
+    t.nt = nt;
+    t.lo = row_span(a, q, t0).lo;
+    t.hi = row_span(a, q, t0 + nt - 1).hi + 1;
+    t.u0 = t.lo >> shift;
+    t.units = ((t.hi + (1 << shift) - 1) >> shift) - t.u0;
+    if (t.hi <= t.lo) {
+        t.lo = 0x3FFFFFFF;
+        t.hi = t.u0 = 0;
+        t.units = 1;
+    }
+    return t;
+}
+// Whether row s of a tile whose first and last rows are f and l breaks the ascent (its keys may then lie outside the tile).
+__device__ __forceinline__ bool span_is_bad(const RowSpan &s, const RowSpan &f, const RowSpan &l) {
+    return s.lo < f.lo || s.lo > l.lo || s.hi < f.hi || s.hi > l.hi;
+}
+
 // What a row's unnormalised output is multiplied by -- 1 / l, the E4M3 value
 // scale, the sink's share and the gate -- and its lse, from its log2-unit
 // maximum m and sum l.  A row that sees no key gives 0 and lse -inf; NaN scores

@@ -109,7 +109,8 @@ enum {
     HD_DEVERR_WAIT_TIMEOUT = 8,      /* a pipeline wait gave up after its time limit        */
     HD_DEVERR_TOKEN_OFFSETS = 16,    /* paged: a sequence's token_offsets are no row range, or
                                       * name more than max_tokens rows                      */
-    HD_DEVERR_PAGE = 32              /* paged: a needed block's page is not in the pool      */
+    HD_DEVERR_PAGE = 32,             /* paged: a needed block's page is not in the pool      */
+    HD_DEVERR_SPAN = 64              /* paged: first / last of hd_scoring do not ascend      */
 };
 
 typedef struct hd_ctx hd_ctx;
@@ -564,6 +565,136 @@ hd_status select_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, 
 hd_status attn_selected_pages(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const void *q_rot,
                               const hd_paged_cache *cache, const int32_t *selected, int32_t num_selected,
                               const float *sink, const float *gate, void *out, float *lse, void *stream);
+
+/* ------------------------------------------- paged caches: entries and scores --
+ *
+ * The same pools and batches for models that norm the heads of their queries and
+ * keys, turn them by other angles, or score them in other ways.  Everything said
+ * above for paged calls (workspace, streams, capture, bad values on the device)
+ * holds here too. */
+
+/* Which dims of a head turn together: dim i with dim i + rotary_dim / 2, or the
+ * neighbours 2 i and 2 i + 1; pair i by the same angle in both. */
+typedef enum { HD_ROPE_HALVES = 0, HD_ROPE_NEIGHBOURS = 1 } hd_rope_layout;
+
+/* How the angles of contexts beyond the trained one are scaled.  Pair i's
+ * frequency, in radians a position, is f_i = theta^(-2 i / rotary_dim) and
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   RAMP    f_i (1 - r_i) + f_i / factor r_i with a ramp over the pairs' numbers,
+ *           r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *           lo = max(floor(n(fast)), 0), hi = min(ceil(n(slow)), rotary_dim - 1),
+ *           n(t) = rotary_dim ln(original_context / (2 pi t)) / (2 ln theta):
+ *           the pair that turns t times over the original context
+ *   BANDS   f_i k_i + f_i / factor (1 - k_i) with a ramp over the turns,
+ *           k_i = clamp((original_context f_i / (2 pi) - slow) / (fast - slow), 0, 1)
+ * Cosines and sines are multiplied by amplitude; 0 stands for 0.1 ln(factor) + 1
+ * with RAMP (factor >= 1) and for 1 with the others. */
+typedef enum { HD_ROPE_PLAIN = 0, HD_ROPE_LINEAR = 1, HD_ROPE_RAMP = 2, HD_ROPE_BANDS = 3 } hd_rope_scaling;
+
+typedef struct {
+    int32_t rotary_dim;        /* 8 .. head_dim, a multiple of 8                                  */
+    int32_t scaling;           /* hd_rope_scaling                                                 */
+    double theta;              /* above 1                                                         */
+    double factor;             /* not PLAIN: positive                                             */
+    double original_context;   /* RAMP, BANDS: positions trained on, positive                     */
+    double slow, fast;         /* RAMP, BANDS: turns over them, 0 < slow < fast                   */
+    double amplitude;          /* positive, or 0                                                  */
+} hd_rope_params;
+
+/* Frequencies [rotary_dim / 2] and amplitude of a set of parameters (pure host function). */
+hd_status hd_rope_frequencies(const hd_rope_params *params, double *frequencies, double *amplitude);
+
+/* Fills a table of angles, device fp32 [positions][rotary_dim / 2][2], 16-byte
+ * aligned, with amplitude * (cos, sin) of position * frequency, evaluated in fp64
+ * and rounded once: laid out once for a model.  Needs no context; runs on the
+ * current device. */
+hd_status hd_rope_fill(const hd_rope_params *params, int32_t positions, float *table, void *stream);
+
+/* A table of angles as hd_rope_fill writes it (or the caller's own of that layout). */
+typedef struct {
+    const float *table;
+    int32_t positions;         /* rows                                                            */
+    int32_t rotary_dim;        /* 8 .. head_dim, a multiple of 8                                  */
+    int32_t layout;            /* hd_rope_layout                                                  */
+} hd_rope_table;
+
+/* Norm of every head of the queries and keys: y = x / sqrt(mean(x^2) + eps) times
+ * (offset + weight), the mean over the head's head_dim dims; squares are summed
+ * in fp32, so heads whose largest value passes 2^60 are not served.  q_weight /
+ * k_weight: device bf16 or fp32 (f32_weights) [head_dim], or one row a head
+ * (per_head: [num_q_heads][head_dim] and [num_kv_heads][head_dim]), 16-byte
+ * aligned; NULL: that factor is 1. */
+typedef struct {
+    const void *q_weight;
+    const void *k_weight;
+    int32_t f32_weights;
+    int32_t per_head;
+    float offset;              /* finite                                                          */
+    float eps;                 /* positive                                                        */
+} hd_head_norm;
+
+/* rope_append_paged for such models: norms the new queries and keys per head, then
+ * rotates them by `rope`'s angles, in one pass, and stores keys and values in
+ * their pages with the pages' bounds.  Norm and rotation are evaluated in fp32 and
+ * rounded once, to bf16 or to E4M3 of the product with the scale's reciprocal;
+ * values are stored as rope_append_paged stores them, bit for bit.
+ *   norm       NULL: none (rotation alone)
+ *   rope       NULL: the context's own angles of the layer's type, in halves
+ *   positions  device [num_tokens], the position whose angles a row takes (packed
+ *              documents); NULL: its position in the sequence, and the table must
+ *              hold those (a sequence that reaches past the table is a sequence
+ *              that cannot be served).  A given position outside the table is
+ *              flagged (HD_DEVERR_CONTEXT_PLAN), and its row's entry and q_rot
+ *              stay as they were.
+ * The other arguments and errors are rope_append_paged's; HD_ERR_INVALID_ARG for
+ * a norm or table outside the limits given at their structs. */
+hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const hd_head_norm *norm,
+                                 const hd_rope_table *rope, const int32_t *positions, const void *q, int64_t q_stride,
+                                 const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_rot,
+                                 const hd_paged_cache *cache, void *stream);
+
+/* What a query scores and sees beyond attn_paged's rule.  With x = scale * q . k
+ * for a query at position p (of its sequence) and a key at position j:
+ *   softcap    x becomes softcap * tanh(x / softcap), to an absolute error of
+ *              2^-20 softcap; 0: no cap.  1/1024 to 1024, HD_ERR_UNSUPPORTED beyond
+ *   slopes     then slopes[h] * |p - j| is taken off for query head h: device fp32
+ *              [num_q_heads], finite, or NULL
+ *   first,     the visible positions of row r, first[r] .. last[r]: device
+ *   last       [num_tokens] each, or NULL (0; p).  A sliding layer's window starts
+ *              them at p - window + 1 at the earliest; they end with the
+ *              sequence's last new token at the latest.  Documents packed into a
+ *              sequence: first is the start of a row's document.  A prefix (or a
+ *              block) whose tokens see each other: last is its last position.  A
+ *              row may see nothing: out 0, lse -inf.  Both ascend (not strictly)
+ *              along a sequence's rows; a row that is found not to is flagged
+ *              (HD_DEVERR_SPAN) and gets NaN, or is served by its own values.
+ *   scale      0: 1 / sqrt(head_dim); else positive and finite
+ * Entries from a sequence's lowest to its highest visible position must be finite. */
+typedef struct {
+    float scale;
+    float softcap;
+    const float *slopes;
+    const int32_t *first;
+    const int32_t *last;
+} hd_scoring;
+
+/* attn_paged by such a rule (NULL: attn_paged's own).  lse is of the scores that
+ * the rule gives. */
+hd_status attn_paged_scored(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const hd_scoring *scoring,
+                            const void *q_rot, const hd_paged_cache *cache, const float *sink, const float *gate,
+                            void *out, float *lse, void *stream);
+
+/* Reads entries back: row r of k / v gets the entry at position context[b] + t of
+ * its sequence, t = r - token_offsets[b] -- batch's "new" tokens are here the
+ * positions to read -- in bf16: bit for bit, or an E4M3 code's value times the
+ * scale, rounded once.  Keys come as they are stored, rotated.
+ *   k, v   bf16 [num_tokens][num_kv_heads][head_dim], rows k_stride / v_stride
+ *          elements apart (multiples of 8), 16-byte aligned; either may be NULL
+ * A page outside the pool reads as zeros and is flagged; rows of a sequence that
+ * cannot be served get NaN. */
+hd_status read_paged(hd_ctx *ctx, const hd_paged_batch *batch, const hd_paged_cache *cache, void *k, int64_t k_stride,
+                     void *v, int64_t v_stride, void *stream);
 
 /* Measurement utility (no counterpart in the pages): one pass of a pure read
  * stream over `bytes` of the device buffer (16-byte aligned), through shared
