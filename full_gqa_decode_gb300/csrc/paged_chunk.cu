@@ -40,6 +40,7 @@
 // of P through a second product, as the decode kernel takes them, would cost a
 // product in two again: 4096 tokens behind 28672 905 us against 657 in the same run.
 #include <climits>
+#include <type_traits>
 
 #include "paged_rows.cuh"
 
@@ -48,12 +49,12 @@ namespace {
 
 constexpr int kTileRows = kChunkRows, kCtaRows = kTileRows / 2, kTileKeys = kChunkKeys, kKeyShift = 7;
 constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-// Stage warps: one behind the MMA warp (bf16); two groups of four, for K and for V operands, at the next multiple of
+// Stage warps, for K and for V operands: one each behind the MMA warp (bf16); two groups of four at the next multiple of
 // four warps (E4M3).  kStage: those that hand on one operand.
 __host__ __device__ constexpr int first_stage_warp(int kv) { return kv == KV_FP8 ? kSoftWarps + 4 : kSoftWarps + 2; }
 __host__ __device__ constexpr int stage_warps(int kv) { return kv == KV_FP8 ? 4 : 1; }
 __host__ __device__ constexpr int chunk_threads(int kv) {
-    return (first_stage_warp(kv) + (kv == KV_FP8 ? 2 : 1) * stage_warps(kv)) * 32;
+    return (first_stage_warp(kv) + 2 * stage_warps(kv)) * 32;
 }
 // E4M3: 640 threads launch with 96 registers each; the groups of four warps then share them out by need.
 // 256 x 128 + 128 x 56 + 256 x 80 <= 640 x 96.
@@ -80,6 +81,10 @@ constexpr int kItemCost = 2;
 constexpr int kSnap = 16, kSnapFew = 12, kFewRows = 64;
 constexpr int kMinTiles = 2 + kItemCost;              // shortest share of a pair
 constexpr float kRescale = 8.f;
+// Scored rows over bf16 pages let a score pass the reference by 32: bf16 weights have fp32's range, so 2^32 a weight costs
+// nothing but range of the sums (values up to 2^78 for 2^17 keys).  Capped scores spread over 8 (natural units) passed 8 in
+// most tiles of a warp's rows: 4096 tokens behind 28672 957 us uncapped with 8.
+constexpr float kRescaleWide = 32.f;
 constexpr uint32_t kTmemCols = 512, kOutCol = 256;
 
 // A segment -- a pair's part of an item, L key tiles -- runs in blocks of products: S(0); S(1) ; then O += P(k) V(k)
@@ -183,7 +188,9 @@ struct Segment {
         return settle(a);
     }
     __device__ bool next(const PagedAttnArgs &a) { return advance(a) && settle(a); }
-    __device__ int key0(int k) const { return (t.u0 + u + k) << kKeyShift; }   // first position of its tile k
+    // First position of its tile k.  Scored rows take their keys from the last to the first: where a bias falls with the
+    // distance, the largest scores come first and the reference of the weights hardly moves.
+    __device__ int key0(int k) const { return (t.u0 + u + (SCORED ? L - 1 - k : k)) << kKeyShift; }
 };
 
 // Position in a ring of slots: index and the parity of its current round.
@@ -210,6 +217,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The same for what was done in tensor memory alone: tcgen05.fence::before_thread_sync orders that before any arrival, and a
+// release of everything else, which the softmax would wait for in every tile, is not needed.
+__device__ __forceinline__ void mbar_arrive_remote_tmem(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // The wait's other side may be the peer CTA, which releases at cluster scope; an acquire of the default scope, the
 // CTA's own, would not take in what it wrote.
@@ -284,6 +296,133 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
+}
+// Whether any of the `threads` threads that meet at the named barrier says so.
+__device__ __forceinline__ bool any_of_barrier(int barrier, int threads, bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(y)
+        : "r"((uint32_t)x), "r"(barrier), "r"(threads)
+        : "memory");
+    return y != 0;
+}
+// 64 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,"
+        "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+          "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+          "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+          "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+          "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+
+// A row's part in a tile of scored rows: what its thread does with its 64 scores, 16 at a time in a loop, as the body has to
+// stay small: unrolled over all 64 the rule's 700 instructions were waited for longer than executed (4096 capped tokens
+// behind 28672 949 us).
+struct RulePart {
+    uint32_t cols;      // of the scores
+    float scale;        // of a score, log2 units
+    float slope, far;   // bias of a position's distance, and the first key's position less the query's
+    int from, to;       // visible ones of the 64
+};
+// Scores c .. c + 15 by the rule, less ref.  EDGE: what is not visible gives -inf, and scores may pass what the cap's exponents
+// reach.
+template <bool CAP, bool BIAS, bool EDGE>
+__device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &r, int c, float ref, float (&s)[16]) {
+    tmem_ld16(r.cols + c, s);
+    const int from = r.from - c, to = r.to - c;
+    if (EDGE && CAP) {   // what is not visible may be NaN, which must not reach its neighbours' reciprocal
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = i >= from && i <= to ? s[i] : 0.f;
+    }
+    if (CAP) {
+        const float z = r.scale * a.two_over_cap;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) capped4<EDGE>(a, z, a.cap - ref, *reinterpret_cast<float(*)[4]>(s + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], r.scale, -ref);
+    }
+    if (BIAS) {
+        const float far = r.far + (float)c;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = fmaf(-r.slope, fabsf(far + (float)i), s[i]);
+    }
+    if (EDGE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = i >= from && i <= to ? s[i] : -INFINITY;
+    }
+}
+__device__ __forceinline__ float max16(const float (&s)[16], float top) {
+    float m[4] = {fmaxf(s[0], top), s[1], s[2], s[3]};
+#pragma unroll
+    for (int i = 4; i < 16; ++i) m[i & 3] = fmaxf(m[i & 3], s[i]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+template <bool CAP, bool BIAS, bool EDGE>
+__device__ __forceinline__ float rule_max(const PagedAttnArgs &a, const RulePart &r) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 16) {
+        float s[16];
+        ruled16<CAP, BIAS, EDGE>(a, r, c, 0.f, s);
+        top = max16(s, top);
+    }
+    return top;
+}
+// Largest raw score.
+__device__ __forceinline__ float raw_max(const RulePart &r) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        float s[32];
+        tmem_ld32(r.cols + c, s);
+        top = max16(*reinterpret_cast<const float(*)[16]>(s + 16), max16(*reinterpret_cast<const float(*)[16]>(s), top));
+    }
+    return top;
+}
+// Weights by the reference, in 16 bits in the first half of the part's own columns (each 8 behind scores that have been read);
+// returns their sum.
+template <bool F16, bool CAP, bool BIAS, bool EDGE>
+__device__ __forceinline__ float rule_weights(const PagedAttnArgs &a, const RulePart &r, float ref) {
+    float2 sum[2] = {};
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 16) {
+        float s[16];
+        uint32_t pw[8];
+        ruled16<CAP, BIAS, EDGE>(a, r, c, ref, s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = fast_exp2(s[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i & 1] = add2(sum[i & 1], make_float2(s[2 * i], s[2 * i + 1]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pw[i] = F16 ? pack_f16(s[2 * i], s[2 * i + 1]) : pack_bf16(s[2 * i], s[2 * i + 1]);
+        tmem_st8(r.cols + c / 2, pw);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+// f(cap, bias, edge) with each as a constant.
+template <class F>
+__device__ __forceinline__ float by_rule(bool cap, bool bias, bool edge, F f) {
+    using Y = std::true_type;
+    using N = std::false_type;
+    if (edge) return cap ? (bias ? f(Y{}, Y{}, Y{}) : f(Y{}, N{}, Y{})) : (bias ? f(N{}, Y{}, Y{}) : f(N{}, N{}, Y{}));
+    return cap ? (bias ? f(Y{}, Y{}, N{}) : f(Y{}, N{}, N{})) : (bias ? f(N{}, Y{}, N{}) : f(N{}, N{}, N{}));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Instruction descriptor for M = 256 rows of the pair: fp32 accumulator, bf16 or f16 operands, A K-major.
@@ -501,7 +640,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         if (!dead) {
 #pragma unroll
                             for (int t = 0; t < 8; ++t)
-                                pair_mma_ts(tmem + kOutCol, p + 8 * t, vd + v_step[t], kIdO, i > 2 || t > 0);
+                                pair_mma_ts(tmem + kOutCol, p + 8 * t + (SCORED && t >= 4 ? 32 : 0), vd + v_step[t], kIdO, i > 2 || t > 0);
                         }
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
@@ -659,22 +798,30 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 if (more) load(0);
             }
         }
-    } else if (!kFp8 && warp == kStageWarp) {
+    } else if (!kFp8 && warp >= kStageWarp) {
         // ---- bf16 stages: hand what has landed on to the MMAs ----
+        // An arrival that releases to the cluster takes about 1000 clocks: one warp for all operands was what a tile took (4096
+        // tokens behind 28672 660 us).  Each waits for every operand, so that it sees every phase of a slot, and hands on its own.
         const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
         const int rv_shift = min(sq.page_shift, 7);
         RingPos<kSlots> pos;
         for (uint32_t seg = 0; more; ++seg) {
-            wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(q_ready);
+            if (warp == kStageWarp) {
+                wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(q_ready);
+            }
             for (int i = 0; i <= w.L; ++i) {
 #pragma unroll
                 for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
                     if (kind == 0 ? i >= w.L : i == 0) continue;
                     uint8_t *slot = ring + pos.st * kSlotBytes;
                     wait_warp(&bar[BAR_FULL + pos.st], pos.ph, dead, err);
+                    if (warp - kStageWarp != kind) {
+                        pos.step();
+                        continue;
+                    }
                     const int key0 = w.key0(i - 1);
                     if (kind == 1 && (key0 < w.t.lo || key0 + kTileKeys > w.t.hi)) {
                         // Rows of positions that no query row sees: zero, whatever their slots hold.
@@ -703,6 +850,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
         auto soft_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         const float lift = kFp8 ? 7.f : 0.f;
+        constexpr float kLimit = kFp8 ? kRescale : kRescaleWide;   // scored rows
         int blocks = 0, tiles = 0;   // before this segment
         for (uint32_t seg = 0; more; ++seg) {
         float m = -INFINITY, l = 0.f, scale = SCORED ? a.qscale : kQScale;
@@ -725,6 +873,21 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         }
         const int rows_here = (w.t.nt << a.group_shift) - rank * kCtaRows;              // valid rows of this CTA
         const bool idle = (warp & 3) * 32 >= rows_here;                                  // none of this warp's rows exists
+        auto rescale_output = [&](int k, float alpha) {
+            if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                wait_block(blocks + k + 1);   // O holds tile k - 1
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    float o[32];
+                    uint32_t ow[32];
+                    tmem_ld32(lanes + kOutCol + half * 128 + c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) ow[i] = __float_as_uint(o[i] * alpha);
+                    tmem_st32(lanes + kOutCol + half * 128 + c, ow);
+                }
+            }
+        };
         for (int k = 0; k < w.L; ++k) {
             const int g = tiles + k;
             const uint32_t buf = lanes + (uint32_t)(g & 1) * 128;
@@ -735,75 +898,82 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             }
             if (!idle) {
                 tc_fence_after();
-                float s[64];
-                tmem_ld32(buf + half * 64, *reinterpret_cast<float(*)[32]>(s));
-                tmem_ld32(buf + half * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
                 const int key0 = w.key0(k) + half * 64;
-                float unit = scale;   // of s in log2 units
                 if constexpr (SCORED) {
-                    if (a.cap != 0.f) {
-                        const float z = scale * a.two_over_cap;
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = capped(a, s[i] * z);
-                        unit = 1.f;
+                    const RulePart part{buf + half * 64, scale, slope, (float)(key0 - pos), lo_pos - key0, hi_pos - key0};
+                    const bool cap = a.cap != 0.f, bias = a.slopes != nullptr;
+                    // Tiles that every row sees whole mostly leave the rows' references as they are, which a bound on their scores
+                    // shows: the cap is monotone, and the bias lies between those of the part's ends.
+                    const bool edge = w.key0(k) < all_lo || w.key0(k) + kTileKeys - 1 > all_hi;
+                    bool moves = edge || k == 0, careful = moves;
+                    if (!moves) {
+                        const float raw = raw_max(part), z = raw * (scale * a.two_over_cap);
+                        careful = cap && __any_sync(0xffffffffu, z > kCapReach);
+                        float top = cap ? capped(a, z) : raw * scale;
+                        if (bias)
+                            top = fmaf(-slope, slope > 0.f ? fmaxf(fmaxf(part.far, -63.f - part.far), 0.f)
+                                                           : fmaxf(fabsf(part.far), fabsf(part.far + 63.f)), top);
+                        moves = any_of_barrier(1 + (warp & 3), 64, top > m + kLimit);   // m = -inf: any score
                     }
-                    if (a.slopes) {
-                        const float far = (float)(key0 - pos);
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = fmaf(-slope, fabsf(far + (float)i), s[i] * unit);
-                        unit = 1.f;
+                    if (moves) {
+                        float top = by_rule(cap, bias, careful, [&](auto c, auto b, auto e) { return rule_max<c.value, b.value, e.value>(a, part); });
+                        float *x = xm + (g & 1) * 2 * kCtaRows;
+                        x[half * kCtaRows + row] = top;
+                        pair_sync();
+                        top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
+                        float alpha = 1.f;
+                        if (top > m + kLimit) {
+                            if (m != -INFINITY) alpha = fast_exp2(m - top);   // else nothing to scale: l and the output are zero
+                            m = top;
+                            l *= alpha;
+                        }
+                        rescale_output(k, alpha);
                     }
-                }
-                if (key0 < all_lo || key0 + 63 > all_hi) {
-                    const int from = lo_pos - key0, to = hi_pos - key0;
+                    const float ref = m == -INFINITY ? 0.f : m - lift;
+                    l += by_rule(cap, bias, careful,
+                                 [&](auto c, auto b, auto e) { return rule_weights<kFp8, c.value, b.value, e.value>(a, part, ref); });
+                } else {
+                    float s[64];
+                    tmem_ld64(buf + half * 64, s);
+                    if (key0 < all_lo || key0 + 63 > all_hi) {
+                        const int from = lo_pos - key0, to = hi_pos - key0;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) s[i] = i >= from && i <= to ? s[i] : -INFINITY;
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                float *x = xm + (g & 1) * 2 * kCtaRows;
-                x[half * kCtaRows + row] = top;
-                pair_sync();
-                top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
-                top *= unit;
-                float alpha = 1.f;
-                if (top > m + kRescale) {   // also a row's first key: m = -inf
-                    alpha = fast_exp2(m - top);   // m = -inf: 0
-                    m = top;
-                    l *= alpha;
-                }
-                if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    wait_block(blocks + k + 1);   // O holds tile k - 1
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
-                        float o[32];
-                        uint32_t ow[32];
-                        tmem_ld32(lanes + kOutCol + half * 128 + c, o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) ow[i] = __float_as_uint(o[i] * alpha);
-                        tmem_st32(lanes + kOutCol + half * 128 + c, ow);
+                        for (int i = 0; i < 64; ++i) s[i] = i >= from && i <= to ? s[i] : -INFINITY;
                     }
-                }
-                const float ref = m == -INFINITY ? 0.f : m - lift;
-                uint32_t pw[32];
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p0 = fast_exp2(fmaf(s[2 * i], unit, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], unit, -ref));
-                    sum[i & 1] += p0;
-                    sum[2 + (i & 1)] += p1;
-                    pw[i] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                    for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float *x = xm + (g & 1) * 2 * kCtaRows;
+                    x[half * kCtaRows + row] = top;
+                    pair_sync();
+                    top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
+                    top *= scale;
+                    float alpha = 1.f;
+                    if (top > m + kRescale) {   // also a row's first key: m = -inf
+                        alpha = fast_exp2(m - top);   // m = -inf: 0
+                        m = top;
+                        l *= alpha;
+                    }
+                    rescale_output(k, alpha);
+                    const float ref = m == -INFINITY ? 0.f : m - lift;
+                    uint32_t pw[32];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = fast_exp2(fmaf(s[2 * i], scale, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], scale, -ref));
+                        sum[i & 1] += p0;
+                        sum[2 + (i & 1)] += p1;
+                        pw[i] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st32(buf + half * 32, pw);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st32(buf + half * 32, pw);
                 tmem_wait_st();
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(p_bar + 8 * (uint32_t)(g & 1));
+            if (lane == 0) mbar_arrive_remote_tmem(p_bar + 8 * (uint32_t)(g & 1));
 
         }
             // ---- the segment's output ----
@@ -884,7 +1054,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(o_free);
+                if (lane == 0) mbar_arrive_remote_tmem(o_free);
                 if (!whole) {
                     // The last of the item's pieces to arrive (for this CTA's rows) merges them.
                     const long long all = call[0], from = call[1] + w.done - w.off + kItemCost;   // the item's first tile

@@ -35,6 +35,57 @@ __device__ __forceinline__ float capped(const PagedAttnArgs &a, float z) {
     return fmaf(-2.f * a.cap, fast_rcp(1.f + fast_exp2(z)), a.cap);
 }
 
+__device__ __forceinline__ float min_or_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c;"
+        " mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+constexpr float kCapReach = 30.f;   // tanh is 1 in binary32 from 2 log2(e) x / cap of 25 on
+// capped() of four scores times z, with one reciprocal, of the product of the four 1 + e, and `top` (the cap, or the cap less
+// what is to be taken off) in place of the cap.  Scores times z must not pass kCapReach, or KEEP keeps the exponents to it.
+// A NaN among them reaches all four.
+template <bool KEEP>
+__device__ __forceinline__ void capped4(const PagedAttnArgs &a, float z, float top, float (&s)[4]) {
+    float2 d[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        d[i] = mul2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(z, z));
+        if (KEEP) d[i] = make_float2(min_or_nan(d[i].x, kCapReach), min_or_nan(d[i].y, kCapReach));
+        d[i] = add2(make_float2(fast_exp2(d[i].x), fast_exp2(d[i].y)), make_float2(1.f, 1.f));
+    }
+    const float2 q = mul2(d[0], d[1]);
+    const float r = -2.f * a.cap * fast_rcp(q.x * q.y);
+    const float2 t = make_float2(r * q.y, r * q.x), c = make_float2(top, top);   // -2 cap over q.x, q.y
+    const float2 u = fma2(t, d[1], c), v = fma2(t, d[0], c);
+    s[0] = u.x;
+    s[1] = u.y;
+    s[2] = v.x;
+    s[3] = v.y;
+}
+
 // Visible positions [lo, hi] of token i of a sequence; none when hi < lo.
 struct RowSpan {
     int lo, hi;
