@@ -40,7 +40,6 @@
 // of P through a second product, as the decode kernel takes them, would cost a
 // product in two again: 4096 tokens behind 28672 905 us against 657 in the same run.
 #include <climits>
-#include <type_traits>
 
 #include "paged_rows.cuh"
 
@@ -139,7 +138,11 @@ __device__ __forceinline__ int longest_whole(const PagedAttnArgs &a) {
 }
 
 // A walk over the segments of a pair's share.
-template <bool SCORED>
+// Rules of attn_paged_scored that a kernel is made for: visible spans alone, or scores that are capped, biased or both (their
+// spans too).  One kernel for all of them took 5 % longer in each: the loops' bodies were not all that was fetched.
+enum : int { RULE_NONE = 0, RULE_SPANS = 1, RULE_CAP = 2, RULE_BIAS = 4 };
+
+template <int RULE>
 struct Segment {
     int b, tile, h;      // the item
     SeqSpan q;
@@ -171,7 +174,7 @@ struct Segment {
                     q = seq_span(a.seqs, ++b, &bit);
                 } while (q.n == 0 && b + 1 < a.seqs.batch);
             }
-            t = make_item<SCORED>(a, q, tile);
+            t = make_item<RULE != RULE_NONE>(a, q, tile);
         }
         return true;
     }
@@ -184,13 +187,13 @@ struct Segment {
         done = 0;
         int bit;
         q = seq_span(a.seqs, b, &bit);
-        t = make_item<SCORED>(a, q, tile);
+        t = make_item<RULE != RULE_NONE>(a, q, tile);
         return settle(a);
     }
     __device__ bool next(const PagedAttnArgs &a) { return advance(a) && settle(a); }
-    // First position of its tile k.  Scored rows take their keys from the last to the first: where a bias falls with the
-    // distance, the largest scores come first and the reference of the weights hardly moves.
-    __device__ int key0(int k) const { return (t.u0 + u + (SCORED ? L - 1 - k : k)) << kKeyShift; }
+    // First position of its tile k.  Biased rows take their keys from the last to the first: the largest scores come first,
+    // where the bias falls with the distance, and the reference of the weights hardly moves.
+    __device__ int key0(int k) const { return (t.u0 + u + (RULE & RULE_BIAS ? L - 1 - k : k)) << kKeyShift; }
 };
 
 // Position in a ring of slots: index and the parity of its current round.
@@ -416,14 +419,6 @@ __device__ __forceinline__ float rule_weights(const PagedAttnArgs &a, const Rule
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
-// f(cap, bias, edge) with each as a constant.
-template <class F>
-__device__ __forceinline__ float by_rule(bool cap, bool bias, bool edge, F f) {
-    using Y = std::true_type;
-    using N = std::false_type;
-    if (edge) return cap ? (bias ? f(Y{}, Y{}, Y{}) : f(Y{}, N{}, Y{})) : (bias ? f(N{}, Y{}, Y{}) : f(N{}, N{}, Y{}));
-    return cap ? (bias ? f(Y{}, Y{}, N{}) : f(Y{}, N{}, N{})) : (bias ? f(N{}, Y{}, N{}) : f(N{}, N{}, N{}));
-}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Instruction descriptor for M = 256 rows of the pair: fp32 accumulator, bf16 or f16 operands, A K-major.
 __host__ __device__ constexpr uint32_t pair_idesc(int n, bool bf16, int b_mn) {
@@ -458,11 +453,11 @@ __device__ __forceinline__ void transpose4(uint4 (&e)[4], int lane) {
         }
 }
 
-template <int KV, bool SCORED>
+template <int KV, int RULE>
 __global__ void __launch_bounds__(chunk_threads(KV), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr bool kFp8 = KV == KV_FP8;
+    constexpr bool kFp8 = KV == KV_FP8, SCORED = RULE != RULE_NONE, kCap = RULE & RULE_CAP, kBias = RULE & RULE_BIAS;
     constexpr int kStage = stage_warps(KV), kStageWarp = first_stage_warp(KV);
     uint8_t *ring = smem + kQBytes;
     float *xm = reinterpret_cast<float *>(smem + kXmOff);
@@ -515,14 +510,14 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     tc_fence_after();
     const uint32_t tmem = *taddr_s;
     const int share = (int)(x1 - x0);
-    Segment<SCORED> w;
+    Segment<RULE> w;
     bool more = w.start(a, c0, share);   // no role has work when the share holds item costs alone
     bool dead = false;
     const int ps = 1 << sq.page_shift;
     // Whole-warp wait for the end of block i.
     auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 3)], (uint32_t)(i >> 2) & 1, dead, err); };
     // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
-    auto pages_of = [&](const Segment<SCORED> &x, int k) {
+    auto pages_of = [&](const Segment<RULE> &x, int k) {
         const int pos = x.key0(k) + 16 * (lane & 7), first = pos & ~(ps - 1);
         int page = sq.num_pages;
         if (first < x.t.hi && first + ps > x.t.lo) {
@@ -640,7 +635,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         if (!dead) {
 #pragma unroll
                             for (int t = 0; t < 8; ++t)
-                                pair_mma_ts(tmem + kOutCol, p + 8 * t + (SCORED && t >= 4 ? 32 : 0), vd + v_step[t], kIdO, i > 2 || t > 0);
+                                pair_mma_ts(tmem + kOutCol, p + 8 * t + ((kCap || kBias) && t >= 4 ? 32 : 0), vd + v_step[t], kIdO, i > 2 || t > 0);
                         }
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
@@ -850,7 +845,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
         auto soft_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         const float lift = kFp8 ? 7.f : 0.f;
-        constexpr float kLimit = kFp8 ? kRescale : kRescaleWide;   // scored rows
+        constexpr float kLimit = SCORED && !kFp8 ? kRescaleWide : kRescale;
         int blocks = 0, tiles = 0;   // before this segment
         for (uint32_t seg = 0; more; ++seg) {
         float m = -INFINITY, l = 0.f, scale = SCORED ? a.qscale : kQScale;
@@ -869,7 +864,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             lo_pos = mine.lo;
             hi_pos = mine.hi;
             bad_span = span_is_bad(mine, f, z);
-            if (a.slopes) slope = a.slopes[(w.h << a.group_shift) + (r & (a.group - 1))] * kLog2e;
+            if (kBias) slope = a.slopes[(w.h << a.group_shift) + (r & (a.group - 1))] * kLog2e;
         }
         const int rows_here = (w.t.nt << a.group_shift) - rank * kCtaRows;              // valid rows of this CTA
         const bool idle = (warp & 3) * 32 >= rows_here;                                  // none of this warp's rows exists
@@ -899,24 +894,23 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
             if (!idle) {
                 tc_fence_after();
                 const int key0 = w.key0(k) + half * 64;
-                if constexpr (SCORED) {
+                if constexpr (kCap || kBias) {
                     const RulePart part{buf + half * 64, scale, slope, (float)(key0 - pos), lo_pos - key0, hi_pos - key0};
-                    const bool cap = a.cap != 0.f, bias = a.slopes != nullptr;
                     // Tiles that every row sees whole mostly leave the rows' references as they are, which a bound on their scores
                     // shows: the cap is monotone, and the bias lies between those of the part's ends.
                     const bool edge = w.key0(k) < all_lo || w.key0(k) + kTileKeys - 1 > all_hi;
                     bool moves = edge || k == 0, careful = moves;
                     if (!moves) {
                         const float raw = raw_max(part), z = raw * (scale * a.two_over_cap);
-                        careful = cap && __any_sync(0xffffffffu, z > kCapReach);
-                        float top = cap ? capped(a, z) : raw * scale;
-                        if (bias)
+                        careful = kCap && __any_sync(0xffffffffu, z > kCapReach);
+                        float top = kCap ? capped(a, z) : raw * scale;
+                        if (kBias)
                             top = fmaf(-slope, slope > 0.f ? fmaxf(fmaxf(part.far, -63.f - part.far), 0.f)
                                                            : fmaxf(fabsf(part.far), fabsf(part.far + 63.f)), top);
                         moves = any_of_barrier(1 + (warp & 3), 64, top > m + kLimit);   // m = -inf: any score
                     }
                     if (moves) {
-                        float top = by_rule(cap, bias, careful, [&](auto c, auto b, auto e) { return rule_max<c.value, b.value, e.value>(a, part); });
+                        float top = careful ? rule_max<kCap, kBias, true>(a, part) : rule_max<kCap, kBias, false>(a, part);
                         float *x = xm + (g & 1) * 2 * kCtaRows;
                         x[half * kCtaRows + row] = top;
                         pair_sync();
@@ -930,8 +924,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                         rescale_output(k, alpha);
                     }
                     const float ref = m == -INFINITY ? 0.f : m - lift;
-                    l += by_rule(cap, bias, careful,
-                                 [&](auto c, auto b, auto e) { return rule_weights<kFp8, c.value, b.value, e.value>(a, part, ref); });
+                    l += careful ? rule_weights<kFp8, kCap, kBias, true>(a, part, ref) : rule_weights<kFp8, kCap, kBias, false>(a, part, ref);
                 } else {
                     float s[64];
                     tmem_ld64(buf + half * 64, s);
@@ -950,7 +943,7 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                     top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
                     top *= scale;
                     float alpha = 1.f;
-                    if (top > m + kRescale) {   // also a row's first key: m = -inf
+                    if (top > m + kLimit) {   // also a row's first key: m = -inf
                         alpha = fast_exp2(m - top);   // m = -inf: 0
                         m = top;
                         l *= alpha;
@@ -1157,13 +1150,13 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     }
 }
 
-template <int KV, bool SCORED>
+template <int KV, int RULE>
 cudaError_t chunk_setup(int *pairs) {
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> limit[64];
     int dev = 0;
     if (!done_on_device(done, &dev)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<KV, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
+        cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<KV, RULE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute at[1];
@@ -1175,7 +1168,7 @@ cudaError_t chunk_setup(int *pairs) {
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, paged_chunk_kernel<KV, SCORED>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, paged_chunk_kernel<KV, RULE>, &cfg);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) limit[dev].store(n, std::memory_order_relaxed);
         *pairs = n;
@@ -1186,14 +1179,23 @@ cudaError_t chunk_setup(int *pairs) {
     return cudaSuccess;
 }
 
-template <int KV, bool SCORED>
+template <int KV, int RULE>
 cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStream_t s) {
     int pairs = 0;
-    cudaError_t e = chunk_setup<KV, SCORED>(&pairs);
+    cudaError_t e = chunk_setup<KV, RULE>(&pairs);
     if (e != cudaSuccess) return e;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    return launch_overlapping(paged_chunk_kernel<KV, SCORED>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
+    return launch_overlapping(paged_chunk_kernel<KV, RULE>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
+}
+
+template <int KV>
+cudaError_t launch_by_rule(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStream_t s) {
+    const bool cap = a.cap != 0.f, bias = a.slopes != nullptr;
+    if (!a.scored) return launch_chunk<KV, RULE_NONE>(maps, a, s);
+    if (cap && bias) return launch_chunk<KV, RULE_CAP | RULE_BIAS>(maps, a, s);
+    if (cap) return launch_chunk<KV, RULE_CAP>(maps, a, s);
+    return bias ? launch_chunk<KV, RULE_BIAS>(maps, a, s) : launch_chunk<KV, RULE_SPANS>(maps, a, s);
 }
 
 }  // namespace
@@ -1201,8 +1203,7 @@ cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStre
 cudaError_t launch_paged_chunk(const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
                                const PagedAttnArgs &a, cudaStream_t s) {
     ChunkMaps maps{*qmap, *kmap, *vmap};
-    if (a.scored) return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8, true>(maps, a, s) : launch_chunk<KV_BF16, true>(maps, a, s);
-    return a.kv_type == KV_FP8 ? launch_chunk<KV_FP8, false>(maps, a, s) : launch_chunk<KV_BF16, false>(maps, a, s);
+    return a.kv_type == KV_FP8 ? launch_by_rule<KV_FP8>(maps, a, s) : launch_by_rule<KV_BF16>(maps, a, s);
 }
 
 }  // namespace hd
