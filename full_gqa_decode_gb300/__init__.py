@@ -563,7 +563,7 @@ def paged_batch(block_table: torch.Tensor, context: torch.Tensor, token_offsets:
 
 def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype, device, strided: bool = False) -> None:
     """A tensor of a paged call: its shape, type and device; contiguous, or (strided) contiguous rows."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not (t.is_contiguous() or (strided and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]))):
         raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
@@ -698,6 +698,15 @@ def _check_ints(name: str, t, n: int, device) -> None:
         raise ValueError(f"{name} must be contiguous int32 of shape ({n},) on {device}")
 
 
+def _check_weight(name: str, w: torch.Tensor, heads: int, device) -> tuple:
+    """A norm's weight: its (type, dims)."""
+    dtype, dims = w.dtype, w.dim()
+    if (w.shape != ((256,) if dims == 1 else (heads, 256)) or not (dtype is torch.bfloat16 or dtype is torch.float32) or
+            w.device != device or not w.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous bf16 or float32 of shape (256,) or ({heads}, 256) on {device}")
+    return dtype, dims
+
+
 def norm_rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
                            rope: RopeTable | None = None, q_weight: torch.Tensor | None = None,
                            k_weight: torch.Tensor | None = None, eps: float = 1.0e-6, weight_offset: float = 0.0,
@@ -708,21 +717,21 @@ def norm_rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v,
     ``q_weight`` / ``k_weight``: bf16 or float32 [256], or one row a head ([Hq, 256] and [Hkv, 256]);
     None: ones.  ``norm=False``: the rotation alone."""
     qs = _check_append(ctx, batch, q, k, v, q_rot, cache)
-    _check_ints("positions", positions, batch.num_tokens, cache.device)
+    if positions is not None:
+        _check_ints("positions", positions, batch.num_tokens, cache.device)
     if rope is not None and rope.table.device != cache.device:
         raise ValueError("the table of angles must be on the pages' device")
     ref = None
     if norm:
-        have = [(n, w, h) for n, w, h in (("q_weight", q_weight, ctx.cfg.num_q_heads), ("k_weight", k_weight, ctx.cfg.num_kv_heads))
-                if w is not None]
-        for n, w, h in have:
-            if (tuple(w.shape) not in ((256,), (h, 256)) or w.dtype not in (torch.bfloat16, torch.float32) or
-                    w.device != cache.device or not w.is_contiguous()):
-                raise ValueError(f"{n} must be contiguous bf16 or float32 of shape (256,) or ({h}, 256) on {cache.device}")
-        if len({(w.dtype, w.dim()) for _, w, _ in have}) > 1:
-            raise ValueError("q_weight and k_weight must share a type and be both per head or both shared")
-        ref = ctypes.byref(hd_head_norm(_ptr(q_weight), _ptr(k_weight), int(any(w.dtype == torch.float32 for _, w, _ in have)),
-                                        int(any(w.dim() == 2 for _, w, _ in have)), weight_offset, eps))
+        kind, q_ptr, k_ptr = (), None, None   # (type, dims) of the weights
+        if q_weight is not None:
+            kind, q_ptr = _check_weight("q_weight", q_weight, ctx.cfg.num_q_heads, cache.device), q_weight.data_ptr()
+        if k_weight is not None:
+            other, k_ptr = _check_weight("k_weight", k_weight, ctx.cfg.num_kv_heads, cache.device), k_weight.data_ptr()
+            if kind and other != kind:
+                raise ValueError("q_weight and k_weight must share a type and be both per head or both shared")
+            kind = other
+        ref = ctypes.byref(hd_head_norm(q_ptr, k_ptr, torch.float32 in kind, 2 in kind, weight_offset, eps))
     elif q_weight is not None or k_weight is not None:
         raise ValueError("weights belong to a norm")
     _check(_lib.norm_rope_append_paged(ctx.handle, layer, batch.ref, ref, None if rope is None else rope.ref, _ptr(positions),

@@ -106,7 +106,7 @@ __device__ __forceinline__ int angle_row(const PagedNormArgs &a, int r, int p) {
 }
 
 template <bool NEIGHBOURS>
-__global__ void __launch_bounds__(kEntryThreads) paged_norm_append_kernel(const __grid_constant__ PagedNormArgs a, int runs) {
+__global__ void __launch_bounds__(kEntryThreads, 4) paged_norm_append_kernel(const __grid_constant__ PagedNormArgs a, int runs) {
     const PagedAppendArgs &e = a.entry;
     const PagedSeqs &sq = e.seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

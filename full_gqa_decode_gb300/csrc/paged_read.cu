@@ -12,7 +12,7 @@ namespace hd {
 namespace {
 
 constexpr int kReadThreads = 256, kReadWarps = kReadThreads / 32;
-constexpr int kReadRows = 4;
+constexpr int kReadRows = 2;
 
 // Eight codes of a lane as bf16: their values times the scale, rounded once.  The product of 4 and 24 bits is first rounded to
 // odd in binary32 (towards zero, the last bit set where that was not exact), which the rounding to bf16 then takes as exact.
@@ -28,7 +28,7 @@ __device__ __forceinline__ uint4 scaled_codes(const uint2 &codes, float scale) {
 }
 
 template <int KV>
-__global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const __grid_constant__ PagedReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads, 6) paged_read_kernel(const __grid_constant__ PagedReadArgs a) {
     constexpr bool kFp8 = KV == KV_FP8;
     const PagedSeqs &sq = a.seqs;
     const int lane = threadIdx.x & 31, ps = 1 << sq.page_shift;
