@@ -25,8 +25,8 @@
 // maxima exchanged through shared memory by pairs of warps); a copy warp; the
 // MMA warp (only the first CTA's issues; its barriers collect the arrivals of
 // both CTAs); and stage warps, which hand a landed stage on to the MMA warp:
-// with bf16 pages one warp, which only zeroes the V rows of positions that no
-// row sees (they may hold NaN); with E4M3 pages four warps for K and four for V,
+// with bf16 pages one warp (scored rows: two), which only zeroes the V rows of
+// positions that no row sees (they may hold NaN); with E4M3 pages four warps for K and four for V,
 // which read the codes a tile ahead into registers and convert them to f16
 // (exact) in the layout of the MMAs.
 //
@@ -48,12 +48,12 @@ namespace {
 
 constexpr int kTileRows = kChunkRows, kCtaRows = kTileRows / 2, kTileKeys = kChunkKeys, kKeyShift = 7;
 constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-// Stage warps, for K and for V operands: one each behind the MMA warp (bf16); two groups of four at the next multiple of
-// four warps (E4M3).  kStage: those that hand on one operand.
+// Stage warps: one behind the MMA warp (bf16; scored rows two, for K and for V operands); two groups of four, for K and for V
+// operands, at the next multiple of four warps (E4M3).  kStage: those that hand on one operand.
 __host__ __device__ constexpr int first_stage_warp(int kv) { return kv == KV_FP8 ? kSoftWarps + 4 : kSoftWarps + 2; }
 __host__ __device__ constexpr int stage_warps(int kv) { return kv == KV_FP8 ? 4 : 1; }
-__host__ __device__ constexpr int chunk_threads(int kv) {
-    return (first_stage_warp(kv) + 2 * stage_warps(kv)) * 32;
+__host__ __device__ constexpr int chunk_threads(int kv, bool scored) {
+    return (first_stage_warp(kv) + (kv == KV_FP8 || scored ? 2 : 1) * stage_warps(kv)) * 32;
 }
 // E4M3: 640 threads launch with 96 registers each; the groups of four warps then share them out by need.
 // 256 x 128 + 128 x 56 + 256 x 80 <= 640 x 96.
@@ -454,7 +454,7 @@ __device__ __forceinline__ void transpose4(uint4 (&e)[4], int lane) {
 }
 
 template <int KV, int RULE>
-__global__ void __launch_bounds__(chunk_threads(KV), 1)
+__global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8, SCORED = RULE != RULE_NONE, kCap = RULE & RULE_CAP, kBias = RULE & RULE_BIAS;
@@ -516,6 +516,19 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
     const int ps = 1 << sq.page_shift;
     // Whole-warp wait for the end of block i.
     auto wait_block = [&](int i) { wait_warp(&bar[BAR_BLOCK + (i & 3)], (uint32_t)(i >> 2) & 1, dead, err); };
+    // bf16: the two stage warps meet for each V operand.
+    auto v_landed = [&]() { asm volatile("bar.sync 6, 64;" ::: "memory"); };
+    // bf16, a warp: zeros for the V rows of positions that no query row sees, whatever their slots hold.
+    auto zero_unseen = [&](uint8_t *slot, const ChunkTile &x, int key0) {
+        if (key0 >= x.lo && key0 + kTileKeys <= x.hi) return;
+        const int rv_shift = min(sq.page_shift, 7);
+        for (int r = 0; r < kTileKeys; ++r) {
+            if (key0 + r >= x.lo && key0 + r < x.hi) continue;
+            const uint32_t at = (uint32_t)(r >> rv_shift << rv_shift) * 256 + (uint32_t)(r & ((1 << rv_shift) - 1)) * 128 +
+                                (lane >> 3 & 1) * (128u << rv_shift) + (lane & 7) * 16;
+            if (lane < 16) *reinterpret_cast<uint4 *>(slot + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
     // Pages of a tile's eight groups of 16 keys, one per lane; a page that no row sees lies outside the map.
     auto pages_of = [&](const Segment<RULE> &x, int k) {
         const int pos = x.key0(k) + 16 * (lane & 7), first = pos & ~(ps - 1);
@@ -793,46 +806,49 @@ __global__ void __launch_bounds__(chunk_threads(KV), 1)
                 if (more) load(0);
             }
         }
-    } else if (!kFp8 && warp >= kStageWarp) {
+    } else if (!kFp8 && warp == kStageWarp) {
         // ---- bf16 stages: hand what has landed on to the MMAs ----
-        // An arrival that releases to the cluster takes about 1000 clocks: one warp for all operands was what a tile took (4096
-        // tokens behind 28672 660 us).  Each waits for every operand, so that it sees every phase of a slot, and hands on its own.
+        // Scored rows: an arrival that releases to the cluster takes about 1000 clocks, and with two a tile this warp was what a
+        // tile took (4096 capped tokens behind 28672 1024 us, so 948).  So a second warp, which this one meets for each V operand,
+        // hands those on.  This one alone waits for copies: it sees every phase of a slot, the other none.
         const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0), q_ready = dsmem_addr(&bar[BAR_Q_READY], 0);
-        const int rv_shift = min(sq.page_shift, 7);
         RingPos<kSlots> pos;
         for (uint32_t seg = 0; more; ++seg) {
-            if (warp == kStageWarp) {
-                wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(q_ready);
-            }
+            wait_warp(&bar[BAR_Q_FULL], seg & 1, dead, err);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(q_ready);
             for (int i = 0; i <= w.L; ++i) {
 #pragma unroll
                 for (int kind = 0; kind < 2; ++kind) {   // K(i), then V(i - 1)
                     if (kind == 0 ? i >= w.L : i == 0) continue;
-                    uint8_t *slot = ring + pos.st * kSlotBytes;
                     wait_warp(&bar[BAR_FULL + pos.st], pos.ph, dead, err);
-                    if (warp - kStageWarp != kind) {
-                        pos.step();
-                        continue;
+                    if (SCORED && kind == 1) {
+                        v_landed();
+                    } else {
+                        if (kind == 1) zero_unseen(ring + pos.st * kSlotBytes, w.t, w.key0(i - 1));
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
                     }
-                    const int key0 = w.key0(i - 1);
-                    if (kind == 1 && (key0 < w.t.lo || key0 + kTileKeys > w.t.hi)) {
-                        // Rows of positions that no query row sees: zero, whatever their slots hold.
-                        for (int r = 0; r < kTileKeys; ++r) {
-                            if (key0 + r >= w.t.lo && key0 + r < w.t.hi) continue;
-                            const uint32_t at = (uint32_t)(r >> rv_shift << rv_shift) * 256 +
-                                                (uint32_t)(r & ((1 << rv_shift) - 1)) * 128 +
-                                                (lane >> 3 & 1) * (128u << rv_shift) + (lane & 7) * 16;
-                            if (lane < 16) *reinterpret_cast<uint4 *>(slot + at) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
                     pos.step();
                 }
+            }
+            more = w.next(a);
+        }
+    } else if (SCORED && !kFp8 && warp == kStageWarp + 1) {
+        // ---- V operands that have landed ----
+        const uint32_t ready0 = dsmem_addr(&bar[BAR_READY], 0);
+        RingPos<kSlots> pos;
+        while (more) {
+            pos.step(w.L > 1 ? 2 : 1);
+            for (int k = 0; k < w.L; ++k) {
+                v_landed();
+                zero_unseen(ring + pos.st * kSlotBytes, w.t, w.key0(k));
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(ready0 + 8 * pos.st);
+                pos.step(k + 2 < w.L ? 2 : 1);
             }
             more = w.next(a);
         }
@@ -1163,7 +1179,7 @@ cudaError_t chunk_setup(int *pairs) {
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim = {2, 1, 1};
         cfg.gridDim = dim3(2 * kMaxPairs);
-        cfg.blockDim = dim3(chunk_threads(KV));
+        cfg.blockDim = dim3(chunk_threads(KV, RULE != RULE_NONE));
         cfg.dynamicSmemBytes = kChunkSmem;
         cfg.attrs = at;
         cfg.numAttrs = 1;
@@ -1186,7 +1202,7 @@ cudaError_t launch_chunk(const ChunkMaps &maps, const PagedAttnArgs &a, cudaStre
     if (e != cudaSuccess) return e;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    return launch_overlapping(paged_chunk_kernel<KV, RULE>, dim3(2 * pairs), chunk_threads(KV), kChunkSmem, 2, s, maps, a);
+    return launch_overlapping(paged_chunk_kernel<KV, RULE>, dim3(2 * pairs), chunk_threads(KV, RULE != RULE_NONE), kChunkSmem, 2, s, maps, a);
 }
 
 template <int KV>
