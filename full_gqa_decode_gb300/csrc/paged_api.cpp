@@ -81,6 +81,30 @@ bool encode_queries(CUtensorMap *map, const void *q, int num_q_heads, int num_to
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the decode kernel serves a call with more rows per kv head than its tiles hold sooner than the chunk kernel: it reads
+// a sequence's keys once per eight rows, the chunk kernel once per 256 rows, but with a longer start and drain.  Estimates in
+// microseconds, fitted to calls of 1 to 256 sequences with 12 to 160 rows each behind 0 to 30000 keys; they pick the slower
+// kernel by more than 8 % in 3 of 140.  Measured decode and chunk: 2 to 7 tokens of 16 sequences in 512-key windows 15.7 and
+// 24.4 us; 16 tokens of one sequence at 8000 27.8 and 42.4; 7 tokens of 16 sequences at 8000 158 and 74; 3 tokens of 64
+// at 8000 over E4M3 pages 170 and 342.
+constexpr int kDecodeRowsMost = 160;
+bool decode_is_sooner(const hd_ctx *ctx, const PagedSeqs &s, int window) {
+    const int64_t rows = (int64_t)s.max_tokens * ctx->group;
+    if (rows <= kDecodeRows || rows > kDecodeRowsMost) return rows <= kDecodeRows;
+    int64_t keys = std::min({(int64_t)s.max_context + s.max_tokens, (int64_t)s.max_position + 1, (int64_t)s.max_blocks << s.page_shift});
+    if (window) keys = std::min(keys, (int64_t)window - 1 + s.max_tokens);
+    // Tiles of the call in each kernel: by the longest sequence, or by all its rows.
+    const auto items = [&](int64_t tile) {
+        const int64_t all = (int64_t)s.num_tokens * ctx->group / tile + s.batch;
+        return (double)std::min(s.batch * ((rows + tile - 1) / tile), all) * ctx->cfg.num_kv_heads;
+    };
+    const bool fp8 = ctx->kv_type == KV_FP8;
+    const double units = keys / 128.0, few = items(kDecodeRows), wide = items(kChunkRows), pairs = ctx->num_sms / 2;
+    const double decode = 10.0 + few * ((fp8 ? 0.0098 : 0.018) * units + 0.01);
+    const double pieces = std::min(pairs / wide, units / 4);   // of an item, which are merged
+    return decode < (fp8 ? 28.0 : 20.0) + (fp8 ? 0.039 : 0.0263) * wide * (units + 2) + 0.6 * pieces;
+}
+
 hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_rot, const hd_paged_cache &c,
                  const int32_t *selected, int num_selected, const hd_scoring *rule, const float *sink, const float *gate,
                  void *out, float *lse, void *stream) {
@@ -120,8 +144,8 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
         a.last = rule->last;
     }
     // More than eight rows per kv head in some sequence: the tensor-memory kernel, which also serves the call's
-    // single tokens; lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
-    const bool chunk = !selected && (int64_t)seqs.max_tokens * ctx->group > kDecodeRows;
+    // single tokens (with a rule, unless the decode kernel is sooner); lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
+    const bool chunk = !selected && (rule ? !decode_is_sooner(ctx, seqs, a.window) : (int64_t)seqs.max_tokens * ctx->group > kDecodeRows);
     const int64_t rows = paged_partial_rows(ctx->num_sms, chunk);
     a.part_o = reinterpret_cast<float *>(ctx->paged_ws());
     a.part_ml = reinterpret_cast<float2 *>(ctx->paged_ws() + rows * kHeadDim * 4);
