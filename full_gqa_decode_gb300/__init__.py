@@ -755,9 +755,11 @@ def scoring(softcap: float = 0.0, scale: float = 0.0, slopes: torch.Tensor | Non
     return Scoring(hd_scoring(scale, softcap, _ptr(slopes), _ptr(first), _ptr(last)), slopes, first, last)
 
 
-def attn_paged_scored(ctx: Context, layer: int, batch: PagedBatch, rule: Scoring, q_rot, cache: PagedCache, sink, out, lse,
-                      gate=None, stream=None) -> None:
-    """attn_paged with capped or biased scores and masks of documents and prefixes (``scoring``)."""
+def attn_paged_scored(ctx: Context, layer: int, batch: PagedBatch, rule: Scoring | None, q_rot, cache: PagedCache, sink, out,
+                      lse, gate=None, stream=None) -> None:
+    """attn_paged with capped or biased scores and masks of documents and prefixes (``scoring``; None: attn_paged's own)."""
+    if rule is None:
+        return attn_paged(ctx, layer, batch, q_rot, cache, sink, out, lse, gate, stream)
     _check_attn_paged(ctx, batch, q_rot, cache, sink, gate, out, lse)
     if rule.slopes is not None and (rule.slopes.dtype != torch.float32 or tuple(rule.slopes.shape) != (ctx.cfg.num_q_heads,) or
                                     rule.slopes.device != cache.device or not rule.slopes.is_contiguous()):

@@ -328,7 +328,8 @@ hd_status attn_paged_scored(hd_ctx *ctx, int32_t layer, const hd_paged_batch *ba
     if (scoring) {
         const float scale = scoring->scale, cap = scoring->softcap;
         if (!std::isfinite(scale) || scale < 0.f || !std::isfinite(cap) || cap < 0.f) return HD_ERR_INVALID_ARG;
-        if (cap != 0.f && (cap < 1.f / 1024.f || cap > 1024.f)) return HD_ERR_UNSUPPORTED;
+        if ((cap != 0.f && (cap < 1.f / 1024.f || cap > 1024.f)) || (scale != 0.f && (scale < 0x1p-32f || scale > 0x1p32f)))
+            return HD_ERR_UNSUPPORTED;
     }
     return attend(ctx, layer, s, q_rot, *cache, nullptr, 0, scoring, sink, gate, out, lse, stream);
 }

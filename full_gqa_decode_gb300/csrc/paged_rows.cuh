@@ -28,8 +28,9 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 // cap tanh(x / cap) of a score: with e = exp(2 x / cap) it is cap - 2 cap / (1 + e), which keeps an absolute error below
-// 2^-21 cap (the roundings of 2^x, of 1 + e, of its reciprocal and of the last step; the first counts at most half, as
-// the slope 2 e / (1 + e)^2 is).  e overflows to infinity and underflows to 0 where tanh is 1 and -1.
+// 2^-21 cap: with u = 2^-24, 2^x (4 u of e, the argument's rounding less) counts 2 u as the slope 2 e / (1 + e)^2 is at most
+// half, 1 + e and its reciprocal 3 u of a term of at most 2 cap / (1 + e), the last step u.  e overflows to infinity and
+// underflows to 0 where tanh is 1 and -1.
 // `z`: x times 2 log2(e) / cap; all else in log2 units.
 __device__ __forceinline__ float capped(const PagedAttnArgs &a, float z) {
     return fmaf(-2.f * a.cap, fast_rcp(1.f + fast_exp2(z)), a.cap);
@@ -65,8 +66,9 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
 }
 constexpr float kCapReach = 30.f;   // tanh is 1 in binary32 from 2 log2(e) x / cap of 25 on
 // capped() of four scores times z, with one reciprocal, of the product of the four 1 + e, and `top` (the cap, or the cap less
-// what is to be taken off) in place of the cap.  Scores times z must not pass kCapReach, or KEEP keeps the exponents to it.
-// A NaN among them reaches all four.
+// what is to be taken off) in place of the cap.  Three products and the scaling add 4 u of the term to the error: below
+// 2^-20 cap in all.  Scores times z must not pass kCapReach, or KEEP keeps the exponents to it.  A NaN among them reaches all
+// four.
 template <bool KEEP>
 __device__ __forceinline__ void capped4(const PagedAttnArgs &a, float z, float top, float (&s)[4]) {
     float2 d[2];

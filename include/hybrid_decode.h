@@ -641,7 +641,7 @@ typedef struct {
  * values are stored as rope_append_paged stores them, bit for bit.
  *   norm       NULL: none (rotation alone)
  *   rope       NULL: the context's own angles of the layer's type, in halves
- *   positions  device [num_tokens], the position whose angles a row takes (packed
+ *   positions  device int32 [num_tokens], the position whose angles a row takes (packed
  *              documents); NULL: its position in the sequence, and the table must
  *              hold those (a sequence that reaches past the table is a sequence
  *              that cannot be served).  A given position outside the table is
@@ -663,14 +663,17 @@ hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batc
  *   first,     the visible positions of row r, first[r] .. last[r]: device
  *   last       [num_tokens] each, or NULL (0; p).  A sliding layer's window starts
  *              them at p - window + 1 at the earliest; they end with the
- *              sequence's last new token at the latest.  Documents packed into a
+ *              sequence's last new token at the latest (int32).  Documents packed into a
  *              sequence: first is the start of a row's document.  A prefix (or a
  *              block) whose tokens see each other: last is its last position.  A
  *              row may see nothing: out 0, lse -inf.  Both ascend (not strictly)
  *              along a sequence's rows; a row that is found not to is flagged
  *              (HD_DEVERR_SPAN) and gets NaN, or is served by its own values.
- *   scale      0: 1 / sqrt(head_dim); else positive and finite
- * Entries from a sequence's lowest to its highest visible position must be finite. */
+ *   scale      0: 1 / sqrt(head_dim); else 2^-32 to 2^32, HD_ERR_UNSUPPORTED beyond
+ * HD_ERR_INVALID_ARG when scale or softcap is negative or not finite.  Entries from
+ * a sequence's lowest to its highest visible position must be finite.  Weights are
+ * rounded before they meet the values as in attn_paged, by the kernel that serves
+ * the call: calls of few rows take the one that an estimate says is sooner. */
 typedef struct {
     float scale;
     float softcap;
@@ -690,7 +693,8 @@ hd_status attn_paged_scored(hd_ctx *ctx, int32_t layer, const hd_paged_batch *ba
  * positions to read -- in bf16: bit for bit, or an E4M3 code's value times the
  * scale, rounded once.  Keys come as they are stored, rotated.
  *   k, v   bf16 [num_tokens][num_kv_heads][head_dim], rows k_stride / v_stride
- *          elements apart (multiples of 8), 16-byte aligned; either may be NULL
+ *          elements apart (multiples of 8), 16-byte aligned, apart from the pages
+ *          and from one another; either may be NULL
  * A page outside the pool reads as zeros and is flagged; rows of a sequence that
  * cannot be served get NaN. */
 hd_status read_paged(hd_ctx *ctx, const hd_paged_batch *batch, const hd_paged_cache *cache, void *k, int64_t k_stride,

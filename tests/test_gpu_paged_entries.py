@@ -376,6 +376,29 @@ def test_read_past_32_bits(hd, kv):
     assert hd.hybrid_decode_device_errors(ctx) == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_append_past_32_bits(hd, kv):
+    """The same entries in the first pages of a pool and behind 2^31 elements."""
+    big = 2 ** 31 // (256 * 256) + 4
+    ctx = context(hd, kv_heads=1, kv=kv)
+    k, v = (torch.zeros(big, 1, 256, D, device="cuda", dtype=torch.uint8 if kv == "e4m3" else torch.bfloat16) for _ in range(2))
+    scale = torch.full((1,), 0.01, device="cuda") if kv == "e4m3" else None
+    bounds = torch.zeros(big, 1, 2, D, dtype=torch.bfloat16, device="cuda")
+    cache = hd.paged_cache(k, v, scale, scale, bounds=bounds)
+    rng = synth.generator(5)
+    new = [synth.normal_bf16(rng, (300, 1, D)).cuda() for _ in range(2)]
+    for at in (0, big - 2):
+        batch = hd.paged_batch(torch.tensor([[at, at + 1]], dtype=torch.int32, device="cuda"),
+                               torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, 300], dtype=torch.int32, device="cuda"),
+                               num_tokens=300, max_tokens=300)
+        hd.norm_rope_append_paged(ctx, 1, batch, None, *new, None, cache, rope=table_of(hd, "halves 64"))
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    for t in (k, v, bounds):
+        assert t[0].float().abs().sum() > 0 and torch.equal(t[:2], t[big - 2:])
+        assert not t[2: 10].any() and not t[big - 6: big - 2].any()
+
+
 def test_read_refusals(hd):
     case = PagedCase(323, [(5, 4)])
     ctx, d = context(hd), case.device()

@@ -317,6 +317,57 @@ def test_prompt_in_parts_equals_one_prompt(hd, orc, kv, window):
     assert at == 330 and hd.hybrid_decode_device_errors(ctx) == 0
 
 
+@pytest.mark.parametrize("n", [1, 12, 90])   # the decode kernel's one tile, several, and the chunk kernel
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(hd, orc, kv, n):
+    """Pages whose offsets in elements pass 2^31."""
+    case = PagedCase(219, [(300, n), (40, n)], kv=kv, page=256, kv_heads=1, group=4, single=n == 1)
+    big = 2 ** 31 // (256 * 256) + 40
+    k, v = (torch.zeros(big, 1, 256, D, dtype=t.dtype, device="cuda") for t in (case.k, case.v))
+    k[big - case.pool:], v[big - case.pool:] = case.k.cuda(), case.v.cuda()
+    d = case.device()
+    ctx = context(hd, 4, 1, kv)
+    cache = hd.paged_cache(k, v, d["k_scale"], d["v_scale"])
+    batch = hd.paged_batch((d["table"] + (big - case.pool)).contiguous(), d["context"], d["offsets"], num_tokens=case.rows,
+                           max_tokens=case.max_tokens, max_context=300)
+    out, lse = torch.empty_like(d["q"]), torch.empty(case.rows, case.q_heads, device="cuda")
+    rule = rule_of("all", case)
+    hd.attn_paged_scored(ctx, 1, batch, rule.device(hd), d["q"], cache, None, out, lse)
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    assert_rows(reference_scored(orc, case, rule, rows=range(0, case.rows, 5)), out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_two_contexts_at_once(hd, orc, n):
+    """Calls of two contexts on two streams, each with its own workspace."""
+    cases = [PagedCase(220 + i, [(2500 - 300 * i, n), (40, n), (700, n)], single=n == 1) for i in range(2)]
+    rules = [Rule(softcap=20.0), Rule(slopes=slopes_of(8), first=documents(cases[1], [50, 9]))]
+    ctxs = [hd.hybrid_decode_init(hd.Config(layer_types=[0, 1], max_batch=8, max_context=4000)) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    d = [c.device() for c in cases]
+    outs = [(torch.empty_like(x["q"]), torch.empty(c.rows, 8, device="cuda")) for c, x in zip(cases, d)]
+    on = [r.device(hd) for r in rules]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            hd.attn_paged_scored(ctxs[i], 1, cases[i].batch_of(hd, d[i]), on[i], d[i]["q"], cache_of(hd, d[i]), None, *outs[i],
+                                 stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert hd.hybrid_decode_device_errors(ctxs[i]) == 0
+        assert_rows(reference_scored(orc, cases[i], rules[i], rows=range(0, cases[i].rows, 7)), *outs[i])
+        ctxs[i].close()
+
+
+@pytest.mark.parametrize("tokens", [3, 9, 40, 41])   # at group 4: 12 to 164 rows, on both sides of the choice of kernel
+@pytest.mark.parametrize("contexts", [(0, 7, 100), (2600, 300, 1900)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_calls_of_few_rows(hd, orc, kv, contexts, tokens):
+    case = PagedCase(222, [(c, tokens - i) for i, c in enumerate(contexts)], kv=kv, page=32)
+    check(hd, orc, case, rule_of("all", case), rows=range(0, case.rows, 3), sink=sinks(case), max_context=max(contexts) or 1)
+
+
 def test_refusals(hd):
     case = PagedCase(218, [(5, 2), (7, 1)])
     ctx, d = context(hd), case.device()
@@ -327,7 +378,8 @@ def test_refusals(hd):
         hd.attn_paged_scored(ctx, 1, batch, hd.scoring(**kw), d["q"], cache, None, out, lse)
 
     for kw, status in (({"softcap": -1.0}, 1), ({"softcap": float("nan")}, 1), ({"softcap": float("inf")}, 1), ({"scale": -1.0}, 1),
-                       ({"scale": float("inf")}, 1), ({"softcap": 1e-4}, 2), ({"softcap": 2000.0}, 2)):
+                       ({"scale": float("inf")}, 1), ({"softcap": 1e-4}, 2), ({"softcap": 2000.0}, 2), ({"scale": 1e-10}, 2),
+                       ({"scale": 1e10}, 2)):
         with pytest.raises(hd.HDError) as e:
             call(**kw)
         assert e.value.status == status, kw
