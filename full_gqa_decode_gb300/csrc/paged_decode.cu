@@ -32,6 +32,13 @@
 // weight); f16 weights are taken 2^15 times as large, which the division by their
 // sum undoes, so that small ones stay clear of f16's subnormals.  Sums and maxima
 // stay in fp32.
+//
+// Scored rows (attn_paged_scored) are an instance of the same kernel: their tiles
+// range over what any of their rows sees, and a score is capped and biased
+// between its product and its weight, a few instructions in the shadow of the
+// reads.  Measured: one sequence at 4096 capped 12.9 us, 64 sequences of 512 to
+// 32768 capped 333 us (7.0 TB/s), 256 of 512 to 8192 at group 8 over E4M3 pages
+// with a bias by distance 201 us (5.8 TB/s).
 #include "paged_rows.cuh"
 
 namespace hd {

@@ -1,9 +1,11 @@
 // Reading a paged cache's entries back as rows in bf16.
 //
 // Bytes: the entries once in, the rows once out; nothing else bounds it.  A warp
-// takes kReadRows neighbouring rows, which mostly lie in one sequence and page,
-// and both heads' K and V pieces of them at a time, so that eight independent
-// loads of 16 bytes a lane (bf16) are under way before the first store.
+// takes two neighbouring rows, which mostly lie in one sequence and page, and K
+// and V of one head of them at a time: four independent loads a lane before the
+// first store, at six CTAs an SM.  Measured: four sequences of up to 32768 over
+// E4M3 pages 60.6 us (6.0 TB/s, 90 % of a copy's rate; four rows a warp 67.5, one
+// 64.6), over bf16 pages 75 us (6.5 TB/s).
 #include <climits>
 
 #include "paged_sched.cuh"
