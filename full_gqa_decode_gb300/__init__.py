@@ -561,12 +561,16 @@ def paged_batch(block_table: torch.Tensor, context: torch.Tensor, token_offsets:
     return PagedBatch(c, (block_table, context, token_offsets), context.device)
 
 
-def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype, device, strided: bool = False) -> None:
-    """A tensor of a paged call: its shape, type and device; contiguous, or (strided) contiguous rows."""
+def _check_rows(name: str, t: torch.Tensor, shape: tuple, dtype, device, strided: bool = False) -> int:
+    """A tensor of a paged call: its shape, type and device; contiguous, or (strided) contiguous rows, of which
+    it returns the stride."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not (t.is_contiguous() or (strided and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]))):
+    if t.is_contiguous():
+        return shape[1] * shape[2] if strided else 0
+    if not (strided and t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2])):
         raise ValueError(f"{name} must be contiguous" + (" within each row" if strided else ""))
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _check_paged(ctx: Context, batch: PagedBatch, cache: PagedCache) -> None:
@@ -576,24 +580,20 @@ def _check_paged(ctx: Context, batch: PagedBatch, cache: PagedCache) -> None:
         raise ValueError("the batch and the pages must be on the current device")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _check_append(ctx: Context, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache) -> int:
+def _check_append(ctx: Context, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache) -> tuple:
+    """Row strides of q (0: none), k and v."""
     _check_paged(ctx, batch, cache)
     n, D, dev = batch.num_tokens, 256, cache.device
     kv = (n, ctx.cfg.num_kv_heads, D)
-    _check_rows("k", k, kv, torch.bfloat16, dev, True)
-    _check_rows("v", v, kv, torch.bfloat16, dev, True)
+    ks = _check_rows("k", k, kv, torch.bfloat16, dev, True)
+    vs = _check_rows("v", v, kv, torch.bfloat16, dev, True)
     qs = 0
     if (q is None) != (q_rot is None):
         raise ValueError("q and q_rot go together")
     if q is not None:
-        _check_rows("q", q, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev, True)
+        qs = _check_rows("q", q, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev, True)
         _check_rows("q_rot", q_rot, (n, ctx.cfg.num_q_heads, D), torch.bfloat16, dev)
-        qs = _row_stride(q)
-    return qs
+    return qs, ks, vs
 
 
 def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_rot, cache: PagedCache,
@@ -601,9 +601,9 @@ def rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v, q_ro
     """Rotate the new q [num_tokens, Hq, 256] into q_rot (bf16; may be q) and the new k, and store
     k / v [num_tokens, Hkv, 256] in their pages, with the pages' bounds when the cache has them.
     q, k and v may be parts of wider rows; q and q_rot may both be None."""
-    qs = _check_append(ctx, batch, q, k, v, q_rot, cache)
-    _check(_lib.rope_append_paged(ctx.handle, layer, batch.ref, _ptr(q), qs, k.data_ptr(), _row_stride(k), v.data_ptr(),
-                                  _row_stride(v), _ptr(q_rot), cache.ref, _stream(stream)), "rope_append_paged")
+    qs, ks, vs = _check_append(ctx, batch, q, k, v, q_rot, cache)
+    _check(_lib.rope_append_paged(ctx.handle, layer, batch.ref, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                  _ptr(q_rot), cache.ref, _stream(stream)), "rope_append_paged")
 
 
 def _check_attn_paged(ctx: Context, batch: PagedBatch, q_rot, cache: PagedCache, sink, gate, out, lse) -> None:
@@ -716,7 +716,7 @@ def norm_rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v,
     angles) at the rows' positions in their sequences, or at ``positions`` (int32 [num_tokens]).
     ``q_weight`` / ``k_weight``: bf16 or float32 [256], or one row a head ([Hq, 256] and [Hkv, 256]);
     None: ones.  ``norm=False``: the rotation alone."""
-    qs = _check_append(ctx, batch, q, k, v, q_rot, cache)
+    qs, ks, vs = _check_append(ctx, batch, q, k, v, q_rot, cache)
     if positions is not None:
         _check_ints("positions", positions, batch.num_tokens, cache.device)
     if rope is not None and rope.table.device != cache.device:
@@ -735,7 +735,7 @@ def norm_rope_append_paged(ctx: Context, layer: int, batch: PagedBatch, q, k, v,
     elif q_weight is not None or k_weight is not None:
         raise ValueError("weights belong to a norm")
     _check(_lib.norm_rope_append_paged(ctx.handle, layer, batch.ref, ref, None if rope is None else rope.ref, _ptr(positions),
-                                       _ptr(q), qs, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), _ptr(q_rot),
+                                       _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_rot),
                                        cache.ref, _stream(stream)), "norm_rope_append_paged")
 
 
@@ -776,11 +776,9 @@ def read_paged(ctx: Context, batch: PagedBatch, cache: PagedCache, k=None, v=Non
     scale, rounded once.  Keys come as stored, rotated."""
     _check_paged(ctx, batch, cache)
     shape = (batch.num_tokens, ctx.cfg.num_kv_heads, 256)
-    for name, t in (("k", k), ("v", v)):
-        if t is not None:
-            _check_rows(name, t, shape, torch.bfloat16, cache.device, True)
-    _check(_lib.read_paged(ctx.handle, batch.ref, cache.ref, _ptr(k), 0 if k is None else _row_stride(k), _ptr(v),
-                           0 if v is None else _row_stride(v), _stream(stream)), "read_paged")
+    ks, vs = (0 if t is None else _check_rows(name, t, shape, torch.bfloat16, cache.device, True)
+              for name, t in (("k", k), ("v", v)))
+    _check(_lib.read_paged(ctx.handle, batch.ref, cache.ref, _ptr(k), ks, _ptr(v), vs, _stream(stream)), "read_paged")
 
 
 def hybrid_decode_read_probe(buffer: torch.Tensor, stream=None) -> int:
