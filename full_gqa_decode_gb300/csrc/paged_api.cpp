@@ -91,7 +91,8 @@ constexpr int kDecodeRowsMost = 160;
 bool decode_is_sooner(const hd_ctx *ctx, const PagedSeqs &s, int window) {
     const int64_t rows = (int64_t)s.max_tokens * ctx->group;
     if (rows <= kDecodeRows || rows > kDecodeRowsMost) return rows <= kDecodeRows;
-    int64_t keys = std::min({(int64_t)s.max_context + s.max_tokens, (int64_t)s.max_position + 1, (int64_t)s.max_blocks << s.page_shift});
+    int64_t keys = std::min({(int64_t)s.max_context + s.max_tokens, (int64_t)s.max_position + 1,
+                             (int64_t)s.max_blocks << s.page_shift});
     if (window) keys = std::min(keys, (int64_t)window - 1 + s.max_tokens);
     // Tiles of the call in each kernel: by the longest sequence, or by all its rows.
     const auto items = [&](int64_t tile) {
@@ -145,7 +146,8 @@ hd_status attend(hd_ctx *ctx, int layer, const PagedSeqs &seqs, const void *q_ro
     }
     // More than eight rows per kv head in some sequence: the tensor-memory kernel, which also serves the call's
     // single tokens (with a rule, unless the decode kernel is sooner); lists of selected blocks are the decode kernel's (each token and kv head has its own keys).
-    const bool chunk = !selected && (rule ? !decode_is_sooner(ctx, seqs, a.window) : (int64_t)seqs.max_tokens * ctx->group > kDecodeRows);
+    const bool few = rule ? decode_is_sooner(ctx, seqs, a.window) : (int64_t)seqs.max_tokens * ctx->group <= kDecodeRows;
+    const bool chunk = !selected && !few;
     const int64_t rows = paged_partial_rows(ctx->num_sms, chunk);
     a.part_o = reinterpret_cast<float *>(ctx->paged_ws());
     a.part_ml = reinterpret_cast<float2 *>(ctx->paged_ws() + rows * kHeadDim * 4);

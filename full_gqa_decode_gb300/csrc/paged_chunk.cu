@@ -26,8 +26,8 @@
 // MMA warp (only the first CTA's issues; its barriers collect the arrivals of
 // both CTAs); and stage warps, which hand a landed stage on to the MMA warp:
 // with bf16 pages one warp (scored rows: two), which only zeroes the V rows of
-// positions that no row sees (they may hold NaN); with E4M3 pages four warps for K and four for V,
-// which read the codes a tile ahead into registers and convert them to f16
+// positions that no row sees (they may hold NaN); with E4M3 pages four warps for
+// K and four for V, which read the codes a tile ahead into registers and convert them to f16
 // (exact) in the layout of the MMAs.
 //
 // Rows keep the reference m of their weights until a score passes it by 8 (in
@@ -48,7 +48,7 @@
 // reference stays, its maximum is not looked for.  Measured: 4096 tokens behind
 // 28672 with scores capped at 50 690 us (1.49 PFLOP/s; 1093 unrolled, with a
 // reciprocal a score and rescaled at 8), uncapped 675, with a bias by distance
-// 685; over E4M3 pages 1057, 913 and 990; documents of some 60 to 2500 tokens
+// 685; over E4M3 pages 1057, 890 and 990; documents of some 60 to 2500 tokens
 // packed into 16384 130 us (an item is about 7 tiles and, of a fifth of its time,
 // set-up and drain); prefix prompts at group 8 over E4M3 pages 319 us.
 #include <climits>
@@ -93,7 +93,7 @@ constexpr int kSnap = 16, kSnapFew = 12, kFewRows = 64;
 constexpr int kMinTiles = 2 + kItemCost;              // shortest share of a pair
 constexpr float kRescale = 8.f;
 // Scored rows over bf16 pages let a score pass the reference by 32: bf16 weights have fp32's range, so 2^32 a weight costs
-// nothing but range of the sums (values up to 2^78 for 2^17 keys).  Capped scores spread over 8 (natural units) passed 8 in
+// nothing but range of the sums (values up to 2^77 for 2^17 keys).  Capped scores spread over 8 (natural units) passed 8 in
 // most tiles of a warp's rows: 4096 tokens behind 28672 957 us uncapped with 8.
 constexpr float kRescaleWide = 32.f;
 constexpr uint32_t kTmemCols = 512, kOutCol = 256;
@@ -233,8 +233,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// The same for what was done in tensor memory alone: tcgen05.fence::before_thread_sync orders that before any arrival, and a
-// release of everything else, which the softmax would wait for in every tile, is not needed.
+// The same for what was done in tensor memory alone: each lane has waited for its own accesses there and fenced them
+// (tcgen05.fence::before_thread_sync) before the warp came together; a release of everything else, which the softmax would
+// wait for in every tile, is not needed.
 __device__ __forceinline__ void mbar_arrive_remote_tmem(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -470,6 +471,9 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
     paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8, SCORED = RULE != RULE_NONE, kCap = RULE & RULE_CAP, kBias = RULE & RULE_BIAS;
+    // Scores in loops of 16, weights in the columns of their own half's scores: rules, and spans over E4M3 pages, where 64 held
+    // scores spill (4096 tokens behind 28672 911 us, so 882; over bf16 pages 676 held and 661, but documents 130 and 140).
+    constexpr bool kPartP = kCap || kBias || (SCORED && kFp8);
     constexpr int kStage = stage_warps(KV), kStageWarp = first_stage_warp(KV);
     uint8_t *ring = smem + kQBytes;
     float *xm = reinterpret_cast<float *>(smem + kXmOff);
@@ -660,7 +664,8 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                         if (!dead) {
 #pragma unroll
                             for (int t = 0; t < 8; ++t)
-                                pair_mma_ts(tmem + kOutCol, p + 8 * t + ((kCap || kBias) && t >= 4 ? 32 : 0), vd + v_step[t], kIdO, i > 2 || t > 0);
+                                pair_mma_ts(tmem + kOutCol, p + 8 * t + (kPartP && t >= 4 ? 32 : 0), vd + v_step[t], kIdO,
+                                            i > 2 || t > 0);
                         }
                         if (kFp8) pair_commit(&bar[BAR_EMPTY + pos.st]);
                         pos.step();
@@ -922,7 +927,7 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
             if (!idle) {
                 tc_fence_after();
                 const int key0 = w.key0(k) + half * 64;
-                if constexpr (kCap || kBias) {
+                if constexpr (kPartP) {
                     const RulePart part{buf + half * 64, scale, slope, (float)(key0 - pos), lo_pos - key0, hi_pos - key0};
                     // Tiles that every row sees whole mostly leave the rows' references as they are, which a bound on their scores
                     // shows: the cap is monotone, and the bias lies between those of the part's ends.
@@ -952,7 +957,8 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                         rescale_output(k, alpha);
                     }
                     const float ref = m == -INFINITY ? 0.f : m - lift;
-                    l += careful ? rule_weights<kFp8, kCap, kBias, true>(a, part, ref) : rule_weights<kFp8, kCap, kBias, false>(a, part, ref);
+                    l += careful ? rule_weights<kFp8, kCap, kBias, true>(a, part, ref)
+                                 : rule_weights<kFp8, kCap, kBias, false>(a, part, ref);
                 } else {
                     float s[64];
                     tmem_ld64(buf + half * 64, s);

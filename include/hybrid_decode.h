@@ -671,7 +671,8 @@ hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batc
  *              (HD_DEVERR_SPAN) and gets NaN, or is served by its own values.
  *   scale      0: 1 / sqrt(head_dim); else 2^-32 to 2^32, HD_ERR_UNSUPPORTED beyond
  * HD_ERR_INVALID_ARG when scale or softcap is negative or not finite.  Entries from
- * a sequence's lowest to its highest visible position must be finite.  Weights are
+ * a sequence's lowest to its highest visible position must be finite, values below
+ * 2^77.  Weights are
  * rounded before they meet the values as in attn_paged, by the kernel that serves
  * the call: calls of few rows take the one that an estimate says is sooner. */
 typedef struct {
