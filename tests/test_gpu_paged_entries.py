@@ -212,13 +212,11 @@ def test_in_place_and_keys_alone(hd, orc):
     hd.norm_rope_append_paged(ctx, 1, batch, d["q"], k, v, d["q"], cache, rope=rope)
     torch.cuda.synchronize()
     assert torch.equal(d["q"], q_rot)
-    held = case.held.clone()
     for r in range(case.rows):
         b, p = case.token(r)
         at = case.table[b, p // case.page], slice(None), p % case.page
         assert torch.equal(d["k"][at], pages[at])
     assert hd.hybrid_decode_device_errors(ctx) == 0
-    del held
 
 
 def test_bad_positions_and_sequences_are_flagged_and_nothing_is_stored(hd, orc):
@@ -410,6 +408,54 @@ def test_read_refusals(hd):
     for k, stride in ((good.data_ptr() + 8, 512), (good.data_ptr(), 504), (good.data_ptr(), 516)):
         assert hd._lib.read_paged(ctx.handle, batch.ref, cache.ref, k, stride, None, 0, None) == 1
     hd.read_paged(ctx, batch, cache)   # nothing to read
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_more_sequences_than_a_block_has_threads(hd, kv):
+    """300 sequences of 0 to 2 tokens in one call, on a stream of its own, and in two: the same pages, queries and rows back."""
+    ctx = context(hd, kv=kv, max_batch=512)
+    rng = synth.generator(6)
+    counts = rng.integers(0, 3, 300)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    n = int(offsets[-1])
+    contexts = torch.from_numpy(rng.integers(0, 31, 300).astype(np.int32)).cuda()
+    table = torch.from_numpy(rng.permutation(600).reshape(300, 2).astype(np.int32)).cuda()
+    q, k, v = (synth.normal_bf16(rng, (n, h, D)).cuda() for h in (8, 2, 2))
+    scale = torch.full((2,), 0.01, device="cuda") if kv == "e4m3" else None
+    rope = table_of(hd, "neighbours 72")
+    stream = torch.cuda.Stream()
+
+    def step(parts, stream=None):
+        pages = [torch.zeros(600, 2, 16, D, device="cuda").to(torch.float8_e4m3fn if kv == "e4m3" else torch.bfloat16) for _ in range(2)]
+        bounds = torch.zeros(600, 2, 2, D, dtype=torch.bfloat16, device="cuda")
+        cache = hd.paged_cache(*pages, scale, scale, bounds=bounds)
+        q_rot, rk, rv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+        torch.cuda.synchronize()
+        for a, b in parts:
+            r = slice(int(offsets[a]), int(offsets[b]))
+            batch = hd.paged_batch(table[a:b], contexts[a:b], torch.from_numpy(offsets[a: b + 1] - offsets[a]).cuda(),
+                                   num_tokens=r.stop - r.start, max_tokens=2)
+            torch.cuda.synchronize()
+            hd.norm_rope_append_paged(ctx, 1, batch, q[r], k[r], v[r], q_rot[r], cache, rope=rope, stream=stream)
+            hd.read_paged(ctx, batch, cache, rk[r], rv[r], stream=stream)
+        torch.cuda.synchronize()
+        assert hd.hybrid_decode_device_errors(ctx) == 0
+        return [x.float() for x in (*pages, bounds, q_rot, rk, rv)]
+
+    for a, b in zip(step([(0, 300)], stream), step([(0, 140), (140, 300)])):
+        assert torch.equal(a, b)
+
+
+def test_calls_of_no_tokens(hd):
+    case = PagedCase(324, [(5, 0), (90, 0)])
+    ctx, d = context(hd), case.device()
+    batch, cache = hd.paged_batch(d["table"], d["context"], d["offsets"], num_tokens=0, max_tokens=1), cache_of(hd, d)
+    q, k = (torch.empty(0, h, D, dtype=torch.bfloat16, device="cuda") for h in (8, 2))
+    hd.norm_rope_append_paged(ctx, 1, batch, q, k, k, q, cache, rope=table_of(hd, "halves 64"))
+    hd.read_paged(ctx, batch, cache, k, k)
+    hd.attn_paged_scored(ctx, 1, batch, hd.scoring(softcap=30.0), q, cache, None, q, torch.empty(0, 8, device="cuda"))
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
 
 
 # -------------------------------------------------------- a step of them all --

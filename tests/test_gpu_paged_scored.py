@@ -249,6 +249,19 @@ def test_more_sequences_than_a_warp(hd, orc, long_one):
     check(hd, orc, case, rule_of("all", case), rows=range(0, case.rows, 5))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_more_sequences_than_a_block_has_threads(hd, orc, kv):
+    """Single tokens of 300 sequences, some of which see nothing, and a chunk among them."""
+    rng = np.random.default_rng(4)
+    for spans in ([(int(c), 1) for c in rng.integers(0, 150, 300)],
+                  [(int(c), int(n)) for c, n in zip(rng.integers(0, 60, 400), rng.integers(0, 2, 400))] + [(30, 260)]):
+        single = len(spans) == 300
+        case = PagedCase(223, spans, kv=kv, page=16, single=single)
+        first = np.concatenate([np.full(n, c + n if i % 7 == 3 else max(0, c - 20)) for i, (c, n) in enumerate(spans)])
+        ctx = context(hd, kv=kv, max_batch=512)
+        check(hd, orc, case, Rule(softcap=10.0, first=first), rows=range(0, case.rows, 3), ctx=ctx, max_context=200)
+
+
 @pytest.mark.parametrize("n", [1, 50])
 def test_captured_and_replayed_on_another_stream(hd, orc, n):
     """A captured call takes new queries, contexts and lists from the same tensors."""
