@@ -48,7 +48,7 @@
 // reference stays, its maximum is not looked for.  Measured: 4096 tokens behind
 // 28672 with scores capped at 50 690 us (1.49 PFLOP/s; 1093 unrolled, with a
 // reciprocal a score and rescaled at 8), uncapped 675, with a bias by distance
-// 685; over E4M3 pages 1057, 890 and 990; documents of some 60 to 2500 tokens
+// 685; over E4M3 pages 1043, 861 and 990; documents of some 60 to 2500 tokens
 // packed into 16384 130 us (an item is about 7 tiles and, of a fifth of its time,
 // set-up and drain); prefix prompts at group 8 over E4M3 pages 319 us.
 #include <climits>
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool kFp8 = KV == KV_FP8, SCORED = RULE != RULE_NONE, kCap = RULE & RULE_CAP, kBias = RULE & RULE_BIAS;
     // Scores in loops of 16, weights in the columns of their own half's scores: rules, and spans over E4M3 pages, where 64 held
-    // scores spill (4096 tokens behind 28672 911 us, so 882; over bf16 pages 676 held and 661, but documents 130 and 140).
+    // scores spill (4096 tokens behind 28672 911 us, so 885; over bf16 pages 676 held and 661, but documents 130 and 140).
     constexpr bool kPartP = kCap || kBias || (SCORED && kFp8);
     constexpr int kStage = stage_warps(KV), kStageWarp = first_stage_warp(KV);
     uint8_t *ring = smem + kQBytes;
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                     const int row = sw * 32 + lane;
                     uint8_t *qrow = smem + row * 128;
                     uint32_t top = 0;
-#pragma unroll 8
+#pragma unroll 4   // 8 spilled more: 4096 tokens behind 28672 885 and 861 us
                     for (int c = 0; c < 32; ++c) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
                         const uint32_t cw[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu};
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                     }
                     const int ex = min(max((int)(top >> 7), 1), 253);
                     const float down = copysignf(__uint_as_float((uint32_t)(254 - ex) << 23), a.k_scale[w.h]);
-#pragma unroll 8
+#pragma unroll 4
                     for (int c = 0; c < 32; ++c) {
                         uint4 *at = reinterpret_cast<uint4 *>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
                         uint4 x = *at;
