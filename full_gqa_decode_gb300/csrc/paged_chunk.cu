@@ -356,9 +356,15 @@ struct RulePart {
     float slope, far;   // bias of a position's distance, and the first key's position less the query's
     int from, to;       // visible ones of the 64
 };
-// Scores c .. c + 15 by the rule, less ref.  EDGE: what is not visible gives -inf, and scores may pass what the cap's exponents
-// reach.
-template <bool CAP, bool BIAS, bool EDGE>
+// Two products that stay rounded: a packed one and a sum behind it are compiled to one step, a single one by its intrinsic is not.
+__device__ __forceinline__ float2 rounded2(float x, float y, float scale) {
+    return make_float2(__fmul_rn(x, scale), __fmul_rn(y, scale));
+}
+// Scores c .. c + 15 by the rule, LESS: less ref.  A score is rounded before ref is taken off, as it was when ref was found:
+// rounding is monotone, so no score passes ref by more than the maximum did, however large both are (in one step, a product
+// of 2^28 rounded for ref and not for the weight left exponents of some 16).  EDGE: what is not visible gives -inf, and
+// scores may pass what the cap's exponents reach.
+template <bool CAP, bool BIAS, bool EDGE, bool LESS>
 __device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &r, int c, float ref, float (&s)[16]) {
     tmem_ld16(r.cols + c, s);
     const int from = r.from - c, to = r.to - c;
@@ -369,10 +375,15 @@ __device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &
     if (CAP) {
         const float z = r.scale * a.two_over_cap;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) capped4<EDGE>(a, z, a.cap - ref, *reinterpret_cast<float(*)[4]>(s + i));
+        for (int i = 0; i < 16; i += 4) capped4<EDGE>(a, z, LESS ? a.cap - ref : a.cap, *reinterpret_cast<float(*)[4]>(s + i));
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], r.scale, -ref);
+        for (int i = 0; i < 16; i += 2) {
+            float2 x = rounded2(s[i], s[i + 1], r.scale);
+            if (LESS) x = add2(x, make_float2(-ref, -ref));
+            s[i] = x.x;
+            s[i + 1] = x.y;
+        }
     }
     if (BIAS) {
         const float far = r.far + (float)c;
@@ -396,7 +407,7 @@ __device__ __forceinline__ float rule_max(const PagedAttnArgs &a, const RulePart
 #pragma unroll 1
     for (int c = 0; c < 64; c += 16) {
         float s[16];
-        ruled16<CAP, BIAS, EDGE>(a, r, c, 0.f, s);
+        ruled16<CAP, BIAS, EDGE, false>(a, r, c, 0.f, s);
         top = max16(s, top);
     }
     return top;
@@ -421,7 +432,7 @@ __device__ __forceinline__ float rule_weights(const PagedAttnArgs &a, const Rule
     for (int c = 0; c < 64; c += 16) {
         float s[16];
         uint32_t pw[8];
-        ruled16<CAP, BIAS, EDGE>(a, r, c, ref, s);
+        ruled16<CAP, BIAS, EDGE, true>(a, r, c, ref, s);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = fast_exp2(s[i]);
 #pragma unroll
@@ -879,6 +890,12 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
         auto soft_sync = [&]() { asm volatile("bar.sync 5, 256;" ::: "memory"); };
         const float lift = kFp8 ? 7.f : 0.f;
         constexpr float kLimit = SCORED && !kFp8 ? kRescaleWide : kRescale;
+        // What a row's weights are taken against: its reference less the lift.  Scored rows may have references beyond 2^23,
+        // where the difference rounds: up, so that no weight is lifted by more.
+        auto lifted = [&](float x) { return SCORED && kFp8 ? __fadd_ru(x, -lift) : x - lift; };
+        // Whether a maximum asks for a new reference (from -inf: always).  The difference is exact where it is small, a sum
+        // of a large reference and the limit is not.
+        auto passes = [&](float top, float m) { return SCORED ? top - m > kLimit : top > m + kLimit; };
         int blocks = 0, tiles = 0;   // before this segment
         for (uint32_t seg = 0; more; ++seg) {
         float m = -INFINITY, l = 0.f, scale = SCORED ? a.qscale : kQScale;
@@ -936,11 +953,11 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                     if (!moves) {
                         const float raw = raw_max(part), z = raw * (scale * a.two_over_cap);
                         careful = kCap && __any_sync(0xffffffffu, z > kCapReach);
-                        float top = kCap ? capped(a, z) : raw * scale;
+                        float top = kCap ? capped(a, z) : __fmul_rn(raw, scale);   // rounded as the scores are
                         if (kBias)
                             top = fmaf(-slope, slope > 0.f ? fmaxf(fmaxf(part.far, -63.f - part.far), 0.f)
                                                            : fmaxf(fabsf(part.far), fabsf(part.far + 63.f)), top);
-                        moves = any_of_barrier(1 + (warp & 3), 64, top > m + kLimit);   // m = -inf: any score
+                        moves = any_of_barrier(1 + (warp & 3), 64, passes(top, m));   // m = -inf: any score
                     }
                     if (moves) {
                         float top = careful ? rule_max<kCap, kBias, true>(a, part) : rule_max<kCap, kBias, false>(a, part);
@@ -949,14 +966,14 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                         pair_sync();
                         top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
                         float alpha = 1.f;
-                        if (top > m + kLimit) {
-                            if (m != -INFINITY) alpha = fast_exp2(m - top);   // else nothing to scale: l and the output are zero
+                        if (passes(top, m)) {
+                            if (m != -INFINITY) alpha = fast_exp2(lifted(m) - lifted(top));   // else l and the output are zero
                             m = top;
                             l *= alpha;
                         }
                         rescale_output(k, alpha);
                     }
-                    const float ref = m == -INFINITY ? 0.f : m - lift;
+                    const float ref = m == -INFINITY ? 0.f : lifted(m);
                     l += careful ? rule_weights<kFp8, kCap, kBias, true>(a, part, ref)
                                  : rule_weights<kFp8, kCap, kBias, false>(a, part, ref);
                 } else {
@@ -975,20 +992,23 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                     x[half * kCtaRows + row] = top;
                     pair_sync();
                     top = fmaxf(top, x[(half ^ 1) * kCtaRows + row]);
-                    top *= scale;
+                    top = SCORED ? __fmul_rn(top, scale) : top * scale;
                     float alpha = 1.f;
-                    if (top > m + kLimit) {   // also a row's first key: m = -inf
+                    if (passes(top, m)) {   // also a row's first key: m = -inf
                         alpha = fast_exp2(m - top);   // m = -inf: 0
                         m = top;
                         l *= alpha;
                     }
                     rescale_output(k, alpha);
-                    const float ref = m == -INFINITY ? 0.f : m - lift;
+                    const float ref = m == -INFINITY ? 0.f : lifted(m);
                     uint32_t pw[32];
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float p0 = fast_exp2(fmaf(s[2 * i], scale, -ref)), p1 = fast_exp2(fmaf(s[2 * i + 1], scale, -ref));
+                        float2 x = make_float2(s[2 * i], s[2 * i + 1]);
+                        if (SCORED) x = add2(rounded2(x.x, x.y, scale), make_float2(-ref, -ref));   // as in ruled16
+                        else x = make_float2(fmaf(x.x, scale, -ref), fmaf(x.y, scale, -ref));
+                        const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
                         sum[i & 1] += p0;
                         sum[2 + (i & 1)] += p1;
                         pw[i] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
@@ -1013,7 +1033,7 @@ __global__ void __launch_bounds__(chunk_threads(KV, RULE != RULE_NONE), 1)
                     pair_sync();
                 }
                 const bool whole = w.L == w.t.units, live = row < rows_here;
-                const float ml_m = m - lift;
+                const float ml_m = lifted(m);
                 const int slot = w.u == 0 ? 2 * pair + 1 : 2 * pair;
                 const size_t prow = (size_t)slot * kTileRows + r;
                 const float vscale = kFp8 ? a.v_scale[w.h] : 1.f;
