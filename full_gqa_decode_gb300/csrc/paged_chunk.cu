@@ -362,7 +362,8 @@ __device__ __forceinline__ float2 rounded2(float x, float y, float scale) {
 }
 // Scores c .. c + 15 by the rule, LESS: less ref.  A score is rounded before ref is taken off, as it was when ref was found:
 // rounding is monotone, so no score passes ref by more than the maximum did, however large both are (in one step, a product
-// of 2^28 rounded for ref and not for the weight left exponents of some 16).  EDGE: what is not visible gives -inf, and
+// of 2^28 rounded for ref and not for the weight left exponents of some 16), and so with its bias, which is rounded with it.
+// EDGE: what is not visible gives -inf, and
 // scores may pass what the cap's exponents reach.
 template <bool CAP, bool BIAS, bool EDGE, bool LESS>
 __device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &r, int c, float ref, float (&s)[16]) {
@@ -375,12 +376,12 @@ __device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &
     if (CAP) {
         const float z = r.scale * a.two_over_cap;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) capped4<EDGE>(a, z, LESS ? a.cap - ref : a.cap, *reinterpret_cast<float(*)[4]>(s + i));
+        for (int i = 0; i < 16; i += 4) capped4<EDGE>(a, z, LESS && !BIAS ? a.cap - ref : a.cap, *reinterpret_cast<float(*)[4]>(s + i));
     } else {
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             float2 x = rounded2(s[i], s[i + 1], r.scale);
-            if (LESS) x = add2(x, make_float2(-ref, -ref));
+            if (LESS && !BIAS) x = add2(x, make_float2(-ref, -ref));
             s[i] = x.x;
             s[i + 1] = x.y;
         }
@@ -388,7 +389,13 @@ __device__ __forceinline__ void ruled16(const PagedAttnArgs &a, const RulePart &
     if (BIAS) {
         const float far = r.far + (float)c;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = fmaf(-r.slope, fabsf(far + (float)i), s[i]);
+        for (int i = 0; i < 16; i += 2) {
+            const float2 d = add2(make_float2(far, far), make_float2((float)i, (float)(i + 1)));
+            float2 x = make_float2(fmaf(-r.slope, fabsf(d.x), s[i]), fmaf(-r.slope, fabsf(d.y), s[i + 1]));
+            if (LESS) x = add2(x, make_float2(-ref, -ref));
+            s[i] = x.x;
+            s[i + 1] = x.y;
+        }
     }
     if (EDGE) {
 #pragma unroll

@@ -1,5 +1,5 @@
-"""GPU tests of the paged calls' far ends: scores so large that only the largest
-counts, against what is then left of the formula."""
+"""GPU tests of the paged calls' far ends: scores and biases so large that only the
+largest counts, against what is then left of the formula."""
 import numpy as np
 import pytest
 import torch
@@ -20,7 +20,7 @@ def _need_gpu():
 
 SPANS = {   # chunks, and a chunk whose items are cut between CTAs
     "chunks": [(0, 150), (300, 90)],
-    "cut": [(9000, 70), (5, 20)],
+    "cut": [(4000, 70), (5, 20)],
 }
 
 
@@ -93,24 +93,26 @@ def check_largest(orc, case, rule, out, lse, rows, gap):
                 assert abs(head - top - np.log(n)) <= 2.0 ** -20 * (1 + abs(top)) + 2.0 ** -6, (r, head, top, n)
 
 
+@pytest.mark.parametrize("slopes", [False, True])   # slopes of zero: the kernels of biased scores
 @pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 32])
 @pytest.mark.parametrize("spans", sorted(SPANS))
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_large_scales(hd, orc, kv, spans, scale):
+def test_large_scales(hd, orc, kv, spans, scale, slopes):
     case = sharp_case(spans, kv)
-    rule = Rule(scale=scale)
+    rule = Rule(scale=scale, slopes=np.zeros(case.q_heads, np.float32) if slopes else None)
     out, lse = run(hd, case, rule)
     check_largest(orc, case, rule, out, lse, range(0, case.rows, 7), 2 * scale)
 
 
+@pytest.mark.parametrize("slopes", [False, True])
 @pytest.mark.parametrize("scale", [2.0 ** 23, 2.0 ** 28, 2.0 ** 32])
 @pytest.mark.parametrize("spans", sorted(SPANS))
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_large_scales_of_any_queries(hd, orc, kv, spans, scale):
+def test_large_scales_of_any_queries(hd, orc, kv, spans, scale, slopes):
     """Weights are never negative, so an output lies between its column's least and largest visible value, to the weights'
     rounding and its own of the largest magnitude; the largest score is near lse."""
     case = PagedCase(402, SPANS[spans], kv=kv, single=spans == "single", page=32)
-    rule = Rule(scale=scale)
+    rule = Rule(scale=scale, slopes=np.zeros(case.q_heads, np.float32) if slopes else None)
     out, lse = run(hd, case, rule)
     assert np.isfinite(out).all() and np.isfinite(lse).all()
     for r in range(0, case.rows, 9):
@@ -132,3 +134,22 @@ def test_the_smallest_scale(hd, orc, kv, spans):
     rule = Rule(scale=2.0 ** -32)
     out, lse = run(hd, case, rule)
     check_largest(orc, case, rule, out, lse, range(0, case.rows, 7), 1.0)
+
+
+STEEP = np.array([1e3, 1e4, 1e5, 1e6, -1e3, -1e5, 300.0, -1e6], np.float32)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 10.0])
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("spans", sorted(SPANS))
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_steep_biases(hd, orc, kv, spans, far, softcap):
+    """Biases of up to 10^10 in pieces far from their query, where the nearest visible key counts alone (or the farthest); all
+    that is visible far behind the query."""
+    case = PagedCase(404, SPANS[spans], kv=kv, single=spans == "single", page=32)
+    last = None
+    if far:
+        last = np.concatenate([np.full(n, min(c, 100), np.int64) for c, n in case.spans])
+    rule = Rule(softcap=softcap, slopes=STEEP, last=last)
+    out, lse = run(hd, case, rule)
+    check_largest(orc, case, rule, out, lse, range(0, case.rows, 7), 200.0)
