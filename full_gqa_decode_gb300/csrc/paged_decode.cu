@@ -165,6 +165,11 @@ struct DecodeRowsState {
     RowSpan span[SCORED ? 2 : 1];     // their visible positions ..
     float slope[SCORED ? 2 : 1];      // .. and biases of a position's distance, log2 units
 
+    // What a row's weights are taken against: its maximum less the lift.  Scored rows may have maxima beyond 2^23, where the
+    // difference rounds: up, so that no weight is lifted by more (2^16, which rounding to nearest gave from 2^27 on, is
+    // infinite in f16).
+    __device__ static __forceinline__ float lifted(float m) { return SCORED && F16 ? __fadd_ru(m, -kLift) : m - kLift; }
+
     __device__ void init_rows() {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -201,7 +206,8 @@ struct DecodeRowsState {
                 v0 = k0 >= lo && k0 <= hi;
                 v1 = k0 + 8 >= lo && k0 + 8 <= hi;
             }
-            float x0 = s[e] * scale[e], x1 = s[2 + e] * scale[e];
+            // Scored rows: rounded as their maximum is, whatever is taken off behind.
+            float x0 = SCORED ? __fmul_rn(s[e], scale[e]) : s[e] * scale[e], x1 = SCORED ? __fmul_rn(s[2 + e], scale[e]) : s[2 + e] * scale[e];
             if constexpr (SCORED) {
                 if (a.cap != 0.f) {
                     x0 = capped(a, x0 * a.two_over_cap);
@@ -218,9 +224,9 @@ struct DecodeRowsState {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float mn = fmaxf(m_run[e], mx);
-            alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
-            p[e] = v0 ? fast_exp2(x0 - (mn - kLift)) : 0.f;
-            p[2 + e] = v1 ? fast_exp2(x1 - (mn - kLift)) : 0.f;
+            alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(SCORED && F16 ? lifted(m_run[e]) - lifted(mn) : m_run[e] - mn);
+            p[e] = v0 ? fast_exp2(x0 - lifted(mn)) : 0.f;
+            p[2 + e] = v1 ? fast_exp2(x1 - lifted(mn)) : 0.f;
             l_run[e] = fmaf(l_run[e], alpha[e], p[e] + p[2 + e]);
             m_run[e] = mn;
         }
@@ -258,7 +264,7 @@ struct DecodeRowsState {
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (lane < 4) {
-                mx[warp * kDecodeRows + 2 * lane + e] = m_run[e] - kLift;
+                mx[warp * kDecodeRows + 2 * lane + e] = lifted(m_run[e]);
                 sums[warp * kDecodeRows + 2 * lane + e] = l;
             }
         }

@@ -18,7 +18,9 @@ def _need_gpu():
         pytest.skip("needs a CUDA GPU")
 
 
-SPANS = {   # chunks, and a chunk whose items are cut between CTAs
+SPANS = {   # one token, calls of few rows, chunks, and a chunk whose items are cut between CTAs
+    "single": [(0, 1), (5, 1), (700, 1), (2047, 1), (9000, 1)],
+    "few": [(0, 2), (250, 3), (1000, 1)],
     "chunks": [(0, 150), (300, 90)],
     "cut": [(4000, 70), (5, 20)],
 }
