@@ -236,7 +236,15 @@ __global__ void __launch_bounds__(kEntryThreads, 4) paged_norm_append_kernel(con
             }
         }
     }
-    if (e.bounds) store_bounds(e, page, h, fp8, (p0 & (ps - 1)) == 0, ld, lo, hi, edge);
+    if (!e.bounds) return;
+    bool fresh = (p0 & (ps - 1)) == 0;
+    if (a.positions) {   // rows that were not stored leave the bounds as they are: a thread looks at each
+        static_assert(kEntryThreads >= 1 << kMaxPageShift, "a run has at most as many rows as a CTA threads");
+        const int pos = p0 + tid, r0 = q.row0 - q.ctx;
+        if (!__syncthreads_or(pos < p1 && angle_row(a, r0 + pos, pos) >= 0)) return;
+        fresh = fresh && angle_row(a, r0 + p0, p0) >= 0;
+    }
+    store_bounds(e, page, h, fp8, fresh, ld, lo, hi, edge);
 }
 
 }  // namespace

@@ -646,7 +646,8 @@ typedef struct {
  *              hold those (a sequence that reaches past the table is a sequence
  *              that cannot be served).  A given position outside the table is
  *              flagged (HD_DEVERR_CONTEXT_PLAN), and its row's entry and q_rot
- *              stay as they were.
+ *              stay as they were, and the page's bounds as the other rows leave
+ *              them (a page whose first slot is not written is not begun anew).
  * The other arguments and errors are rope_append_paged's; HD_ERR_INVALID_ARG for
  * a norm or table outside the limits given at their structs. */
 hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batch *batch, const hd_head_norm *norm,

@@ -1,0 +1,56 @@
+"""GPU tests of the normed append's edges and of what it stores, and of its tables
+of angles.  Tolerances as in test_gpu_paged_entries.py."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from harness import FULL, assert_bits_equal
+from paged_harness import D, PagedCase, reference_append
+from test_gpu_paged import cache_of, context
+from test_gpu_paged_entries import APPEND_SPANS, angles, check_append, reference, reference_read, table_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_bounds_of_pages_whose_rows_are_not_all_stored(hd, kv):
+    """Rows whose given position is not in the table stay out of the bounds; a page that gets no row keeps its bounds to the
+    bit, and one whose first slot is not written keeps what it had among them."""
+    case = PagedCase(501, [(0, 40), (5, 8), (20, 3), (16, 16)], kv=kv, page=16, appended=False)
+    ctx, d = context(hd, kv=kv), case.device()
+    k, v = (synth.normal_bf16(case.rng, (case.rows, case.kv_heads, D), 0.5).cuda() for _ in range(2))
+    held = synth.normal_bf16(case.rng, (case.pool, case.kv_heads, 2, D))
+    held[:, :, 0] -= 0.5
+    held[:, :, 1] += 0.5
+    bad = np.zeros(case.rows, bool)
+    bad[:16] = True                  # all of a page that the call starts
+    bad[[16, 19]] = True             # the first slot of one, and another
+    bad[33:40] = True                # all but the first slot
+    bad[40:48] = True                # all of a page that has entries
+    bad[51 + 1: 51 + 16] = True      # one row in a warp, none in the others
+    held[case.table[1, 0]] = float("nan")
+    held[case.table[0, 0], 0, 0, :2] = float("inf")
+    pos = np.where(bad, 102, np.arange(case.rows) % 102)
+    bounds = held.cuda()
+    hd.norm_rope_append_paged(ctx, 1, case.batch_of(hd, d), None, k, v, None, cache_of(hd, d, bounds), rope=table_of(hd, "halves 64", 102),
+                              positions=torch.from_numpy(pos.astype(np.int32)).cuda())
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 4
+    pages = d["k"].cpu()
+    if kv == "e4m3":
+        pages = pages.view(torch.float8_e4m3fn)
+    want = held.float()
+    for r in np.flatnonzero(~bad):   # in order: a page's first slot comes first
+        b, p = case.token(r)
+        page, x = case.table[b, p // 16], pages[case.table[b, p // 16], :, p % 16].float()
+        if p % 16 == 0:
+            want[page] = x[:, None]
+        want[page, :, 0], want[page, :, 1] = torch.minimum(want[page, :, 0], x), torch.maximum(want[page, :, 1], x)
+    assert_bits_equal(bounds, synth.bits(want.to(torch.bfloat16)), "bounds")
