@@ -86,7 +86,8 @@ __device__ __forceinline__ void norm_rotate(const PagedNormArgs &a, const uint4 
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-        const float r = rsqrtf(fmaf(warp_sum(sq), 1.f / kHeadDim, a.eps));
+        // The mean in two steps of 2^-4: the sum of a whole head of values of 2^60 alone is infinite.
+        const float r = rsqrtf(fmaf(warp_sum(sq * (1.f / 16)), 16.f / kHeadDim, a.eps));
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
     }

@@ -54,3 +54,14 @@ def test_bounds_of_pages_whose_rows_are_not_all_stored(hd, kv):
             want[page] = x[:, None]
         want[page, :, 0], want[page, :, 1] = torch.minimum(want[page, :, 0], x), torch.maximum(want[page, :, 1], x)
     assert_bits_equal(bounds, synth.bits(want.to(torch.bfloat16)), "bounds")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_heads_of_the_largest_values(hd, orc, kv):
+    """Every value of a head +-2^60: its squares sum to 2^128, which fp32 does not hold."""
+    case = PagedCase(502, [(5, 40), (1, 3)], page=16, kv=kv, appended=False)
+    signs = lambda shape: torch.from_numpy(np.where(case.rng.random(shape) < 0.5, -1.0, 1.0)).to(torch.bfloat16)  # noqa: E731
+    case.q[:4] = signs(case.q[:4].shape) * 2.0 ** 60
+    case.q[4] = signs(case.q[4].shape) * 1.9921875 * 2.0 ** 59
+    check_append(hd, orc, case, "halves 256 bands")
+    check_append(hd, orc, case, "neighbours 72", kind=None)
