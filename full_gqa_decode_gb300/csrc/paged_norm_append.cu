@@ -104,6 +104,9 @@ __device__ __forceinline__ uint4 to_bf16(const float (&y)[8]) {
     return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
 }
 
+// A call, as it is hardly ever wanted.
+__device__ __noinline__ float quotient(float x, float y) { return __fdiv_rn(x, y); }
+
 // The table row of new token r, at position p: -1 when a given position is not in the table.
 __device__ __forceinline__ int angle_row(const PagedNormArgs &a, int r, int p) {
     if (!a.positions) return p;
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kEntryThreads, 4) paged_norm_append_kernel(con
     const bool fp8 = e.kv_type == KV_FP8;
     const Recip vr = recip_of(fp8 ? e.v_scale[h] : 1.f);
     const float k_inv = fp8 ? 1.f / e.k_scale[h] : 1.f;
+    const bool no_inv = fp8 && recip_of(e.k_scale[h]).odd;
     float w[8];
     load_weights(weights_of(a.k_weight, a, h), a.f32_weights, a.offset, ld, w);
     uint32_t lo[4], hi[4];   // of the keys' dims: bf16 pairs, or f16 pairs, which hold every E4M3 value
@@ -207,9 +211,11 @@ __global__ void __launch_bounds__(kEntryThreads, 4) paged_norm_append_kernel(con
             norm_rotate<NEIGHBOURS>(a, x[i], w, c[i], s[i], ld.i >= 0, y);
             const size_t o = (size_t)page * e.page_stride + ((size_t)h * ps + (pos & (ps - 1))) * kHeadDim;
             if (fp8) {
-                // Codes of y times the scale's reciprocal: two more roundings to 2^-24 before the one to E4M3.
-                const uint32_t cx = e4m3x4(y[0] * k_inv, y[1] * k_inv, y[2] * k_inv, y[3] * k_inv);
-                const uint32_t cy = e4m3x4(y[4] * k_inv, y[5] * k_inv, y[6] * k_inv, y[7] * k_inv);
+                // Codes of y times the scale's reciprocal: two more roundings to 2^-24 before the one to E4M3.  Of their
+                // quotient where the reciprocal is no normal number: infinite, it would make a NaN of a zero.
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = no_inv ? quotient(y[j], e.k_scale[h]) : y[j] * k_inv;
+                const uint32_t cx = e4m3x4(y[0], y[1], y[2], y[3]), cy = e4m3x4(y[4], y[5], y[6], y[7]);
                 uint8_t *kd = static_cast<uint8_t *>(e.cache_k) + o;
                 if (NEIGHBOURS) {
                     *reinterpret_cast<uint2 *>(kd + ld.d0) = make_uint2(cx, cy);

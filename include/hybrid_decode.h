@@ -637,7 +637,8 @@ typedef struct {
 /* rope_append_paged for such models: norms the new queries and keys per head, then
  * rotates them by `rope`'s angles, in one pass, and stores keys and values in
  * their pages with the pages' bounds.  Norm and rotation are evaluated in fp32 and
- * rounded once, to bf16 or to E4M3 of the product with the scale's reciprocal;
+ * rounded once, to bf16 or to E4M3 of the product with the scale's reciprocal (of the
+ * quotient, where that reciprocal is no normal fp32 number);
  * values are stored as rope_append_paged stores them, bit for bit.
  *   norm       NULL: none (rotation alone)
  *   rope       NULL: the context's own angles of the layer's type, in halves

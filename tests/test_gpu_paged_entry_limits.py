@@ -65,3 +65,40 @@ def test_heads_of_the_largest_values(hd, orc, kv):
     case.q[4] = signs(case.q[4].shape) * 1.9921875 * 2.0 ** 59
     check_append(hd, orc, case, "halves 256 bands")
     check_append(hd, orc, case, "neighbours 72", kind=None)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -130, 2.0 ** -149, 2.0 ** -127, 3e38])
+@pytest.mark.parametrize("name", ["halves 64", "neighbours 72"])
+def test_scales_without_a_reciprocal(hd, orc, name, scale):
+    """K scales whose reciprocal is infinite or subnormal: zeros stay zeros, what is beyond 448 saturates, and values of the
+    scale's own size are coded as their quotients."""
+    case = PagedCase(503, [(5, 40), (1, 3)], kv="e4m3", page=16, appended=False)
+    case.k_scale = torch.full((case.kv_heads,), scale, dtype=torch.float32)
+    rng, ctx, d = case.rng, context(hd, kv="e4m3"), case.device()
+    k = torch.from_numpy(rng.standard_normal((case.rows, case.kv_heads, D)) * min(100 * scale, 2.0 ** 125))
+    k[0] = 0.0
+    k[1] = torch.from_numpy(np.where(rng.random(k[1].shape) < 0.5, -1.0, 1.0)) * 2.0 ** 100   # beyond 448, but for 3e38: zero
+    k[2, :, ::3] = 0.0
+    k = k.to(torch.bfloat16)
+    hd.norm_rope_append_paged(ctx, 1, case.batch_of(hd, d), None, k.cuda(), k.cuda(), None, cache_of(hd, d), rope=table_of(hd, name),
+                              norm=False)
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    at = [case.token(r) for r in range(case.rows)]
+    cs, sn, amp = angles(hd, name, [p for _, p in at])
+    rot, layout = (64, 0) if name == "halves 64" else (72, 1)
+    z, _ = reference(k, None, 0.0, cs, sn, amp, layout, rot, norm=False)
+    rows = torch.stack([d["k"][case.table[b, p // 16], :, p % 16] for b, p in at])
+    got = orc.e4m3_to_f64(synth.bits(rows)).reshape(z.shape)
+    sc = float(case.k_scale[0])
+    # e: the rotation's fp32 error, and subnormal products and sums (three half steps of 2^-149) over the scale; the
+    # quotient's half step; then half a code's step.
+    a = np.abs(z)
+    other = np.zeros_like(a)
+    x = np.abs(k.double().numpy())
+    other[..., :rot] = np.repeat(x[..., :rot].max(-1, keepdims=True), rot, -1) * amp
+    e = 2.0 ** -19 * (a + other) / sc + 1.5 * 2.0 ** -149 / sc * (a > 0) + 2.0 ** -22 * np.minimum(a / sc, 1e6)
+    t = np.clip(z / sc, -448, 448)
+    over = np.abs(got - t) - (np.maximum(2.0 ** -4 * (np.abs(t) + e), 2.0 ** -10) + e)
+    assert np.isfinite(got).all() and (got[0] == 0).all()
+    assert (over <= 0).all(), f"{over.max():.3e} over the bound"
