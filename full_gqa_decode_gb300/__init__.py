@@ -677,7 +677,8 @@ def rope_table(rotary_dim: int, positions: int, theta: float = 1.0e4, layout: in
     """A table of ``positions`` rows of angles for norm_rope_append_paged, made once for a model:
     HD_ROPE_PLAIN, or scaled for long contexts (LINEAR, RAMP, BANDS; include/hybrid_decode.h has the
     formulas), turning dims in HD_ROPE_HALVES or as HD_ROPE_NEIGHBOURS.  ``table``: float32
-    [positions, rotary_dim / 2, 2] on the current device to fill (default: a new one)."""
+    [positions, rotary_dim / 2, 2] on the current device to fill (default: a new one, of ``stream``'s
+    memory when one is given: other streams wait for that one before they use the table)."""
     p = _rope_params(rotary_dim, theta, scaling, factor, original_context, slow, fast, amplitude)
     f, m = (ctypes.c_double * 128)(), ctypes.c_double()
     _check(_lib.hd_rope_frequencies(ctypes.byref(p), f, ctypes.byref(m)), "rope_table")
@@ -685,7 +686,11 @@ def rope_table(rotary_dim: int, positions: int, theta: float = 1.0e4, layout: in
         raise ValueError("layout must be HD_ROPE_HALVES or HD_ROPE_NEIGHBOURS, positions at least 1")
     shape = (positions, rotary_dim // 2, 2)
     if table is None:
-        table = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()))
+        # Memory that the current stream gave back may still be written there: a fill elsewhere takes its own stream's.
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            table = torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()))
     elif (tuple(table.shape) != shape or table.dtype != torch.float32 or not table.is_contiguous() or not table.is_cuda or
           table.device.index != torch.cuda.current_device()):
         raise ValueError(f"table must be contiguous float32 of shape {shape} on the current device")

@@ -102,3 +102,16 @@ def test_scales_without_a_reciprocal(hd, orc, name, scale):
     over = np.abs(got - t) - (np.maximum(2.0 ** -4 * (np.abs(t) + e), 2.0 ** -10) + e)
     assert np.isfinite(got).all() and (got[0] == 0).all()
     assert (over <= 0).all(), f"{over.max():.3e} over the bound"
+
+
+def test_a_table_filled_on_a_stream_of_its_own(hd):
+    """Its memory may have been something else's, which the current stream is still to write."""
+    shape, stream = (5000, 32, 2), torch.cuda.Stream()
+    want = hd.rope_table(64, 5000, theta=1e4).table.clone()
+    torch.cuda.synchronize()
+    for given in (stream, stream.cuda_stream):
+        torch.cuda._sleep(200_000_000)
+        torch.empty(shape, device="cuda").fill_(7.0)   # freed, and still to be filled
+        got = hd.rope_table(64, 5000, theta=1e4, stream=given).table
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
