@@ -104,6 +104,31 @@ def test_scales_without_a_reciprocal(hd, orc, name, scale):
     assert (over <= 0).all(), f"{over.max():.3e} over the bound"
 
 
+@pytest.mark.parametrize("spans", ["ragged", "single"])
+def test_e4m3_entries_read_back_after_a_normed_append(hd, orc, spans):
+    """The rows that come back are the stored codes times their scale, rounded once: for values the codes of the given rows,
+    for keys codes within a normed and rotated key's bound (check_append)."""
+    case = PagedCase(504, APPEND_SPANS[spans], kv="e4m3", page=32, appended=False, single=spans == "single")
+    ctx, d = context(hd, kv="e4m3"), case.device()
+    k, v = (synth.normal_bf16(case.rng, (case.rows, case.kv_heads, D), 3.0) for _ in range(2))
+    batch, cache = case.batch_of(hd, d), cache_of(hd, d)
+    hd.norm_rope_append_paged(ctx, 1, batch, None, k.cuda(), v.cuda(), None, cache, rope=table_of(hd, "halves 256 bands"))
+    rk, rv = torch.empty_like(k, device="cuda"), torch.empty_like(v, device="cuda")
+    hd.read_paged(ctx, batch, cache, rk, rv)
+    torch.cuda.synchronize()
+    assert hd.hybrid_decode_device_errors(ctx) == 0
+    _, vp, _, _ = reference_append(orc, case, FULL, None, k, v)
+    assert_bits_equal(rv, reference_read(orc, case, torch.from_numpy(vp), case.v_scale), "values")
+    assert_bits_equal(rk, reference_read(orc, case, d["k"].cpu(), case.k_scale), "keys")
+    cs, sn, amp = angles(hd, "halves 256 bands", [case.token(r)[1] for r in range(case.rows)])
+    z, e = reference(k, None, 0.0, cs, sn, amp, 0, 256)
+    sc = case.k_scale.double().numpy()[None, :, None]
+    t, e = np.clip(z / sc, -448, 448), e / sc + 2.0 ** -22 * np.abs(z / sc)
+    got = rk.double().cpu().numpy() / sc
+    over = np.abs(got - t) - (np.maximum(2.0 ** -4 * (np.abs(t) + e), 2.0 ** -10) + e + 2.0 ** -8 * np.abs(got))
+    assert (over <= 0).all(), f"{over.max():.3e} over the bound"
+
+
 def test_a_table_filled_on_a_stream_of_its_own(hd):
     """Its memory may have been something else's, which the current stream is still to write."""
     shape, stream = (5000, 32, 2), torch.cuda.Stream()
