@@ -84,9 +84,9 @@ bool encode_queries(CUtensorMap *map, const void *q, int num_q_heads, int num_to
 // Whether the decode kernel serves a call with more rows per kv head than its tiles hold sooner than the chunk kernel: it reads
 // a sequence's keys once per eight rows, the chunk kernel once per 256 rows, but with a longer start and drain.  Estimates in
 // microseconds, fitted to calls of 1 to 256 sequences with 12 to 160 rows each behind 0 to 30000 keys; they pick the slower
-// kernel by more than 8 % in 3 of 140.  Measured decode and chunk: 2 to 7 tokens of 16 sequences in 512-key windows 15.7 and
-// 24.4 us; 16 tokens of one sequence at 8000 27.8 and 42.4; 7 tokens of 16 sequences at 8000 158 and 74; 3 tokens of 64
-// at 8000 over E4M3 pages 170 and 342.
+// kernel by more than 8 % in 3 of 140, given exact bounds (a max_context of 0 is taken for the whole capacity).  Measured
+// decode and chunk: 2 to 7 tokens of 16 sequences in 512-key windows 15.7 and 24.4 us; 16 tokens of one sequence at 8000 27.8
+// and 42.4; 7 tokens of 16 sequences at 8000 158 and 74; 3 tokens of 64 at 8000 over E4M3 pages 170 and 342.
 constexpr int kDecodeRowsMost = 160;
 bool decode_is_sooner(const hd_ctx *ctx, const PagedSeqs &s, int window) {
     const int64_t rows = (int64_t)s.max_tokens * ctx->group;

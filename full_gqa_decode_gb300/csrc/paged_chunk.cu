@@ -45,12 +45,15 @@
 // loops over 16 scores, read from tensor memory and written back there as
 // weights; the instructions of a rule unrolled over 64 scores were waited for
 // longer than executed.  Where a bound on a tile's raw scores shows that a row's
-// reference stays, its maximum is not looked for.  Measured: 4096 tokens behind
-// 28672 with scores capped at 50 690 us (1.49 PFLOP/s; 1093 unrolled, with a
-// reciprocal a score and rescaled at 8), uncapped 675, with a bias by distance
-// 685; over E4M3 pages 1043, 861 and 990; documents of some 60 to 2500 tokens
-// packed into 16384 130 us (an item is about 7 tiles and, of a fifth of its time,
-// set-up and drain); prefix prompts at group 8 over E4M3 pages 319 us.
+// reference stays, its maximum is not looked for.  Measured, in bursts of 20 calls
+// (long runs meet the power limit and take 5 % more): 4096 tokens behind 28672 with
+// scores capped at 50 692 us (1.49 PFLOP/s; 1093 unrolled, with a reciprocal a score
+// and rescaled at 8), uncapped 680, with a bias by distance 687, with both 725 (the
+// bound takes a part's largest score at its smallest distance, and is passed more
+// often); over E4M3 pages 1045, 960, 984 and 991; documents of some 60 to 2500 tokens
+// packed into 16384 132 us (an item is about 7 tiles and, of a fifth of its time,
+// set-up and drain), in 512-key windows 96, over E4M3 pages 195; prefix prompts at
+// group 8 over E4M3 pages 322 us.
 #include <climits>
 
 #include "paged_rows.cuh"

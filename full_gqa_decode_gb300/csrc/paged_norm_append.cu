@@ -11,10 +11,11 @@
 // another's sums; keys and values go by runs -- the new tokens of one page and
 // kv head, one CTA, which owns the page's bounds -- two rows a warp at a time.
 // Bound by the latency of its chains of loads (offsets, context, angles): four
-// CTAs an SM at 64 registers beat both fewer and larger warps.  Measured: a packed
-// prompt of 16384 tokens 38.1 us (5.7 TB/s, 86 % of a copy's rate; at 80 registers
-// 42.7, eight heads a warp 39.5, five CTAs 44), 9026 tokens at 16 heads over E4M3
-// pages 36.3 us (5.1 TB/s), one token of 64 sequences 2.9 us from a graph.
+// CTAs an SM at 64 registers, some 50 bytes a thread spilled, beat both fewer and
+// larger warps.  Measured: a packed prompt of 16384 tokens 38.2 us (5.7 TB/s, 86 % of a
+// copy's rate; at 80 registers 42.7, eight heads a warp 39.5, five CTAs 44), 9026 tokens
+// at 16 heads over E4M3 pages 36.8 us (5.0 TB/s), one token of 64 sequences 2.9 us from
+// a graph.
 #include <climits>
 
 #include "paged_entry.cuh"

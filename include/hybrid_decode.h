@@ -436,7 +436,8 @@ hd_status decode_attn_full_static_scratch_plan(int32_t batch, int32_t num_q_head
  * and over selected blocks, to 2^-8 in calls with more; over E4M3 pages to 2^-11.
  * Sums and maxima are fp32.
  *
- * Entries at visible positions must be finite; slots no query may see (behind
+ * Entries at visible positions must be finite, and attn_paged's scores q . k / 16
+ * below 2^22 in magnitude; slots no query may see (behind
  * a sequence's end, before its window) can hold anything, NaN included.  A
  * non-finite entry among the positions of a chunk can reach every row of that
  * chunk.
@@ -486,7 +487,9 @@ typedef struct {
  * context[b] (0: the configuration's).  Whatever the bounds, a sequence is
  * served when its last new token's position is at most the configuration's
  * max_context; they pick kernels and grid sizes, and results agree within the
- * stated tolerances whatever they are. */
+ * stated tolerances whatever they are.  Bounds near the truth are faster: a
+ * max_context of 0 is taken for the configuration's, and so is a prompt from its
+ * start, for which 1 is the bound that says so. */
 typedef struct {
     const int32_t *block_table;
     const int32_t *context;
@@ -661,7 +664,7 @@ hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batc
  *   softcap    x becomes softcap * tanh(x / softcap), to an absolute error of
  *              2^-20 softcap; 0: no cap.  1/1024 to 1024, HD_ERR_UNSUPPORTED beyond
  *   slopes     then slopes[h] * |p - j| is taken off for query head h: device fp32
- *              [num_q_heads], finite, or NULL
+ *              [num_q_heads], or NULL; a bias counts with fp32's rounding of it
  *   first,     the visible positions of row r, first[r] .. last[r]: device
  *   last       [num_tokens] each, or NULL (0; p).  A sliding layer's window starts
  *              them at p - window + 1 at the earliest; they end with the
@@ -673,10 +676,13 @@ hd_status norm_rope_append_paged(hd_ctx *ctx, int32_t layer, const hd_paged_batc
  *              (HD_DEVERR_SPAN) and gets NaN, or is served by its own values.
  *   scale      0: 1 / sqrt(head_dim); else 2^-32 to 2^32, HD_ERR_UNSUPPORTED beyond
  * HD_ERR_INVALID_ARG when scale or softcap is negative or not finite.  Entries from
- * a sequence's lowest to its highest visible position must be finite, values below
- * 2^77.  Weights are
+ * a sequence's lowest to its highest visible position must be finite and in pages
+ * of the pool, values below 2^77; scale times any product of a query's and a key's
+ * dim, and any bias, stay below 2^100 (scores and biases of 2^23 and more, where fp32
+ * has no fractions left, leave little but the largest).  Weights are
  * rounded before they meet the values as in attn_paged, by the kernel that serves
- * the call: calls of few rows take the one that an estimate says is sooner. */
+ * the call: calls of few rows (up to 160 a kv head and sequence) take the one that an
+ * estimate says is sooner, from the batch's bounds on tokens, context and blocks. */
 typedef struct {
     float scale;
     float softcap;
